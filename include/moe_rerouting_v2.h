@@ -309,6 +309,130 @@ const char* mrr_status_string(mrr_status status);
  * ship with and refuse a library built from others.) */
 const char* mrr_source_hash(void);
 
+/* ------------------------------------------------------------------------
+ * The experts' operators: what makes the 4-bit rows that the re-routing
+ * moves, and what multiplies them with the experts. The conventions at the top
+ * of this file hold for them too: device pointers, dense rows, host-detectable
+ * errors before anything is launched, asynchronous on `stream`, no allocation.
+ *
+ * The microscaled 4-bit format (OCP MX v1.0: elements e2m1, scales e8m0), laid
+ * out as the re-routing operator takes it: a row of H values (H even) is H/2
+ * bytes, two values a byte, the first in the low nibble, and 2 * ceil(H/64)
+ * scale bytes; 32 values share the scale 2^(s - 127). Scale bytes past
+ * ceil(H/32) (an odd number of blocks) are 0. A scale byte of 255 is a NaN and
+ * so is every value under it.
+ * ------------------------------------------------------------------------ */
+
+/* One conversion between wide rows and microscaled 4-bit rows. */
+typedef struct mrr_mx_args {
+  void* wide;                      /* [rows, H] F16, BF16 or F32 */
+  int32_t wide_dtype;
+  int64_t rows;                    /* >= 0 */
+  int64_t H;                       /* even, 0 < H < 2^24 */
+  void* packed;                    /* [rows, H/2] bytes */
+  void* scales;                    /* [rows, ceil(H/64), 2] e8m0 bytes */
+} mrr_mx_args;
+
+/*
+ * wide -> packed, scales. Of each block of 32 values (the last one of a row
+ * may be shorter) s = floor(log2(max |x|)) - 2 + 127, clamped to [0, 254], and
+ * each value is x / 2^(s - 127) rounded to the nearest e2m1 value, ties to the
+ * even code, beyond 6 to 6; signs are kept, of zeros too. A block of zeros has
+ * s = 0; one that holds a NaN or an infinity has s = 255.
+ */
+mrr_status mrr_mx_quantize(const mrr_mx_args* args, struct ihipStream_t* stream);
+
+/* packed, scales -> wide: the values, rounded once to wide's type. */
+mrr_status mrr_mx_dequantize(const mrr_mx_args* args, struct ihipStream_t* stream);
+
+/*
+ * The experts' product over expert-major rows, as the re-routing leaves them:
+ *     out[r, n] = row_weight[r] * sum over k of tokens[r, k] * weight[e(r), n, k]
+ * where e(r) is the expert of row r by expert_token_num. With gated = 1 the
+ * first N/2 rows of an expert's weight are its gate and the others its up
+ * projection: out[r, n] = row_weight[r] * silu(g[r, n]) * u[r, n], n < N/2,
+ * with silu(g) = g / (1 + exp(-g)). Sums are kept in 32 bits and the result
+ * is rounded once.
+ */
+typedef struct mrr_grouped_mm_args {
+  const void* tokens;              /* [A, K] microscaled 4-bit rows, 16-byte aligned */
+  const void* token_scales;        /* [A, ceil(K/64), 2] */
+  int64_t A;                       /* 0 <= A <= INT32_MAX */
+  int64_t K;                       /* a multiple of 32, 0 < K < 2^20 */
+  const void* weight;              /* [E, N, K] microscaled 4-bit rows, 16-byte aligned */
+  const void* weight_scales;       /* [E, N, ceil(K/64), 2] */
+  int64_t E;                       /* 0 <= E <= 4096; E == 0 requires A == 0 */
+  int64_t N;                       /* 0 < N < 2^20; even with gated */
+  const void* expert_token_num;    /* [E]: rows of each expert (type 1), or their running sum
+                                      (type 0), as the re-routing writes it; checked on the device */
+  int32_t counts_dtype;            /* MRR_I32 or MRR_I64 */
+  int64_t expert_token_num_type;   /* 1 or 0 */
+  int64_t gated;                   /* 0 or 1 */
+  const float* row_weight;         /* [A], optional (NULL = 1) */
+  void* out;                       /* [A, gated ? N/2 : N] */
+  int32_t out_dtype;               /* F16, BF16 or F32 */
+} mrr_grouped_mm_args;
+
+/* The checks mrr_mx_grouped_mm() makes on the host; no HIP call. */
+mrr_status mrr_grouped_mm_validate(const mrr_grouped_mm_args* args, const void* workspace, size_t workspace_bytes);
+
+/*
+ * Runs it on `stream`. Counts that are negative or do not sum to A are found
+ * on the device, and then nothing is written to out. The workspace is
+ * optional: with MRR_GROUPED_MM_WORKSPACE_BYTES (16-byte aligned) the verdict on
+ * the counts is left there for mrr_get_device_status(); NULL and 0 otherwise.
+ */
+#define MRR_GROUPED_MM_WORKSPACE_BYTES ((size_t)256)
+mrr_status mrr_mx_grouped_mm(const mrr_grouped_mm_args* args, void* workspace, size_t workspace_bytes,
+                             struct ihipStream_t* stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens:
+ *     y[t] = sum over the chosen experts e of p[t, e] * Wd[e] (silu(Wg[e] x[t]) * (Wu[e] x[t]))
+ * Routing comes in one of two forms:
+ *   - router_logits [T, E]: the top_k largest of each row, ties to the lowest
+ *     expert; p is the row's softmax, over all E logits, or with renormalize
+ *     over the chosen ones. An expert whose logit is -inf is never chosen, so a
+ *     row of nothing else gives y = 0; a NaN or +inf in a row gives NaN.
+ *   - expert_ids and expert_weight [T, top_k]: p as given. An id outside
+ *     [0, E) chooses nothing (an expert of another rank); an expert that a
+ *     token names twice counts with the sum of the two weights.
+ * p silu(g) u is rounded once to x's type between the two products; sums are
+ * kept in 32 bits.
+ */
+typedef struct mrr_few_tokens_args {
+  const void* x;                   /* [T, H], 16-byte aligned */
+  int32_t dtype;                   /* x and y: F16 or BF16 (BF16 with 4-bit weights) */
+  int64_t T;                       /* 0 <= T <= MRR_FEW_TOKENS_MAX */
+  int64_t H;                       /* a multiple of 32, 0 < H <= 65536 */
+  int64_t E;                       /* 0 < E <= 1024 */
+  int64_t I;                       /* a multiple of 32, 0 < I <= 65536 */
+  int64_t top_k;                   /* 1 <= top_k <= min(E, 16) */
+  const float* router_logits;      /* [T, E], or NULL */
+  int64_t renormalize;             /* 0 or 1, with router_logits */
+  const int32_t* expert_ids;       /* [T, top_k], or NULL */
+  const float* expert_weight;      /* [T, top_k], with expert_ids */
+  int32_t weights_dtype;           /* dtype, or F4_E2M1: microscaled 4-bit rows */
+  const void* gate_up;             /* [E, 2 I, H]: the gate's I rows, then up's; 16-byte aligned */
+  const void* gate_up_scales;      /* [E, 2 I, ceil(H/64), 2] with 4-bit weights, else NULL */
+  const void* down;                /* [E, H, I], 16-byte aligned */
+  const void* down_scales;         /* [E, H, ceil(I/64), 2] with 4-bit weights, else NULL */
+  void* y;                         /* [T, H] */
+} mrr_few_tokens_args;
+
+#define MRR_FEW_TOKENS_MAX 128
+
+/* Bytes of workspace (16-byte aligned) that T tokens with top_k experts each
+ * of I intermediate values need; 0 for sizes outside the contract. */
+size_t mrr_few_tokens_workspace_size(int64_t T, int64_t top_k, int64_t I);
+
+/* The checks mrr_few_tokens() makes on the host; no HIP call. */
+mrr_status mrr_few_tokens_validate(const mrr_few_tokens_args* args, const void* workspace, size_t workspace_bytes);
+
+/* Runs it on `stream`: two kernels. */
+mrr_status mrr_few_tokens(const mrr_few_tokens_args* args, void* workspace, size_t workspace_bytes,
+                          struct ihipStream_t* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -31,7 +31,9 @@ F16, BF16, I8, F8_E5M2, F8_E4M3FN, HIF8, F4_E2M1, F4_E1M2, I32, I64, F32, F8_E8M
 
 EXPORTS = ("mrr_workspace_size", "mrr_validate", "mrr_describe_plan", "moe_rerouting_v2",
            "moe_rerouting_v2_offsets", "moe_rerouting_v2_gather", "mrr_get_device_status", "mrr_status_string",
-           "mrr_source_hash", "moe_rerouting_v2_noalloc")
+           "mrr_source_hash", "moe_rerouting_v2_noalloc", "mrr_mx_quantize", "mrr_mx_dequantize",
+           "mrr_grouped_mm_validate", "mrr_mx_grouped_mm", "mrr_few_tokens_workspace_size",
+           "mrr_few_tokens_validate", "mrr_few_tokens")
 NOALLOC_SCRATCH_BYTES = 8 << 20  # MRR_NOALLOC_SCRATCH_BYTES
 
 
@@ -83,6 +85,65 @@ class MrrPlanInfo(ctypes.Structure):
     ]
 
 
+class MrrMxArgs(ctypes.Structure):
+    """struct mrr_mx_args, field for field."""
+
+    _fields_ = [
+        ("wide", ctypes.c_void_p),
+        ("wide_dtype", ctypes.c_int32),
+        ("rows", ctypes.c_int64),
+        ("H", ctypes.c_int64),
+        ("packed", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+    ]
+
+
+class MrrGroupedMmArgs(ctypes.Structure):
+    """struct mrr_grouped_mm_args, field for field."""
+
+    _fields_ = [
+        ("tokens", ctypes.c_void_p),
+        ("token_scales", ctypes.c_void_p),
+        ("A", ctypes.c_int64),
+        ("K", ctypes.c_int64),
+        ("weight", ctypes.c_void_p),
+        ("weight_scales", ctypes.c_void_p),
+        ("E", ctypes.c_int64),
+        ("N", ctypes.c_int64),
+        ("expert_token_num", ctypes.c_void_p),
+        ("counts_dtype", ctypes.c_int32),
+        ("expert_token_num_type", ctypes.c_int64),
+        ("gated", ctypes.c_int64),
+        ("row_weight", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("out_dtype", ctypes.c_int32),
+    ]
+
+
+class MrrFewTokensArgs(ctypes.Structure):
+    """struct mrr_few_tokens_args, field for field."""
+
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("T", ctypes.c_int64),
+        ("H", ctypes.c_int64),
+        ("E", ctypes.c_int64),
+        ("I", ctypes.c_int64),
+        ("top_k", ctypes.c_int64),
+        ("router_logits", ctypes.c_void_p),
+        ("renormalize", ctypes.c_int64),
+        ("expert_ids", ctypes.c_void_p),
+        ("expert_weight", ctypes.c_void_p),
+        ("weights_dtype", ctypes.c_int32),
+        ("gate_up", ctypes.c_void_p),
+        ("gate_up_scales", ctypes.c_void_p),
+        ("down", ctypes.c_void_p),
+        ("down_scales", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -91,6 +152,8 @@ def load() -> ctypes.CDLL:
     """The loaded library; raises RuntimeError if it has not been built, or was
     built from sources other than the ones beside it (mrr_source_hash)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -125,6 +188,20 @@ def load() -> ctypes.CDLL:
             lib.moe_rerouting_v2_noalloc.restype = ctypes.c_int
             lib.mrr_get_device_status.argtypes = [vp, vp]
             lib.mrr_get_device_status.restype = ctypes.c_int
+            for name in ("mrr_mx_quantize", "mrr_mx_dequantize"):
+                fn = getattr(lib, name)
+                fn.argtypes = [ctypes.POINTER(MrrMxArgs), vp]
+                fn.restype = ctypes.c_int
+            for name, struct in (("grouped_mm", MrrGroupedMmArgs), ("few_tokens", MrrFewTokensArgs)):
+                check = getattr(lib, f"mrr_{name}_validate")
+                check.argtypes = [ctypes.POINTER(struct), vp, sz]
+                check.restype = ctypes.c_int
+            lib.mrr_mx_grouped_mm.argtypes = [ctypes.POINTER(MrrGroupedMmArgs), vp, sz, vp]
+            lib.mrr_mx_grouped_mm.restype = ctypes.c_int
+            lib.mrr_few_tokens.argtypes = [ctypes.POINTER(MrrFewTokensArgs), vp, sz, vp]
+            lib.mrr_few_tokens.restype = ctypes.c_int
+            lib.mrr_few_tokens_workspace_size.argtypes = [ctypes.c_int64] * 3
+            lib.mrr_few_tokens_workspace_size.restype = sz
             lib.mrr_status_string.argtypes = [ctypes.c_int]
             lib.mrr_status_string.restype = ctypes.c_char_p
             _lib = lib

@@ -1,9 +1,10 @@
 """Builds the HIP library libmoe_rerouting_v2.so in-tree, for gfx950.
 
-The host checks (mrr_validate.cpp) are compiled by g++ with no HIP header; the
-kernel files (mrr_offsets.hip, mrr_gather.hip, mrr_fused.hip,
-mrr_one_launch.hip) and the entry points (mrr_entry.hip) by hipcc, in
-parallel. Packed-fp32 instructions are
+The host checks (mrr_validate.cpp, mrr_experts_validate.cpp) are compiled by
+g++ with no HIP header; the kernel files (mrr_offsets.hip, mrr_gather.hip,
+mrr_fused.hip, mrr_one_launch.hip; mrr_mx_quant.hip, mrr_grouped_mm.hip,
+mrr_few_tokens.hip, with their own entry points) and the re-routing's entry
+points (mrr_entry.hip) by hipcc, in parallel. Packed-fp32 instructions are
 disabled for all device code.
 """
 from __future__ import annotations
@@ -55,17 +56,20 @@ def _run(cmd, verbose):
     subprocess.run(cmd, check=True)
 
 
-HIP_SOURCES = ("mrr_offsets.hip", "mrr_gather.hip", "mrr_fused.hip", "mrr_one_launch.hip", "mrr_entry.hip")
+HIP_SOURCES = ("mrr_offsets.hip", "mrr_gather.hip", "mrr_fused.hip", "mrr_one_launch.hip", "mrr_entry.hip",
+               "mrr_mx_quant.hip", "mrr_grouped_mm.hip", "mrr_few_tokens.hip")
+HOST_SOURCES = ("mrr_validate.cpp", "mrr_experts_validate.cpp")
 
 
 def build_library(verbose: bool = False) -> str:
     """Compile and link the library; returns its path. Always recompiles."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    v_obj = os.path.join(BUILD_DIR, "mrr_validate.o")
-    cmds = [["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-Werror", "-I", INCLUDE,
-             f'-DMRR_SOURCE_HASH="{source_hash()}"',
-             "-c", os.path.join(CSRC, "mrr_validate.cpp"), "-o", v_obj]]
-    objs = [v_obj]
+    cmds, objs = [], []
+    for src in HOST_SOURCES:
+        obj = os.path.join(BUILD_DIR, src.replace(".cpp", ".o"))
+        cmds.append(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-Werror", "-I", INCLUDE,
+                     f'-DMRR_SOURCE_HASH="{source_hash()}"', "-c", os.path.join(CSRC, src), "-o", obj])
+        objs.append(obj)
     for src in HIP_SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".hip", ".o"))
         cmds.append([HIPCC, *HIP_FLAGS, "-I", INCLUDE, "-c", os.path.join(CSRC, src), "-o", obj])

@@ -1,0 +1,295 @@
+// mrr_mx_quant.hip -- conversion between wide rows (fp16, bf16, fp32) and
+// microscaled 4-bit rows (OCP MX v1.0: e2m1 values, e8m0 scales), in the layout
+// the re-routing operator moves: [rows, H/2] bytes and [rows, ceil(H/64), 2]
+// scales.
+//
+// Per block of 32 values: s = max(exponent field of max |x| - 2, 0), so that
+// 2^(s - 127) = 2^(floor(log2 max |x|) - 2), and q = round(x / 2^(s - 127)) to
+// e2m1. Bound by memory: a value costs its 2 or 4 bytes and 17/32 byte. A lane
+// takes 8 values (16 bytes of fp16 or bf16), the 4 lanes of a quad share a
+// block and find its maximum by two DPP steps, and the conversions are the
+// chip's scaled ones (division by the scale, round to nearest even, saturating).
+#include "mrr_device.h"
+#include "mrr_experts.h"
+
+namespace mrr {
+namespace {
+
+using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
+using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
+using f32x2 = float __attribute__((ext_vector_type(2)));
+
+constexpr int kUnit = 8;  // values of a lane
+constexpr int kThreads = 256;
+
+// The scale as the conversions take it: 2^(s - 127). They read the exponent
+// alone; 2^-127 is the subnormal with its top mantissa bit set.
+__device__ __forceinline__ float scale_float(uint32_t s) {
+  return __uint_as_float(s == 0 ? 0x00400000u : s << 23);
+}
+
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E;  // quad_perm [1,0,3,2] and [2,3,0,1]
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), kSwap1, 0xf, 0xf, false)));
+  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), kSwap2, 0xf, 0xf, false)));
+}
+
+// Eight values of one type: loading, the largest |x| as fp32 bits (so that
+// infinities and NaN compare above every finite value), and both conversions.
+template <int kDtype>
+struct Eight;
+
+template <>
+struct Eight<MRR_BF16> {
+  uint32_t w[4];
+  static constexpr int kBytes = 2;
+  __device__ void set(int i, const uint8_t* p) {
+    uint16_t v;
+    __builtin_memcpy(&v, p, 2);
+    w[i / 2] |= static_cast<uint32_t>(v) << (i % 2 * 16);
+  }
+  __device__ uint32_t top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max((w[i] << 16) & 0x7fffffffu, w[i] & 0x7fff0000u));
+    return m;
+  }
+  __device__ uint32_t pack(float s) const {
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, w[0]), s, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, w[1]), s, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, w[2]), s, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(r, __builtin_bit_cast(bf16x2, w[3]), s, 3);
+  }
+  __device__ void unpack(uint32_t c, float s) {
+    w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 0));
+    w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 1));
+    w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 2));
+    w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s, 3));
+  }
+  __device__ void get(int i, uint8_t* p) const {
+    const uint16_t v = static_cast<uint16_t>(w[i / 2] >> (i % 2 * 16));
+    __builtin_memcpy(p, &v, 2);
+  }
+};
+
+template <>
+struct Eight<MRR_F16> : Eight<MRR_BF16> {
+  __device__ uint32_t top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f16x2 h = __builtin_bit_cast(f16x2, w[i]);
+      m = max(m, max(__float_as_uint(static_cast<float>(h[0])) & 0x7fffffffu,
+                     __float_as_uint(static_cast<float>(h[1])) & 0x7fffffffu));
+    }
+    return m;
+  }
+  __device__ uint32_t pack(float s) const {
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(f16x2, w[0]), s, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(f16x2, w[1]), s, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(f16x2, w[2]), s, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(r, __builtin_bit_cast(f16x2, w[3]), s, 3);
+  }
+  __device__ void unpack(uint32_t c, float s) {
+    w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 0));
+    w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 1));
+    w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 2));
+    w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(c, s, 3));
+  }
+};
+
+template <>
+struct Eight<MRR_F32> {
+  float w[8];
+  static constexpr int kBytes = 4;
+  __device__ void set(int i, const uint8_t* p) { __builtin_memcpy(&w[i], p, 4); }
+  __device__ uint32_t top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(w[i]) & 0x7fffffffu);
+    return m;
+  }
+  __device__ uint32_t pack(float s) const {
+    uint32_t r = 0;
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, w[0], w[1], s, 0);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, w[2], w[3], s, 1);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, w[4], w[5], s, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, w[6], w[7], s, 3);
+  }
+  __device__ void unpack(uint32_t c, float s) {
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
+    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2);
+    const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
+    w[0] = a[0], w[1] = a[1], w[2] = b[0], w[3] = b[1], w[4] = d[0], w[5] = d[1], w[6] = e[0], w[7] = e[1];
+  }
+  __device__ void get(int i, uint8_t* p) const { __builtin_memcpy(p, &w[i], 4); }
+};
+
+struct MxArgs {
+  uint8_t* wide;
+  uint8_t* packed;
+  uint8_t* scales;
+  uint32_t units;          // of this launch, padding included
+  uint32_t units_per_row;  // 4 per scale byte; unused when kFlat
+  uint32_t H;              // unused when kFlat
+};
+
+// Where a unit lies. kFlat: H is a multiple of 64, so rows follow each other
+// without padding and no row number is needed.
+struct Place {
+  uint64_t wide, packed, scale;  // element, byte and byte offsets
+  int count;                     // values of the unit that exist: 8, or fewer at a row's end
+};
+
+template <bool kFlat>
+__device__ __forceinline__ Place place_of(const MxArgs& a, uint32_t u) {
+  Place p;
+  p.scale = u / 4;
+  if constexpr (kFlat) {
+    p.wide = static_cast<uint64_t>(u) * kUnit;
+    p.packed = static_cast<uint64_t>(u) * (kUnit / 2);
+    p.count = kUnit;
+  } else {
+    const uint32_t row = u / a.units_per_row;
+    const uint32_t col = (u - row * a.units_per_row) * kUnit;
+    p.count = col >= a.H ? 0 : min(a.H - col, static_cast<uint32_t>(kUnit));
+    p.wide = static_cast<uint64_t>(row) * a.H + col;
+    p.packed = p.wide / 2;
+  }
+  return p;
+}
+
+template <int kDtype, bool kFlat, int kIter>
+__global__ __launch_bounds__(kThreads) void mx_quantize_kernel(MxArgs a) {
+  using V = Eight<kDtype>;
+  const uint32_t u0 = blockIdx.x * static_cast<uint32_t>(kThreads * kIter) + threadIdx.x;
+  V v[kIter];
+  Place p[kIter];
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const uint32_t u = u0 + i * kThreads;
+    v[i] = V{};
+    p[i] = place_of<kFlat>(a, u);
+    if (u >= a.units) p[i].count = 0;
+    const uint8_t* src = a.wide + p[i].wide * V::kBytes;
+    if (p[i].count == kUnit) {
+      __builtin_memcpy(&v[i].w, src, sizeof(v[i].w));
+    } else {
+      for (int k = 0; k < kUnit; ++k)
+        if (k < p[i].count) v[i].set(k, src + k * V::kBytes);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    // units come in whole quads, so the lanes of a quad are in range together
+    const uint32_t e = quad_max(v[i].top()) >> 23;
+    const uint32_t s = e == 255 ? 255 : e > 2 ? e - 2 : 0;
+    const uint32_t c = s == 255 ? 0 : v[i].pack(scale_float(s));
+    uint8_t* dst = a.packed + p[i].packed;
+    if (p[i].count == kUnit) {
+      __builtin_memcpy(dst, &c, 4);
+    } else {
+      for (int k = 0; k < kUnit / 2; ++k)
+        if (2 * k < p[i].count) dst[k] = static_cast<uint8_t>(c >> (8 * k));
+    }
+    if (threadIdx.x % 4 == 0 && u0 + i * kThreads < a.units) a.scales[p[i].scale] = static_cast<uint8_t>(s);
+  }
+}
+
+template <int kDtype, bool kFlat, int kIter>
+__global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxArgs a) {
+  using V = Eight<kDtype>;
+  const uint32_t u0 = blockIdx.x * static_cast<uint32_t>(kThreads * kIter) + threadIdx.x;
+  uint32_t c[kIter];
+  uint32_t s[kIter];
+  Place p[kIter];
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    const uint32_t u = u0 + i * kThreads;
+    p[i] = place_of<kFlat>(a, u);
+    if (u >= a.units) p[i].count = 0;
+    c[i] = s[i] = 0;
+    const uint8_t* src = a.packed + p[i].packed;
+    if (p[i].count == kUnit) {
+      __builtin_memcpy(&c[i], src, 4);
+    } else {
+      for (int k = 0; k < kUnit / 2; ++k)
+        if (2 * k < p[i].count) c[i] |= static_cast<uint32_t>(src[k]) << (8 * k);
+    }
+    if (p[i].count > 0) s[i] = a.scales[p[i].scale];
+  }
+#pragma unroll
+  for (int i = 0; i < kIter; ++i) {
+    V v;
+    v.unpack(c[i], scale_float(s[i]));  // s = 255: the scale is an infinity, every value a NaN
+    uint8_t* dst = a.wide + p[i].wide * V::kBytes;
+    if (p[i].count == kUnit) {
+      __builtin_memcpy(dst, &v.w, sizeof(v.w));
+    } else {
+      for (int k = 0; k < kUnit; ++k)
+        if (k < p[i].count) v.get(k, dst + k * V::kBytes);
+    }
+  }
+}
+
+// Units are numbered in 32 bits, so more rows than this take several launches.
+constexpr int64_t kMaxUnits = int64_t(1) << 30;
+// From this many units on a lane takes four of them.
+constexpr int64_t kManyUnits = int64_t(kThreads) * 2048;
+
+template <int kDtype, bool kFlat>
+void launch_mx(const MxArgs& a, bool quantize, hipStream_t stream) {
+  if (a.units >= kManyUnits) {
+    const dim3 grid((a.units + kThreads * 4 - 1) / (kThreads * 4));
+    if (quantize)
+      mx_quantize_kernel<kDtype, kFlat, 4><<<grid, kThreads, 0, stream>>>(a);
+    else
+      mx_dequantize_kernel<kDtype, kFlat, 4><<<grid, kThreads, 0, stream>>>(a);
+  } else {
+    const dim3 grid((a.units + kThreads - 1) / kThreads);
+    if (quantize)
+      mx_quantize_kernel<kDtype, kFlat, 1><<<grid, kThreads, 0, stream>>>(a);
+    else
+      mx_dequantize_kernel<kDtype, kFlat, 1><<<grid, kThreads, 0, stream>>>(a);
+  }
+}
+
+mrr_status run_mx(const mrr_mx_args* args, bool quantize, hipStream_t stream) {
+  const mrr_status st = check_mx(args, quantize);
+  if (st != MRR_SUCCESS || args->rows == 0) return st;
+  const int64_t w = args->wide_dtype == MRR_F32 ? 4 : 2;
+  const int64_t per_row = 4 * mx_scale_bytes(args->H);
+  const bool flat = args->H % 64 == 0;
+  const int64_t step = kMaxUnits / per_row;  // rows of a launch
+  for (int64_t row = 0; row < args->rows; row += step) {
+    const int64_t rows = args->rows - row < step ? args->rows - row : step;
+    MxArgs a;
+    a.wide = static_cast<uint8_t*>(args->wide) + row * args->H * w;
+    a.packed = static_cast<uint8_t*>(args->packed) + row * (args->H / 2);
+    a.scales = static_cast<uint8_t*>(args->scales) + row * (per_row / 4);
+    a.units = static_cast<uint32_t>(rows * per_row);
+    a.units_per_row = static_cast<uint32_t>(per_row);
+    a.H = static_cast<uint32_t>(args->H);
+    switch (args->wide_dtype) {
+      case MRR_F16: flat ? launch_mx<MRR_F16, true>(a, quantize, stream) : launch_mx<MRR_F16, false>(a, quantize, stream); break;
+      case MRR_BF16: flat ? launch_mx<MRR_BF16, true>(a, quantize, stream) : launch_mx<MRR_BF16, false>(a, quantize, stream); break;
+      default: flat ? launch_mx<MRR_F32, true>(a, quantize, stream) : launch_mx<MRR_F32, false>(a, quantize, stream); break;
+    }
+    if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
+  }
+  return MRR_SUCCESS;
+}
+
+}  // namespace
+}  // namespace mrr
+
+extern "C" mrr_status mrr_mx_quantize(const mrr_mx_args* args, struct ihipStream_t* stream) {
+  return mrr::run_mx(args, true, stream);
+}
+
+extern "C" mrr_status mrr_mx_dequantize(const mrr_mx_args* args, struct ihipStream_t* stream) {
+  return mrr::run_mx(args, false, stream);
+}
