@@ -19,8 +19,8 @@ using f32x16 = float __attribute__((ext_vector_type(16)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
 constexpr int kMxFp4 = 4;        // the matrix instruction's operand format e2m1
-constexpr int kTileBlocks = 8;   // blocks of a row in a K tile (256 values, 128 bytes)
-constexpr int kRowBytes = 128;   // of a row in a K tile
+constexpr int kTileBlocks = 4;   // blocks of a row in a K tile (128 values)
+constexpr int kRowBytes = 64;    // of a row in a K tile
 
 struct GroupedArgs {
   const uint8_t* x;
@@ -62,17 +62,14 @@ __device__ __forceinline__ int32_t count_of(const GroupedArgs& a, int e) {
 }
 
 // Finds the workgroup's tile; false when it has none or the counts are bad.
-// Every thread takes a run of experts; the runs' rows and tiles are scanned
-// over the workgroup. The exact sum of the counts is kept in two 16-bit halves
-// (4096 counts of at most 2^31).
-template <int kBM, int kWgThreads>
-__device__ bool find_tile(const GroupedArgs& a, Tile* t) {
-  constexpr int kWaves = kWgThreads / 64;
-  __shared__ uint32_t s_rows[kWaves], s_tiles[kWaves], s_low[kWaves], s_high[kWaves], s_bad[kWaves];
-  __shared__ Tile s_tile;
-  const int tid = threadIdx.x, wave = tid / 64;
-  const int per = (a.E + kWgThreads - 1) / kWgThreads;
-  const int e0 = tid * per, e1 = min(a.E, e0 + per);
+// Every wave does it for itself, without LDS or barriers: a lane takes a run of
+// experts, the runs' rows and tiles are scanned over the wave. The exact sum of
+// the counts is kept in two 16-bit halves (4096 counts of at most 2^31).
+template <int kBM>
+__device__ __forceinline__ bool find_tile(const GroupedArgs& a, Tile* t) {
+  const int lane = threadIdx.x % 64;
+  const int per = (a.E + 63) / 64;
+  const int e0 = lane * per, e1 = min(a.E, e0 + per);
   uint32_t rows = 0, tiles = 0, low = 0, high = 0, bad = 0;
   for (int e = e0; e < e1; ++e) {
     const int32_t c = count_of(a, e);
@@ -86,29 +83,11 @@ __device__ bool find_tile(const GroupedArgs& a, Tile* t) {
     high += static_cast<uint32_t>(c) >> 16;
   }
   const uint32_t rows_in = wave_scan_u32(rows), tiles_in = wave_scan_u32(tiles);
-  const uint32_t low_sum = wave_sum_u32(low), high_sum = wave_sum_u32(high);
-  const bool any_bad = __any(bad != 0);
-  if (tid % 64 == 63) {
-    s_rows[wave] = rows_in;
-    s_tiles[wave] = tiles_in;
-    s_low[wave] = low_sum;
-    s_high[wave] = high_sum;
-    s_bad[wave] = any_bad;
-  }
-  __syncthreads();
-  uint32_t row0 = rows_in - rows, tile0 = tiles_in - tiles, all_tiles = 0, is_bad = 0;
-  uint64_t total = 0;
-  for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) {
-      row0 += s_rows[w];
-      tile0 += s_tiles[w];
-    }
-    all_tiles += s_tiles[w];
-    total += s_low[w] + (static_cast<uint64_t>(s_high[w]) << 16);
-    is_bad |= s_bad[w];
-  }
-  const bool valid = is_bad == 0 && total == static_cast<uint64_t>(a.A);
-  if (a.hdr != nullptr && blockIdx.x == 0 && tid == 0) {
+  const uint64_t total = wave_sum_u32(low) + (static_cast<uint64_t>(wave_sum_u32(high)) << 16);
+  const bool is_bad = __any(bad != 0);
+  const uint32_t all_tiles = __builtin_amdgcn_readlane(tiles_in, 63);
+  const bool valid = !is_bad && total == static_cast<uint64_t>(a.A);
+  if (a.hdr != nullptr && blockIdx.x == 0 && threadIdx.x == 0) {
     a.hdr->status = valid ? kCountsValid : kTablesBad;
     a.hdr->flags = is_bad ? kFlagNegative : valid ? 0 : kFlagSumMismatch;
     a.hdr->inverse = 0;
@@ -125,43 +104,82 @@ __device__ bool find_tile(const GroupedArgs& a, Tile* t) {
   const uint32_t base = work / 8, extra = work % 8;
   const uint32_t id = xcd * base + min(xcd, extra) + at;
   const uint32_t m = id / a.n_tiles;
-  if (m >= tile0 && m < tile0 + tiles) {
-    uint32_t first = tile0, r = row0;
+  uint32_t first = tiles_in - tiles, r = rows_in - rows;
+  const uint64_t mine = __ballot(m >= first && m < first + tiles);
+  const int owner = __ffsll(static_cast<unsigned long long>(mine)) - 1;  // one lane's run holds tile m
+  int expert = e0;
+  uint32_t k = 0, exist = 0;
+  if (lane == owner)
     for (int e = e0; e < e1; ++e) {
       const uint32_t c = static_cast<uint32_t>(count_of(a, e)), n = (c + kBM - 1) / kBM;
       if (m < first + n) {
-        const uint32_t k = m - first;
-        s_tile.expert = e;
-        s_tile.row = static_cast<int>(r + k * kBM);
-        s_tile.rows = static_cast<int>(min(c - k * kBM, static_cast<uint32_t>(kBM)));
-        s_tile.n = static_cast<int>(id - m * a.n_tiles);
+        expert = e;
+        k = m - first;
+        exist = min(c - k * kBM, static_cast<uint32_t>(kBM));
+        r += k * kBM;
         break;
       }
       first += n;
       r += c;
     }
-  }
-  __syncthreads();
-  *t = s_tile;
+  t->expert = __builtin_amdgcn_readlane(expert, owner);
+  t->row = static_cast<int>(__builtin_amdgcn_readlane(r, owner));
+  t->rows = static_cast<int>(__builtin_amdgcn_readlane(exist, owner));
+  t->n = __builtin_amdgcn_readfirstlane(static_cast<int>(id - m * a.n_tiles));
   return true;
 }
 
-__device__ __forceinline__ void load_to_lds(const uint8_t* src, uint8_t* lds) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+// 16 bytes of every lane, at `base` + its offset, to LDS from byte `lds` on in
+// the order of the lanes. In assembly, as the compiler would wait for every
+// such load before it lets any LDS read pass; the kernel waits by itself.
+__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
+               : "memory");
 }
 
-// The four scale bytes of blocks b .. b + 3 of a row; 127 (a factor of one)
-// past its end.
+// The four scale bytes of blocks b .. b + 3 of a row of n; 127 (a factor of
+// one) past its end. b and n are the same for all lanes.
 __device__ __forceinline__ uint32_t load_scales(const uint8_t* row, int b, int n) {
-  uint32_t v = 0x7f7f7f7fu;
-  if (b + 4 <= n) {
-    __builtin_memcpy(&v, row + b, 4);
-  } else {
-    for (int i = 0; i < 4; ++i)
-      if (b + i < n) v = (v & ~(0xffu << (8 * i))) | static_cast<uint32_t>(row[b + i]) << (8 * i);
+  constexpr uint32_t kOnes = 0x7f7f7f7fu;
+  if (n >= 4) {  // the row's last four bytes hold what there is of them
+    const int at = min(b, n - 4), over = b - at;
+    uint32_t v;
+    __builtin_memcpy(&v, row + at, 4);
+    return over == 0 ? v : over >= 4 ? kOnes : v >> (8 * over) | kOnes << (32 - 8 * over);
+  }
+  uint32_t v = kOnes;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const uint32_t byte = row[min(b + i, n - 1)];
+    if (b + i < n) v = (v & ~(0xffu << (8 * i))) | byte << (8 * i);
   }
   return v;
+}
+
+// A pointer that is the same for all lanes, in scalar registers.
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t low = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t high = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(high) << 32 | low);
+}
+
+// Which bits of a row's number permute its chunks: with them, eight rows of 64
+// bytes fill 128 bytes of banks once, and sixteen rows 256 bytes.
+__device__ __forceinline__ int swizzle(int row) { return (row >> 1 & 2) | ((row >> 1 ^ row >> 3) & 1); }
+
+// Waits until at most kLeft of the wave's loads are on their way, or none.
+template <int kLeft>
+__device__ __forceinline__ void wait_loads(bool more) {
+  if (more)
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft) : "memory");
+  else
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// A barrier of LDS alone: loads from memory stay on their way.
+__device__ __forceinline__ void workgroup_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
@@ -179,25 +197,27 @@ __device__ __forceinline__ void store4(T* p, const float (&v)[4], int count) {
 }
 
 // kFN x kFM fragments of 32 weight rows x 32 token rows a wave, kWN x kWM
-// waves a workgroup. A K tile is 256 values: the halves of a wave take its
-// first and last four blocks, so that the four scales a lane needs for the
-// tile's four products are one dword. A row of the tile is 128 bytes of LDS,
-// its 16-byte chunks permuted by the row's number so that eight neighbouring
-// rows touch all banks; the tiles go from memory to LDS directly, the next one
-// while this one is multiplied.
-template <int kFM, int kFN, int kWM, int kWN, bool kGated>
-__global__ __launch_bounds__(64 * kWM * kWN) void grouped_mm_kernel(GroupedArgs a) {
+// waves a workgroup. A K tile is 128 values, 64 bytes of a row: the halves of a
+// wave take its first and last two blocks. The tiles go from memory to LDS
+// directly, kStages of them in turn: while one is multiplied, the next ones are
+// on their way. A row's 16-byte chunks are permuted by the row's number so that
+// eight or sixteen neighbouring rows touch all banks. The scales of four K tiles
+// (16 bytes of a row) go through registers, as their rows have any alignment.
+template <int kFM, int kFN, int kWM, int kWN, int kStages, bool kGated>
+__global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedArgs a) {
   constexpr int kWaves = kWM * kWN, kWgThreads = 64 * kWaves;
-  constexpr int kBM = 32 * kFM * kWM, kBN = 32 * kFN * kWN;
-  constexpr int kStage = (kBM + kBN) * kRowBytes;
-  constexpr int kXLoads = kBM / 8 / kWaves, kWLoads = kBN / 8 / kWaves;
-  static_assert(kXLoads * 8 * kWaves == kBM && kWLoads * 8 * kWaves == kBN, "whole loads");
-  __shared__ __align__(1024) uint8_t lds[2 * kStage];
+  constexpr int kBM = 32 * kFM * kWM, kBN = 32 * kFN * kWN, kRows = kBM + kBN;
+  constexpr int kStage = kRows * kRowBytes;
+  constexpr int kXLoads = kBM / 16 / kWaves, kWLoads = kBN / 16 / kWaves;
+  constexpr int kOwn = (kRows + kWgThreads - 1) / kWgThreads;  // rows whose scales a thread loads
+  static_assert(kXLoads * 16 * kWaves == kBM && kWLoads * 16 * kWaves == kBN, "whole loads");
+  __shared__ __align__(1024) uint8_t lds[kStages * kStage];
+  __shared__ uint32_t lds_scales[4 * kRows];  // [K tile of four][row]
 
   Tile t;
-  if (!find_tile<kBM, kWgThreads>(a, &t)) return;
+  if (!find_tile<kBM>(a, &t)) return;
 
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wm = wave % kWM, wn = wave / kWM;
   const int r32 = lane % 32, half = lane / 32;
   const int half_n = a.N / 2;                            // gated: the up projection's first row
@@ -206,52 +226,77 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_mm_kernel(GroupedArgs 
   const int64_t row_bytes = static_cast<int64_t>(a.blocks) * 16;
   const int64_t w_row0 = static_cast<int64_t>(t.expert) * a.N;
 
-  // The weight row in place j of the tile: within a wave's fragments, gated
-  // ones are the gate's and then the same columns of the up projection.
-  auto weight_row = [&](int j) {
-    int col, part = 0;
-    if constexpr (kGated) {
-      constexpr int kHalf = 32 * kFN / 2;
-      const int in_wave = j % (32 * kFN);
-      part = in_wave / kHalf;
-      col = n0 + j / (32 * kFN) * kHalf + in_wave % kHalf;
-    } else {
-      col = n0 + j;
-    }
-    return w_row0 + min(col, n_end - 1) + (part ? half_n : 0);
+  // The weight row in place j of the tile is column `col` of part `part`:
+  // gated, a wave's fragments are the gate's and then the same columns of the
+  // up projection.
+  constexpr int kHalf = 32 * kFN / 2;
+  auto part_of = [&](int j) { return kGated ? j % (32 * kFN) / kHalf : 0; };
+  auto col_of = [&](int j) {
+    const int col = n0 + (kGated ? j / (32 * kFN) * kHalf + j % kHalf : j);
+    return min(col, n_end - 1);
   };
 
-  // What this lane stages: chunk lane % 8 (permuted) of a row of every eight.
-  const uint8_t* src[kXLoads + kWLoads];
-  int chunk[1];
-  chunk[0] = (lane % 8) ^ (lane / 8);
+  // What this lane stages: of every 16 rows chunk lane % 4 (permuted) of one.
+  const int chunk = (lane % 4) ^ swizzle(lane / 4);
+  uint32_t offset[kXLoads + kWLoads];
+  const uint8_t* base[kXLoads + kWLoads];
 #pragma unroll
   for (int i = 0; i < kXLoads; ++i) {
-    const int j = (i * kWaves + wave) * 8 + lane / 8;
-    src[i] = a.x + static_cast<int64_t>(t.row + min(j, t.rows - 1)) * row_bytes;
+    const int j = (i * kWaves + wave) * 16 + lane / 4;
+    base[i] = uniform(a.x + t.row * row_bytes);
+    offset[i] = static_cast<uint32_t>(min(j, t.rows - 1) * row_bytes) + chunk * 16;
   }
 #pragma unroll
   for (int i = 0; i < kWLoads; ++i) {
-    const int j = (i * kWaves + wave) * 8 + lane / 8;
-    src[kXLoads + i] = a.w + weight_row(j) * row_bytes;
+    const int j0 = (i * kWaves + wave) * 16;
+    base[kXLoads + i] = uniform(a.w + (w_row0 + n0 + (part_of(j0) ? half_n : 0)) * row_bytes);
+    offset[kXLoads + i] = static_cast<uint32_t>((col_of(j0 + lane / 4) - n0) * row_bytes) + chunk * 16;
   }
-  auto stage = [&](int kt, int buf) {
-    uint8_t* base = lds + buf * kStage + wave * 1024;
-    const int b = min(kt * kTileBlocks + chunk[0], a.blocks - 1);  // past the row's end: any block of it
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
+      static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds)));
+  const int k_tiles = (a.blocks + kTileBlocks - 1) / kTileBlocks;
+  auto stage = [&](int kt) {
+    const uint32_t to = __builtin_amdgcn_readfirstlane(lds0 + kt % kStages * kStage + wave * 1024);
+    // past the row's end: its last block again, which does not count
+    const int left = a.blocks - kt * kTileBlocks;
+    const uint32_t back = chunk >= left ? (chunk - left + 1) * 16 : 0;
 #pragma unroll
-    for (int i = 0; i < kXLoads; ++i) load_to_lds(src[i] + b * 16, base + i * kWaves * 1024);
+    for (int i = 0; i < kXLoads; ++i) load_to_lds(base[i] + kt * kRowBytes, offset[i] - back, to + i * kWaves * 1024);
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
-      load_to_lds(src[kXLoads + i] + b * 16, base + kBM * kRowBytes + i * kWaves * 1024);
+      load_to_lds(base[kXLoads + i] + kt * kRowBytes, offset[kXLoads + i] - back,
+                  to + kBM * kRowBytes + i * kWaves * 1024);
   };
 
-  const uint8_t* xs[kFM];
-  const uint8_t* ws[kFN];
+  const uint8_t* s_row[kOwn];
 #pragma unroll
-  for (int i = 0; i < kFM; ++i)
-    xs[i] = a.x_scales + static_cast<int64_t>(t.row + min((wm * kFM + i) * 32 + r32, t.rows - 1)) * a.scale_bytes;
+  for (int i = 0; i < kOwn; ++i) {
+    const int j = threadIdx.x + i * kWgThreads, w = j - kBM;
+    s_row[i] = j < kBM ? a.x_scales + static_cast<int64_t>(t.row + min(j, t.rows - 1)) * a.scale_bytes
+                       : a.w_scales + (w_row0 + col_of(w) + (part_of(w) ? half_n : 0)) * a.scale_bytes;
+  }
+  u32x4 held[kOwn];
+  auto fetch_scales = [&](int kt) {  // kt a multiple of 4
+    const int b = kt * kTileBlocks;
 #pragma unroll
-  for (int i = 0; i < kFN; ++i) ws[i] = a.w_scales + weight_row((wn * kFN + i) * 32 + r32) * a.scale_bytes;
+    for (int i = 0; i < kOwn; ++i) {
+      if (b + 16 <= a.blocks) {
+        __builtin_memcpy(&held[i], s_row[i] + b, 16);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) held[i][c] = load_scales(s_row[i], b + 4 * c, a.blocks);
+      }
+    }
+  };
+  auto keep_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const int j = threadIdx.x + i * kWgThreads;
+      if (kRows % kWgThreads != 0 && j >= kRows) continue;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) lds_scales[c * kRows + j] = held[i][c];
+    }
+  };
 
   f32x16 acc[kFN][kFM];
 #pragma unroll
@@ -261,42 +306,24 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_mm_kernel(GroupedArgs 
 #pragma unroll
       for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.0f;
 
-  uint32_t sx[kFM], sw[kFN];
-  auto fetch_scales = [&](int kt) {
-    const int b = kt * kTileBlocks + half * 4;
+  const int at0 = r32 * kRowBytes + (((half * 2) ^ swizzle(r32)) * 16);
+  const bool works = wm * kFM * 32 < t.rows;  // a wave without rows only stages
+  auto multiply = [&](int kt) {
+    const uint8_t* xt = lds + kt % kStages * kStage + wm * kFM * 32 * kRowBytes;
+    const uint8_t* wt = lds + kt % kStages * kStage + (kBM + wn * kFN * 32) * kRowBytes;
+    const uint8_t* st = reinterpret_cast<const uint8_t*>(lds_scales + kt % 4 * kRows + r32) + half * 2;
+    int sx[kFM], sw[kFN];
 #pragma unroll
-    for (int i = 0; i < kFM; ++i) sx[i] = load_scales(xs[i], b, a.blocks);
+    for (int j = 0; j < kFM; ++j) sx[j] = *reinterpret_cast<const uint16_t*>(st + (wm * kFM + j) * 128);
 #pragma unroll
-    for (int i = 0; i < kFN; ++i) sw[i] = load_scales(ws[i], b, a.blocks);
-  };
-
-  const int k_tiles = (a.blocks + kTileBlocks - 1) / kTileBlocks;
-  stage(0, 0);
-  fetch_scales(0);
-  for (int kt = 0; kt < k_tiles; ++kt) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    uint32_t cx[kFM], cw[kFN];
-#pragma unroll
-    for (int i = 0; i < kFM; ++i) cx[i] = sx[i];
-#pragma unroll
-    for (int i = 0; i < kFN; ++i) cw[i] = sw[i];
-    if (kt + 1 < k_tiles) {
-      stage(kt + 1, (kt + 1) % 2);
-      fetch_scales(kt + 1);
-    }
-    const uint8_t* xt = lds + kt % 2 * kStage + wm * kFM * 32 * kRowBytes;
-    const uint8_t* wt = lds + kt % 2 * kStage + (kBM + wn * kFN * 32) * kRowBytes;
-    const int left = a.blocks - kt * kTileBlocks;  // blocks of the rows in this tile
+    for (int i = 0; i < kFN; ++i) sw[i] = *reinterpret_cast<const uint16_t*>(st + (kBM + (wn * kFN + i) * 32) * 4);
     auto step = [&](auto s_) {
       constexpr int s = decltype(s_)::value;
-      const int block = half * 4 + s;
-      const int at = r32 * kRowBytes + ((block ^ (r32 % 8)) * 16);
+      const int at = at0 ^ (s * 16);
       i32x8 xf[kFM], wf[kFN];
 #pragma unroll
       for (int j = 0; j < kFM; ++j) {
-        u32x4 v = *reinterpret_cast<const u32x4*>(xt + j * 32 * kRowBytes + at);
-        if (block >= left) v = u32x4{0, 0, 0, 0};
+        const u32x4 v = *reinterpret_cast<const u32x4*>(xt + j * 32 * kRowBytes + at);
         xf[j] = i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
       }
 #pragma unroll
@@ -308,13 +335,35 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_mm_kernel(GroupedArgs 
       for (int i = 0; i < kFN; ++i)
 #pragma unroll
         for (int j = 0; j < kFM; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[i], xf[j], acc[i][j], kMxFp4, kMxFp4, s,
-                                                                      (int)cw[i], s, (int)cx[j]);
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[i], xf[j], acc[i][j], kMxFp4, kMxFp4, s, sw[i],
+                                                                      s, sx[j]);
     };
     step(std::integral_constant<int, 0>{});
     step(std::integral_constant<int, 1>{});
-    step(std::integral_constant<int, 2>{});
-    step(std::integral_constant<int, 3>{});
+  };
+
+  fetch_scales(0);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i)
+    if (i < k_tiles) stage(i);
+  for (int kt = 0; kt < k_tiles; ++kt) {
+    // this tile has arrived for the wave, and after the barrier for all of them
+    wait_loads<(kXLoads + kWLoads) * (kStages - 2)>(kt + kStages - 1 <= k_tiles);
+    workgroup_barrier();
+    if (kt % 4 == 0) {  // no wave reads the last four tiles' scales any more
+      keep_scales();
+      workgroup_barrier();
+      if (kt + 4 < k_tiles) fetch_scales(kt + 4);
+    }
+    if (kt + kStages - 1 < k_tiles) stage(kt + kStages - 1);
+    const int left = a.blocks - kt * kTileBlocks;
+    if (left < kTileBlocks) {  // no products past the row's end: zeros for the tokens' values there
+      for (int i = threadIdx.x; i < kBM * 4; i += kWgThreads)
+        if (((i % 4) ^ swizzle(i / 4)) >= left)
+          *reinterpret_cast<u32x4*>(lds + kt % kStages * kStage + i * 16) = u32x4{0, 0, 0, 0};
+      workgroup_barrier();
+    }
+    if (works) multiply(kt);
   }
 
   // A lane holds one token row of each fragment and, of its 32 weight rows,
@@ -354,10 +403,10 @@ __global__ __launch_bounds__(64 * kWM * kWN) void grouped_mm_kernel(GroupedArgs 
 // The counts alone, for a call without rows: their verdict.
 __global__ void check_counts_kernel(GroupedArgs a) {
   Tile t;
-  find_tile<256, 256>(a, &t);
+  find_tile<64>(a, &t);
 }
 
-template <int kFM, int kFN, int kWM, int kWN>
+template <int kFM, int kFN, int kWM, int kWN, int kStages>
 mrr_status launch_grouped(GroupedArgs a, bool gated, hipStream_t stream) {
   constexpr int kBM = 32 * kFM * kWM, kBN = 32 * kFN * kWN;
   a.n_tiles = gated ? (a.N / 2 + kBN / 2 - 1) / (kBN / 2) : (a.N + kBN - 1) / kBN;
@@ -367,9 +416,9 @@ mrr_status launch_grouped(GroupedArgs a, bool gated, hipStream_t stream) {
   if (grid > max_launch_grid(64 * kWM * kWN)) return MRR_ERROR_INVALID_SHAPE;
   const dim3 g(static_cast<unsigned>(grid)), b(64 * kWM * kWN);
   if (gated)
-    hipLaunchKernelGGL((grouped_mm_kernel<kFM, kFN, kWM, kWN, true>), g, b, 0, stream, a);
+    hipLaunchKernelGGL((grouped_mm_kernel<kFM, kFN, kWM, kWN, kStages, true>), g, b, 0, stream, a);
   else
-    hipLaunchKernelGGL((grouped_mm_kernel<kFM, kFN, kWM, kWN, false>), g, b, 0, stream, a);
+    hipLaunchKernelGGL((grouped_mm_kernel<kFM, kFN, kWM, kWN, kStages, false>), g, b, 0, stream, a);
   return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
 }
 
@@ -399,8 +448,8 @@ extern "C" mrr_status mrr_mx_grouped_mm(const mrr_grouped_mm_args* args, void* w
   a.out_dtype = args->out_dtype;
   if (args->A == 0) {
     if (workspace == nullptr) return MRR_SUCCESS;
-    hipLaunchKernelGGL(mrr::check_counts_kernel, dim3(1), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL(mrr::check_counts_kernel, dim3(1), dim3(64), 0, stream, a);
     return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
   }
-  return mrr::launch_grouped<2, 2, 2, 2>(a, args->gated == 1, stream);
+  return mrr::launch_grouped<2, 4, 2, 2, 3>(a, args->gated == 1, stream);
 }

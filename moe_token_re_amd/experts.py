@@ -29,21 +29,28 @@ FEW_TOKENS_MAX = 128  # MRR_FEW_TOKENS_MAX
 GROUPED_MM_WORKSPACE_BYTES = 256  # MRR_GROUPED_MM_WORKSPACE_BYTES
 
 
+# The current stream's handle by device index, without a Stream object around it
+# (0.1 us against 1.8 us, of a call of about 8).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _gpu(name, t):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU device (there is no CPU path)")
     return t.device
 
 
 def _call(fn, where, dev, *args):
     """Calls a library entry point on dev's current stream."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = fn(*args, _raw_stream(index))
     if st != _lib.SUCCESS:
         _raise(st, where)
 
@@ -51,19 +58,19 @@ def _call(fn, where, dev, *args):
 def _check_mx(name, packed, scales, dev, lead=None):
     """Checks a pair of packed rows and scales; returns (leading shape, values per row)."""
     _check_tensor(name, packed, dev)
-    _check_tensor(f"{name} scales", scales, dev)
+    _check_tensor(name, scales, dev)
     if packed.dtype not in _PACKED:
         raise TypeError(f"{name} must be float4_e2m1fn_x2 (or its bytes as uint8), got {packed.dtype}")
     if scales.dtype not in _SCALES:
         raise TypeError(f"{name} scales must be float8_e8m0fnu (or uint8), got {scales.dtype}")
     shape = tuple(packed.shape)
-    if len(shape) < 1 or (lead is not None and len(shape) != lead + 1):
+    if len(shape) != (lead + 1 if lead is not None else max(1, len(shape))):
         raise ValueError(f"{name} has shape {shape}" + (f", expected {lead + 1} dimensions" if lead else ""))
     values = 2 * shape[-1]
-    want = shape[:-1] + ((values + 63) // 64, 2)
-    if tuple(scales.shape) != want:
-        raise ValueError(f"{name} scales have shape {tuple(scales.shape)}, expected {want}")
-    return shape[:-1], values
+    rows = shape[:-1]
+    if scales.shape != rows + ((values + 63) // 64, 2):
+        raise ValueError(f"{name} scales have shape {tuple(scales.shape)}, expected {rows + ((values + 63) // 64, 2)}")
+    return rows, values
 
 
 def _mx_args(wide, packed, scales):
@@ -86,7 +93,8 @@ def mx_quantize(x: torch.Tensor, *, out: Optional[Tuple[torch.Tensor, torch.Tens
         raise TypeError(f"x must be float16, bfloat16 or float32, got {x.dtype}")
     if x.dim() < 1 or x.shape[-1] == 0 or x.shape[-1] % 2:
         raise ValueError(f"x must hold rows of an even number of values, got shape {tuple(x.shape)}")
-    lead, H = tuple(x.shape[:-1]), x.shape[-1]
+    *lead, H = x.shape
+    lead = tuple(lead)
     if out is None:
         packed = torch.empty(lead + (H // 2,), dtype=torch.float4_e2m1fn_x2, device=dev)
         scales = torch.empty(lead + ((H + 63) // 64, 2), dtype=torch.float8_e8m0fnu, device=dev)
@@ -146,7 +154,7 @@ def mx_grouped_mm(tokens: torch.Tensor, scales: torch.Tensor, weight: torch.Tens
     _check_tensor("expert_token_num", expert_token_num, dev)
     if expert_token_num.dtype not in _COUNTS:
         raise TypeError(f"expert_token_num must be int32 or int64, got {expert_token_num.dtype}")
-    if tuple(expert_token_num.shape) != (E,):
+    if expert_token_num.shape != (E,):
         raise ValueError(f"expert_token_num has shape {tuple(expert_token_num.shape)}, expected {(E,)}")
     if row_weight is not None:
         _check_tensor("row_weight", row_weight, dev)
@@ -177,7 +185,7 @@ def mx_grouped_mm(tokens: torch.Tensor, scales: torch.Tensor, weight: torch.Tens
     _call(_lib.load().mrr_mx_grouped_mm, "mrr_mx_grouped_mm", dev, ctypes.byref(args), _ptr(workspace), ws_bytes)
     if check:
         with torch.cuda.device(dev):
-            st = _lib.load().mrr_get_device_status(workspace.data_ptr(), torch.cuda.current_stream(dev).cuda_stream)
+            st = _lib.load().mrr_get_device_status(workspace.data_ptr(), _raw_stream(dev.index))
         if st != _lib.SUCCESS:
             _raise(st, "device count check")
     return out
@@ -241,7 +249,7 @@ def moe_few_tokens(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, *
         _check_tensor("router_logits", router_logits, dev)
         if router_logits.dtype != torch.float32:
             raise TypeError("router_logits must be float32")
-        if tuple(router_logits.shape) != (T, E):
+        if router_logits.shape != (T, E):
             raise ValueError(f"router_logits have shape {tuple(router_logits.shape)}, expected {(T, E)}")
         if expert_weight is not None:
             raise ValueError("expert_weight goes with expert_ids")
