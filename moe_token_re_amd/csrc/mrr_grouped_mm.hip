@@ -19,8 +19,8 @@ using f32x16 = float __attribute__((ext_vector_type(16)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
 constexpr int kMxFp4 = 4;        // the matrix instruction's operand format e2m1
-constexpr int kTileBlocks = 4;   // blocks of a row in a K tile (128 values)
-constexpr int kRowBytes = 64;    // of a row in a K tile
+constexpr int kTileBlocks = 8;   // blocks of a row in a K tile (256 values)
+constexpr int kRowBytes = 128;   // of a row in a K tile
 
 struct GroupedArgs {
   const uint8_t* x;
@@ -40,7 +40,7 @@ struct GroupedArgs {
   int32_t out_dtype;
 };
 
-// This workgroup's tile.
+// A tile of the output.
 struct Tile {
   int expert, row, rows, n;  // row: its first row; rows: how many exist; n: the n tile
 };
@@ -61,73 +61,102 @@ __device__ __forceinline__ int32_t count_of(const GroupedArgs& a, int e) {
   return c < 0 || c > a.A ? -1 : static_cast<int32_t>(c);
 }
 
-// Finds the workgroup's tile; false when it has none or the counts are bad.
-// Every wave does it for itself, without LDS or barriers: a lane takes a run of
-// experts, the runs' rows and tiles are scanned over the wave. The exact sum of
-// the counts is kept in two 16-bit halves (4096 counts of at most 2^31).
+// The tiles of all experts, and which of them are this workgroup's. Every wave
+// holds all of it for itself, without LDS or barriers: a lane has a run of
+// experts, the runs' rows and tiles are scanned over the wave.
 template <int kBM>
-__device__ __forceinline__ bool find_tile(const GroupedArgs& a, Tile* t) {
-  const int lane = threadIdx.x % 64;
-  const int per = (a.E + 63) / 64;
-  const int e0 = lane * per, e1 = min(a.E, e0 + per);
-  uint32_t rows = 0, tiles = 0, low = 0, high = 0, bad = 0;
-  for (int e = e0; e < e1; ++e) {
-    const int32_t c = count_of(a, e);
-    if (c < 0) {
-      bad = 1;
-      continue;
-    }
-    rows += c;
-    tiles += (static_cast<uint32_t>(c) + kBM - 1) / kBM;
-    low += c & 0xffff;
-    high += static_cast<uint32_t>(c) >> 16;
-  }
-  const uint32_t rows_in = wave_scan_u32(rows), tiles_in = wave_scan_u32(tiles);
-  const uint64_t total = wave_sum_u32(low) + (static_cast<uint64_t>(wave_sum_u32(high)) << 16);
-  const bool is_bad = __any(bad != 0);
-  const uint32_t all_tiles = __builtin_amdgcn_readlane(tiles_in, 63);
-  const bool valid = !is_bad && total == static_cast<uint64_t>(a.A);
-  if (a.hdr != nullptr && blockIdx.x == 0 && threadIdx.x == 0) {
-    a.hdr->status = valid ? kCountsValid : kTablesBad;
-    a.hdr->flags = is_bad ? kFlagNegative : valid ? 0 : kFlagSumMismatch;
-    a.hdr->inverse = 0;
-    a.hdr->A = a.A;
-    a.hdr->N = 1;
-    a.hdr->E = a.E;
-    a.hdr->total = static_cast<int64_t>(total);
-  }
-  const uint32_t work = all_tiles * static_cast<uint32_t>(a.n_tiles);
-  if (!valid || blockIdx.x >= work) return false;
-  // The hardware deals workgroups to the 8 XCDs in turn; each XCD gets a run of
-  // neighbouring tiles (n fastest), so that they share rows in its L2.
-  const uint32_t xcd = blockIdx.x % 8, at = blockIdx.x / 8;
-  const uint32_t base = work / 8, extra = work % 8;
-  const uint32_t id = xcd * base + min(xcd, extra) + at;
-  const uint32_t m = id / a.n_tiles;
-  uint32_t first = tiles_in - tiles, r = rows_in - rows;
-  const uint64_t mine = __ballot(m >= first && m < first + tiles);
-  const int owner = __ffsll(static_cast<unsigned long long>(mine)) - 1;  // one lane's run holds tile m
-  int expert = e0;
-  uint32_t k = 0, exist = 0;
-  if (lane == owner)
+struct Tiles {
+  int e0, e1;            // the lane's run of experts
+  int32_t head;          // rows of the run's first expert
+  uint32_t rows, tiles;  // first row and first row tile of the run
+  uint32_t end;          // first row tile behind it
+  uint32_t all;          // row tiles of all experts
+  uint32_t first, count, step;  // this workgroup's tiles: first + i step, i < count
+
+  // False when the counts are bad. Their exact sum is kept in two 16-bit
+  // halves (4096 counts of at most 2^31).
+  __device__ __forceinline__ bool scan(const GroupedArgs& a) {
+    const int lane = threadIdx.x % 64;
+    const int per = (a.E + 63) / 64;
+    e0 = lane * per, e1 = min(a.E, e0 + per);
+    uint32_t r = 0, n = 0, low = 0, high = 0, bad = 0;
+    head = 0;
     for (int e = e0; e < e1; ++e) {
-      const uint32_t c = static_cast<uint32_t>(count_of(a, e)), n = (c + kBM - 1) / kBM;
-      if (m < first + n) {
-        expert = e;
-        k = m - first;
-        exist = min(c - k * kBM, static_cast<uint32_t>(kBM));
-        r += k * kBM;
-        break;
+      const int32_t c = count_of(a, e);
+      if (e == e0) head = c;
+      if (c < 0) {
+        bad = 1;
+        continue;
       }
-      first += n;
       r += c;
+      n += (static_cast<uint32_t>(c) + kBM - 1) / kBM;
+      low += c & 0xffff;
+      high += static_cast<uint32_t>(c) >> 16;
     }
-  t->expert = __builtin_amdgcn_readlane(expert, owner);
-  t->row = static_cast<int>(__builtin_amdgcn_readlane(r, owner));
-  t->rows = static_cast<int>(__builtin_amdgcn_readlane(exist, owner));
-  t->n = __builtin_amdgcn_readfirstlane(static_cast<int>(id - m * a.n_tiles));
-  return true;
-}
+    end = wave_scan_u32(n);
+    rows = wave_scan_u32(r) - r;
+    tiles = end - n;
+    all = __builtin_amdgcn_readlane(end, 63);
+    const uint64_t total = wave_sum_u32(low) + (static_cast<uint64_t>(wave_sum_u32(high)) << 16);
+    const bool is_bad = __any(bad != 0);
+    const bool valid = !is_bad && total == static_cast<uint64_t>(a.A);
+    if (a.hdr != nullptr && blockIdx.x == 0 && threadIdx.x == 0) {
+      a.hdr->status = valid ? kCountsValid : kTablesBad;
+      a.hdr->flags = is_bad ? kFlagNegative : valid ? 0 : kFlagSumMismatch;
+      a.hdr->inverse = 0;
+      a.hdr->A = a.A;
+      a.hdr->N = 1;
+      a.hdr->E = a.E;
+      a.hdr->total = static_cast<int64_t>(total);
+    }
+    return valid;
+  }
+
+  // The hardware deals workgroups to the 8 XCDs in turn. Each XCD gets a run of
+  // neighbouring tiles, which its workgroups take in turn, so that they share
+  // rows in its L2.
+  __device__ __forceinline__ void deal(const GroupedArgs& a) {
+    const uint32_t work = all * static_cast<uint32_t>(a.n_tiles);
+    const uint32_t xcd = blockIdx.x % 8, at = blockIdx.x / 8;
+    const uint32_t run = work / 8 + (xcd < work % 8);
+    step = (gridDim.x - xcd + 7) / 8;
+    first = xcd * (work / 8) + min(xcd, work % 8) + at;
+    count = at < run ? (run - at + step - 1) / step : 0;
+  }
+
+  // Tile i of this workgroup. Neighbours go down kGroup row tiles, then to the
+  // next columns: a square of tiles shares the most rows.
+  __device__ __forceinline__ Tile find(const GroupedArgs& a, uint32_t i) const {
+    constexpr uint32_t kGroup = 4;
+    const uint32_t id = first + i * step;
+    const uint32_t band = id / (kGroup * a.n_tiles), in_band = id - band * kGroup * a.n_tiles;
+    const uint32_t high = min(kGroup, all - band * kGroup);
+    const uint32_t n = in_band / high;
+    const uint32_t m = band * kGroup + in_band - n * high;
+    const uint64_t mine = __ballot(m >= tiles && m < end);
+    const int owner = __ffsll(static_cast<unsigned long long>(mine)) - 1;  // one lane's run holds tile m
+    int expert = e0;
+    uint32_t r = rows, exist = 0, before = tiles;
+    if (static_cast<int>(threadIdx.x % 64) == owner)
+      for (int e = e0; e < e1; ++e) {
+        const uint32_t c = static_cast<uint32_t>(e == e0 ? head : count_of(a, e)), t = (c + kBM - 1) / kBM;
+        if (m < before + t) {
+          expert = e;
+          exist = min(c - (m - before) * kBM, static_cast<uint32_t>(kBM));
+          r += (m - before) * kBM;
+          break;
+        }
+        before += t;
+        r += c;
+      }
+    Tile t;
+    t.expert = __builtin_amdgcn_readlane(expert, owner);
+    t.row = static_cast<int>(__builtin_amdgcn_readlane(r, owner));
+    t.rows = static_cast<int>(__builtin_amdgcn_readlane(exist, owner));
+    t.n = static_cast<int>(__builtin_amdgcn_readfirstlane(n));
+    return t;
+  }
+};
 
 // 16 bytes of every lane, at `base` + its offset, to LDS from byte `lds` on in
 // the order of the lanes. In assembly, as the compiler would wait for every
@@ -164,9 +193,9 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
   return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(high) << 32 | low);
 }
 
-// Which bits of a row's number permute its chunks: with them, eight rows of 64
-// bytes fill 128 bytes of banks once, and sixteen rows 256 bytes.
-__device__ __forceinline__ int swizzle(int row) { return (row >> 1 & 2) | ((row >> 1 ^ row >> 3) & 1); }
+// How a row's 16-byte chunks are permuted: by bits of the row's number such that
+// eight rows' same chunks fill 128 bytes of banks once, and sixteen rows' 256.
+__device__ __forceinline__ int swizzle(int row) { return (row >> 1 & 3) | ((row ^ row >> 3) & 1) << 2; }
 
 // Waits until at most kLeft of the wave's loads are on their way, or none.
 template <int kLeft>
@@ -197,87 +226,117 @@ __device__ __forceinline__ void store4(T* p, const float (&v)[4], int count) {
 }
 
 // kFN x kFM fragments of 32 weight rows x 32 token rows a wave, kWN x kWM
-// waves a workgroup. A K tile is 128 values, 64 bytes of a row: the halves of a
-// wave take its first and last two blocks. The tiles go from memory to LDS
+// waves a workgroup, which stays and takes tile after tile. A K tile is 256
+// values, 128 bytes of a row, a whole line of the caches: the halves of a wave
+// take its first and last four blocks, so that the four scales a lane needs for
+// the tile's four products are one dword. The K tiles go from memory to LDS
 // directly, kStages of them in turn: while one is multiplied, the next ones are
-// on their way. A row's 16-byte chunks are permuted by the row's number so that
-// eight or sixteen neighbouring rows touch all banks. The scales of four K tiles
-// (16 bytes of a row) go through registers, as their rows have any alignment.
+// on their way, those of the next output tile among them. The scales of two K
+// tiles (16 bytes of a row) go through registers, as their rows have any alignment.
 template <int kFM, int kFN, int kWM, int kWN, int kStages, bool kGated>
 __global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedArgs a) {
   constexpr int kWaves = kWM * kWN, kWgThreads = 64 * kWaves;
   constexpr int kBM = 32 * kFM * kWM, kBN = 32 * kFN * kWN, kRows = kBM + kBN;
   constexpr int kStage = kRows * kRowBytes;
-  constexpr int kXLoads = kBM / 16 / kWaves, kWLoads = kBN / 16 / kWaves;
+  constexpr int kXLoads = kBM / 8 / kWaves, kWLoads = kBN / 8 / kWaves;
+  static_assert(kXLoads * 8 * kWaves == kBM && kWLoads * 8 * kWaves == kBN, "whole loads");
   constexpr int kOwn = (kRows + kWgThreads - 1) / kWgThreads;  // rows whose scales a thread loads
-  static_assert(kXLoads * 16 * kWaves == kBM && kWLoads * 16 * kWaves == kBN, "whole loads");
   __shared__ __align__(1024) uint8_t lds[kStages * kStage];
-  __shared__ uint32_t lds_scales[4 * kRows];  // [K tile of four][row]
+  __shared__ uint32_t lds_scales[2 * 2 * kRows];  // [K tile of two][half][row]
 
-  Tile t;
-  if (!find_tile<kBM>(a, &t)) return;
+  Tiles<kBM> tiles;
+  if (!tiles.scan(a)) return;
+  tiles.deal(a);
+  if (tiles.count == 0) return;
 
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wm = wave % kWM, wn = wave / kWM;
   const int r32 = lane % 32, half = lane / 32;
-  const int half_n = a.N / 2;                            // gated: the up projection's first row
-  const int n0 = t.n * (kGated ? kBN / 2 : kBN);         // first output column of the tile
+  const int half_n = a.N / 2;                      // gated: the up projection's first row
   const int n_end = kGated ? half_n : a.N;
+  constexpr int kCols = kGated ? kBN / 2 : kBN;    // output columns of a tile
   const int64_t row_bytes = static_cast<int64_t>(a.blocks) * 16;
-  const int64_t w_row0 = static_cast<int64_t>(t.expert) * a.N;
+  const int k_tiles = (a.blocks + kTileBlocks - 1) / kTileBlocks;
 
-  // The weight row in place j of the tile is column `col` of part `part`:
-  // gated, a wave's fragments are the gate's and then the same columns of the
-  // up projection.
+  // The weight row in place j of a tile is column `col` of part `part`: gated,
+  // a wave's fragments are the gate's and then the same columns of the up
+  // projection.
   constexpr int kHalf = 32 * kFN / 2;
   auto part_of = [&](int j) { return kGated ? j % (32 * kFN) / kHalf : 0; };
-  auto col_of = [&](int j) {
+  auto col_of = [&](int j, int n0) {
     const int col = n0 + (kGated ? j / (32 * kFN) * kHalf + j % kHalf : j);
     return min(col, n_end - 1);
   };
 
-  // What this lane stages: of every 16 rows chunk lane % 4 (permuted) of one.
-  const int chunk = (lane % 4) ^ swizzle(lane / 4);
+  // Staging: of every 8 rows a lane brings chunk lane % 8 (permuted) of one.
+  const int chunk_even = (lane % 8) ^ swizzle(lane / 8);  // of rows with bit 3 clear
   uint32_t offset[kXLoads + kWLoads];
   const uint8_t* base[kXLoads + kWLoads];
+  int stage_rows = 0, stage_kt = 0, stage_slot = 0;
+  uint32_t stage_tile = 0;
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
+  // A wave's eight rows are number i * kWaves + wave of the operand's.
+  auto chunk_of = [&](int i) { return chunk_even ^ ((i * kWaves + wave) % 2 * 4); };
+  auto stage_next = [&]() {
+    if (stage_tile >= tiles.count) return;
+    if (stage_kt == 0) {
+      const Tile t = tiles.find(a, stage_tile);
+      const int n0 = t.n * kCols;
+      stage_rows = t.rows;
 #pragma unroll
-  for (int i = 0; i < kXLoads; ++i) {
-    const int j = (i * kWaves + wave) * 16 + lane / 4;
-    base[i] = uniform(a.x + t.row * row_bytes);
-    offset[i] = static_cast<uint32_t>(min(j, t.rows - 1) * row_bytes) + chunk * 16;
-  }
+      for (int i = 0; i < kXLoads; ++i) {
+        const int j = (i * kWaves + wave) * 8 + lane / 8;
+        base[i] = uniform(a.x + t.row * row_bytes);
+        offset[i] = static_cast<uint32_t>(min(j, t.rows - 1) * row_bytes) + chunk_of(i) * 16;
+      }
 #pragma unroll
-  for (int i = 0; i < kWLoads; ++i) {
-    const int j0 = (i * kWaves + wave) * 16;
-    base[kXLoads + i] = uniform(a.w + (w_row0 + n0 + (part_of(j0) ? half_n : 0)) * row_bytes);
-    offset[kXLoads + i] = static_cast<uint32_t>((col_of(j0 + lane / 4) - n0) * row_bytes) + chunk * 16;
-  }
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane(
-      static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds)));
-  const int k_tiles = (a.blocks + kTileBlocks - 1) / kTileBlocks;
-  auto stage = [&](int kt) {
-    const uint32_t to = __builtin_amdgcn_readfirstlane(lds0 + kt % kStages * kStage + wave * 1024);
+      for (int i = 0; i < kWLoads; ++i) {
+        const int j0 = (i * kWaves + wave) * 8;
+        const int64_t row0 = static_cast<int64_t>(t.expert) * a.N + n0 + (part_of(j0) ? half_n : 0);
+        base[kXLoads + i] = uniform(a.w + row0 * row_bytes);
+        offset[kXLoads + i] = static_cast<uint32_t>((col_of(j0 + lane / 8, n0) - n0) * row_bytes) + chunk_of(i) * 16;
+      }
+    }
+    const uint32_t to = __builtin_amdgcn_readfirstlane(lds0 + stage_slot * kStage + wave * 1024);
+    const int left = a.blocks - stage_kt * kTileBlocks;
     // past the row's end: its last block again, which does not count
-    const int left = a.blocks - kt * kTileBlocks;
-    const uint32_t back = chunk >= left ? (chunk - left + 1) * 16 : 0;
+    auto back = [&](int i) { return left < kTileBlocks && chunk_of(i) >= left ? (chunk_of(i) - left + 1) * 16 : 0; };
 #pragma unroll
-    for (int i = 0; i < kXLoads; ++i) load_to_lds(base[i] + kt * kRowBytes, offset[i] - back, to + i * kWaves * 1024);
+    for (int i = 0; i < kXLoads; ++i) {
+      // rows that do not exist stay as they are (with more stages the wait counts all loads)
+      if (kStages == 2 && (i * kWaves + wave) * 8 >= stage_rows) continue;
+      load_to_lds(base[i] + stage_kt * kRowBytes, offset[i] - back(i), to + i * kWaves * 1024);
+    }
 #pragma unroll
     for (int i = 0; i < kWLoads; ++i)
-      load_to_lds(base[kXLoads + i] + kt * kRowBytes, offset[kXLoads + i] - back,
+      load_to_lds(base[kXLoads + i] + stage_kt * kRowBytes, offset[kXLoads + i] - back(i),
                   to + kBM * kRowBytes + i * kWaves * 1024);
+    stage_slot = stage_slot + 1 == kStages ? 0 : stage_slot + 1;
+    if (++stage_kt == k_tiles) {
+      stage_kt = 0;
+      ++stage_tile;
+    }
   };
 
+  // The scales of this thread's rows for two K tiles.
   const uint8_t* s_row[kOwn];
-#pragma unroll
-  for (int i = 0; i < kOwn; ++i) {
-    const int j = threadIdx.x + i * kWgThreads, w = j - kBM;
-    s_row[i] = j < kBM ? a.x_scales + static_cast<int64_t>(t.row + min(j, t.rows - 1)) * a.scale_bytes
-                       : a.w_scales + (w_row0 + col_of(w) + (part_of(w) ? half_n : 0)) * a.scale_bytes;
-  }
   u32x4 held[kOwn];
-  auto fetch_scales = [&](int kt) {  // kt a multiple of 4
-    const int b = kt * kTileBlocks;
+  int scale_kt = 0;
+  uint32_t scale_tile = 0;
+  auto fetch_scales = [&]() {
+    if (scale_tile >= tiles.count) return;
+    if (scale_kt == 0) {
+      const Tile t = tiles.find(a, scale_tile);
+      const int n0 = t.n * kCols;
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        const int j = threadIdx.x + i * kWgThreads, w = min(j, kRows - 1) - kBM;
+        s_row[i] = j < kBM ? a.x_scales + static_cast<int64_t>(t.row + min(j, t.rows - 1)) * a.scale_bytes
+                           : a.w_scales + (static_cast<int64_t>(t.expert) * a.N + col_of(w, n0) +
+                                           (part_of(w) ? half_n : 0)) * a.scale_bytes;
+      }
+    }
+    const int b = scale_kt * kTileBlocks;
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
       if (b + 16 <= a.blocks) {
@@ -286,6 +345,11 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedAr
 #pragma unroll
         for (int c = 0; c < 4; ++c) held[i][c] = load_scales(s_row[i], b + 4 * c, a.blocks);
       }
+    }
+    scale_kt += 2;
+    if (scale_kt >= k_tiles) {
+      scale_kt = 0;
+      ++scale_tile;
     }
   };
   auto keep_scales = [&]() {
@@ -299,24 +363,16 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedAr
   };
 
   f32x16 acc[kFN][kFM];
-#pragma unroll
-  for (int i = 0; i < kFN; ++i)
-#pragma unroll
-    for (int j = 0; j < kFM; ++j)
-#pragma unroll
-      for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.0f;
-
-  const int at0 = r32 * kRowBytes + (((half * 2) ^ swizzle(r32)) * 16);
-  const bool works = wm * kFM * 32 < t.rows;  // a wave without rows only stages
-  auto multiply = [&](int kt) {
-    const uint8_t* xt = lds + kt % kStages * kStage + wm * kFM * 32 * kRowBytes;
-    const uint8_t* wt = lds + kt % kStages * kStage + (kBM + wn * kFN * 32) * kRowBytes;
-    const uint8_t* st = reinterpret_cast<const uint8_t*>(lds_scales + kt % 4 * kRows + r32) + half * 2;
+  const int at0 = r32 * kRowBytes + (((half * 4) ^ swizzle(r32)) * 16);
+  auto multiply = [&](int kt, int slot) {
+    const uint8_t* xt = lds + slot * kStage + wm * kFM * 32 * kRowBytes;
+    const uint8_t* wt = lds + slot * kStage + (kBM + wn * kFN * 32) * kRowBytes;
+    const uint32_t* st = lds_scales + (kt % 2 * 2 + half) * kRows + r32;
     int sx[kFM], sw[kFN];
 #pragma unroll
-    for (int j = 0; j < kFM; ++j) sx[j] = *reinterpret_cast<const uint16_t*>(st + (wm * kFM + j) * 128);
+    for (int j = 0; j < kFM; ++j) sx[j] = static_cast<int>(st[(wm * kFM + j) * 32]);
 #pragma unroll
-    for (int i = 0; i < kFN; ++i) sw[i] = *reinterpret_cast<const uint16_t*>(st + (kBM + (wn * kFN + i) * 32) * 4);
+    for (int i = 0; i < kFN; ++i) sw[i] = static_cast<int>(st[kBM + (wn * kFN + i) * 32]);
     auto step = [&](auto s_) {
       constexpr int s = decltype(s_)::value;
       const int at = at0 ^ (s * 16);
@@ -340,61 +396,80 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedAr
     };
     step(std::integral_constant<int, 0>{});
     step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
   };
 
-  fetch_scales(0);
+  fetch_scales();
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i)
-    if (i < k_tiles) stage(i);
-  for (int kt = 0; kt < k_tiles; ++kt) {
-    // this tile has arrived for the wave, and after the barrier for all of them
-    wait_loads<(kXLoads + kWLoads) * (kStages - 2)>(kt + kStages - 1 <= k_tiles);
-    workgroup_barrier();
-    if (kt % 4 == 0) {  // no wave reads the last four tiles' scales any more
-      keep_scales();
+  for (int i = 0; i < kStages - 1; ++i) stage_next();
+  int slot = 0;
+  for (uint32_t tile = 0; tile < tiles.count; ++tile) {
+    const Tile t = tiles.find(a, tile);
+    const bool works = wm * kFM * 32 < t.rows;  // a wave without rows only stages
+#pragma unroll
+    for (int i = 0; i < kFN; ++i)
+#pragma unroll
+      for (int j = 0; j < kFM; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.0f;
+    for (int kt = 0; kt < k_tiles; ++kt) {
+      // this K tile has arrived for the wave, and after the barrier for all of
+      // them (the last ones of all tiles are not followed by enough others)
+      if (kt > 0 || tile == 0) wait_loads<(kXLoads + kWLoads) * (kStages - 2)>(stage_tile < tiles.count);
       workgroup_barrier();
-      if (kt + 4 < k_tiles) fetch_scales(kt + 4);
+      if (kt % 2 == 0) {  // no wave reads the last two K tiles' scales any more
+        keep_scales();
+        workgroup_barrier();
+        fetch_scales();
+      }
+      stage_next();
+      const int left = a.blocks - kt * kTileBlocks;
+      if (left < kTileBlocks) {  // no products past the row's end: zeros for the tokens' values there
+        for (int i = threadIdx.x; i < kBM * 8; i += kWgThreads)
+          if (((i % 8) ^ swizzle(i / 8)) >= left)
+            *reinterpret_cast<u32x4*>(lds + slot * kStage + i * 16) = u32x4{0, 0, 0, 0};
+        workgroup_barrier();
+      }
+      if (works) multiply(kt, slot);
+      slot = slot + 1 == kStages ? 0 : slot + 1;
     }
-    if (kt + kStages - 1 < k_tiles) stage(kt + kStages - 1);
-    const int left = a.blocks - kt * kTileBlocks;
-    if (left < kTileBlocks) {  // no products past the row's end: zeros for the tokens' values there
-      for (int i = threadIdx.x; i < kBM * 4; i += kWgThreads)
-        if (((i % 4) ^ swizzle(i / 4)) >= left)
-          *reinterpret_cast<u32x4*>(lds + kt % kStages * kStage + i * 16) = u32x4{0, 0, 0, 0};
-      workgroup_barrier();
-    }
-    if (works) multiply(kt);
-  }
+    // what the next tile begins with is here before the stores are on their way,
+    // which it need not wait for
+    wait_loads<0>(false);
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) asm volatile("" : "+v"(held[i]));
 
-  // A lane holds one token row of each fragment and, of its 32 weight rows,
-  // four times four neighbours.
-  constexpr int kOutFN = kGated ? kFN / 2 : kFN;
+    // A lane holds one token row of each fragment and, of its 32 weight rows,
+    // four times four neighbours.
+    constexpr int kOutFN = kGated ? kFN / 2 : kFN;
 #pragma unroll
-  for (int j = 0; j < kFM; ++j) {
-    const int m = (wm * kFM + j) * 32 + r32;
-    if (m >= t.rows) continue;
-    const int64_t row = t.row + m;
-    const float rw = a.row_weight != nullptr ? a.row_weight[row] : 1.0f;
+    for (int j = 0; j < kFM; ++j) {
+      const int m = (wm * kFM + j) * 32 + r32;
+      if (m >= t.rows) continue;
+      const int64_t row = t.row + m;
+      const float rw = a.row_weight != nullptr ? a.row_weight[row] : 1.0f;
 #pragma unroll
-    for (int i = 0; i < kOutFN; ++i) {
+      for (int i = 0; i < kOutFN; ++i) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int col = n0 + (wn * kOutFN + i) * 32 + q * 8 + half * 4;
-        if (col >= n_end) continue;
-        float v[4];
+        for (int q = 0; q < 4; ++q) {
+          const int col = t.n * kCols + (wn * kOutFN + i) * 32 + q * 8 + half * 4;
+          if (col >= n_end) continue;
+          float v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[k] = acc[i][j][q * 4 + k];
-          if constexpr (kGated) v[k] = silu(v[k]) * acc[i + kOutFN][j][q * 4 + k];
-          v[k] *= rw;
+          for (int k = 0; k < 4; ++k) {
+            v[k] = acc[i][j][q * 4 + k];
+            if constexpr (kGated) v[k] = silu(v[k]) * acc[i + kOutFN][j][q * 4 + k];
+            v[k] *= rw;
+          }
+          const int64_t o = row * n_end + col;
+          if (a.out_dtype == MRR_BF16)
+            store4(static_cast<__bf16*>(a.out) + o, v, n_end - col);
+          else if (a.out_dtype == MRR_F16)
+            store4(static_cast<_Float16*>(a.out) + o, v, n_end - col);
+          else
+            store4(static_cast<float*>(a.out) + o, v, n_end - col);
         }
-        const int64_t o = row * n_end + col;
-        if (a.out_dtype == MRR_BF16)
-          store4(static_cast<__bf16*>(a.out) + o, v, n_end - col);
-        else if (a.out_dtype == MRR_F16)
-          store4(static_cast<_Float16*>(a.out) + o, v, n_end - col);
-        else
-          store4(static_cast<float*>(a.out) + o, v, n_end - col);
       }
     }
   }
@@ -402,18 +477,21 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedAr
 
 // The counts alone, for a call without rows: their verdict.
 __global__ void check_counts_kernel(GroupedArgs a) {
-  Tile t;
-  find_tile<64>(a, &t);
+  Tiles<64> t;
+  t.scan(a);
 }
 
 template <int kFM, int kFN, int kWM, int kWN, int kStages>
 mrr_status launch_grouped(GroupedArgs a, bool gated, hipStream_t stream) {
   constexpr int kBM = 32 * kFM * kWM, kBN = 32 * kFN * kWN;
+  constexpr int kLdsBytes = (kBM + kBN) * (kStages * kRowBytes + 16);
   a.n_tiles = gated ? (a.N / 2 + kBN / 2 - 1) / (kBN / 2) : (a.N + kBN - 1) / kBN;
   // the most row tiles there can be: every expert may end in a partial one
   const int64_t m_tiles = a.A / kBM + (a.E < a.A ? a.E : a.A);
-  const int64_t grid = m_tiles * a.n_tiles;
-  if (grid > max_launch_grid(64 * kWM * kWN)) return MRR_ERROR_INVALID_SHAPE;
+  if (m_tiles * a.n_tiles > INT32_MAX) return MRR_ERROR_INVALID_SHAPE;  // tiles are numbered in 32 bits
+  // as many workgroups as the chip holds at once, each taking its tiles in turn
+  const int64_t resident = 256 * (kLdsBytes * 2 <= 160 * 1024 ? 2 : 1);
+  const int64_t grid = m_tiles * a.n_tiles < resident ? m_tiles * a.n_tiles : resident;
   const dim3 g(static_cast<unsigned>(grid)), b(64 * kWM * kWN);
   if (gated)
     hipLaunchKernelGGL((grouped_mm_kernel<kFM, kFN, kWM, kWN, kStages, true>), g, b, 0, stream, a);
@@ -451,5 +529,7 @@ extern "C" mrr_status mrr_mx_grouped_mm(const mrr_grouped_mm_args* args, void* w
     hipLaunchKernelGGL(mrr::check_counts_kernel, dim3(1), dim3(64), 0, stream, a);
     return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
   }
-  return mrr::launch_grouped<2, 4, 2, 2, 3>(a, args->gated == 1, stream);
+  const bool gated = args->gated == 1;
+  if (args->A <= 32 * args->E) return mrr::launch_grouped<1, 2, 1, 4, 2>(a, gated, stream);
+  return mrr::launch_grouped<2, 4, 4, 2, 2>(a, gated, stream);
 }
