@@ -15,6 +15,7 @@ namespace mrr {
 namespace {
 
 using i32x8 = int __attribute__((ext_vector_type(8)));
+using f32x4 = float __attribute__((ext_vector_type(4)));
 using f32x16 = float __attribute__((ext_vector_type(16)));
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 
@@ -197,13 +198,10 @@ __device__ __forceinline__ const uint8_t* uniform(const uint8_t* p) {
 // eight rows' same chunks fill 128 bytes of banks once, and sixteen rows' 256.
 __device__ __forceinline__ int swizzle(int row) { return (row >> 1 & 3) | ((row ^ row >> 3) & 1) << 2; }
 
-// Waits until at most kLeft of the wave's loads are on their way, or none.
+// Waits until at most kLeft of the wave's loads are on their way.
 template <int kLeft>
-__device__ __forceinline__ void wait_loads(bool more) {
-  if (more)
-    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft) : "memory");
-  else
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLeft) : "memory");
 }
 
 // A barrier of LDS alone: loads from memory stay on their way.
@@ -213,15 +211,71 @@ __device__ __forceinline__ void workgroup_barrier() {
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
 
-// Four neighbouring outputs of one row, of which `count` exist.
-template <typename T>
-__device__ __forceinline__ void store4(T* p, const float (&v)[4], int count) {
-  T q[4] = {static_cast<T>(v[0]), static_cast<T>(v[1]), static_cast<T>(v[2]), static_cast<T>(v[3])};
-  if (count >= 4) {
-    __builtin_memcpy(p, q, sizeof(q));
-  } else {
-    for (int i = 0; i < 4; ++i)
-      if (i < count) p[i] = q[i];
+// A wave's results, kFM x kFN fragments, to rows m0 + ... of the tile's `rows`
+// and columns col0 on of `cols`. A lane has one token row of each fragment and,
+// of its 32 weight rows, four times four neighbours; by way of LDS (of the wave
+// alone: 8 KiB, rows' 16-byte chunks permuted) it stores 16 bytes of a row, and
+// its neighbours the next ones.
+template <typename T, int kFM, int kFN, bool kGated>
+__device__ __forceinline__ void store_tile(const f32x16 (&acc)[kFN][kFM], uint8_t* lds, T* out, const float* row_weight,
+                                           int64_t row0, int m0, int rows, int col0, int cols) {
+  constexpr int kOutFN = kGated ? kFN / 2 : kFN;
+  constexpr int kPerPass = kOutFN * 32 * sizeof(T) > 256 ? 256 / 32 / sizeof(T) : kOutFN;  // fragments of a pass
+  constexpr int kChunks = kPerPass * 32 * sizeof(T) / 16;  // of a row
+  constexpr int kValues = 16 / sizeof(T);
+  constexpr int kLineRows = 64 / kChunks;                  // rows that the wave stores at a time
+  using Out = T __attribute__((ext_vector_type(kValues)));
+  // opaque, or the compiler keeps the addresses below in registers that the
+  // products need, spills them, and waits for the stores when it reloads them
+  int lane = threadIdx.x % 64;
+  asm volatile("" : "+v"(lane));
+  const int r32 = lane % 32, half = lane / 32;
+  constexpr int kWide = 4 * sizeof(T);  // bytes of four values
+  const int chunk = lane % kChunks, line = lane / kChunks;
+  // bits of the chunk are below those of the row, so the permutation is one xor
+  const int write0 = r32 * kChunks * 16 + ((r32 % kChunks) * 16 ^ half * kWide / 16 * 16) + half * kWide % 16;
+  const int read0 = line * kChunks * 16;
+  const int64_t pitch = static_cast<int64_t>(cols) * sizeof(T);
+#pragma unroll
+  for (int j = 0; j < kFM; ++j) {
+    const int left = rows - m0 - j * 32;  // rows of this fragment that exist
+    if (left <= 0) return;
+    const int64_t first = row0 + m0 + j * 32;
+    const float rw = row_weight != nullptr ? row_weight[first + min(r32, left - 1)] : 1.0f;
+#pragma unroll
+    for (int i0 = 0; i0 < kOutFN; i0 += kPerPass) {
+#pragma unroll
+      for (int i = i0; i < i0 + kPerPass; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          T v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float y = acc[i][j][q * 4 + k];
+            if constexpr (kGated) y = silu(y) * acc[i + kOutFN][j][q * 4 + k];
+            v[k] = static_cast<T>(y * rw);
+          }
+          uint8_t* to = lds + (write0 ^ ((i - i0) * 32 + q * 8) * static_cast<int>(sizeof(T)));
+          if constexpr (sizeof(T) == 4)
+            *reinterpret_cast<f32x4*>(to) = f32x4{v[0], v[1], v[2], v[3]};
+          else
+            *reinterpret_cast<T __attribute__((ext_vector_type(4)))*>(to) = {v[0], v[1], v[2], v[3]};
+        }
+      const int col = col0 + i0 * 32 + chunk * kValues;
+      uint8_t* p = reinterpret_cast<uint8_t*>(out + first * cols + col) + line * pitch;
+#pragma unroll
+      for (int l = 0; l < 32; l += kLineRows, p += kLineRows * pitch) {
+        const int permuted = (chunk ^ ((l + line) % kChunks)) * 16;
+        const Out v = *reinterpret_cast<const Out*>(lds + read0 + l * kChunks * 16 + permuted);
+        if (l + line >= left) continue;
+        if (col + kValues <= cols) {
+          __builtin_memcpy(p, &v, 16);
+        } else {
+          for (int k = 0; k < kValues; ++k)
+            if (col + k < cols) reinterpret_cast<T*>(p)[k] = v[k];
+        }
+      }
+    }
   }
 }
 
@@ -242,7 +296,7 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedAr
   static_assert(kXLoads * 8 * kWaves == kBM && kWLoads * 8 * kWaves == kBN, "whole loads");
   constexpr int kOwn = (kRows + kWgThreads - 1) / kWgThreads;  // rows whose scales a thread loads
   __shared__ __align__(1024) uint8_t lds[kStages * kStage];
-  __shared__ uint32_t lds_scales[2 * 2 * kRows];  // [K tile of two][half][row]
+  __shared__ uint32_t lds_scales[2 * 2 * 2 * kRows];  // two of [K tile of two][half][row]
 
   Tiles<kBM> tiles;
   if (!tiles.scan(a)) return;
@@ -272,51 +326,51 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedAr
   const int chunk_even = (lane % 8) ^ swizzle(lane / 8);  // of rows with bit 3 clear
   uint32_t offset[kXLoads + kWLoads];
   const uint8_t* base[kXLoads + kWLoads];
-  int stage_rows = 0, stage_kt = 0, stage_slot = 0;
+  int stage_kt = 0, stage_slot = 0;
   uint32_t stage_tile = 0;
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)lds));
   // A wave's eight rows are number i * kWaves + wave of the operand's.
   auto chunk_of = [&](int i) { return chunk_even ^ ((i * kWaves + wave) % 2 * 4); };
-  auto stage_next = [&]() {
-    if (stage_tile >= tiles.count) return;
-    if (stage_kt == 0) {
-      const Tile t = tiles.find(a, stage_tile);
-      const int n0 = t.n * kCols;
-      stage_rows = t.rows;
-#pragma unroll
-      for (int i = 0; i < kXLoads; ++i) {
-        const int j = (i * kWaves + wave) * 8 + lane / 8;
-        base[i] = uniform(a.x + t.row * row_bytes);
-        offset[i] = static_cast<uint32_t>(min(j, t.rows - 1) * row_bytes) + chunk_of(i) * 16;
-      }
-#pragma unroll
-      for (int i = 0; i < kWLoads; ++i) {
-        const int j0 = (i * kWaves + wave) * 8;
-        const int64_t row0 = static_cast<int64_t>(t.expert) * a.N + n0 + (part_of(j0) ? half_n : 0);
-        base[kXLoads + i] = uniform(a.w + row0 * row_bytes);
-        offset[kXLoads + i] = static_cast<uint32_t>((col_of(j0 + lane / 8, n0) - n0) * row_bytes) + chunk_of(i) * 16;
-      }
-    }
-    const uint32_t to = __builtin_amdgcn_readfirstlane(lds0 + stage_slot * kStage + wave * 1024);
+  constexpr int kParity = kWaves % 2;  // whether a wave's loads alternate between the two permutations
+  uint32_t back[2];  // past the row's end: its last block again, which does not count
+  auto stage_begin = [&]() {
     const int left = a.blocks - stage_kt * kTileBlocks;
-    // past the row's end: its last block again, which does not count
-    auto back = [&](int i) { return left < kTileBlocks && chunk_of(i) >= left ? (chunk_of(i) - left + 1) * 16 : 0; };
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      back[i] = left < kTileBlocks && chunk_of(i) >= left ? (chunk_of(i) - left + 1) * 16 : 0;
+    if (stage_tile >= tiles.count || stage_kt != 0) return;  // behind the last tile: its first K tile again
+    const Tile t = tiles.find(a, stage_tile);
+    const int n0 = t.n * kCols;
+    int lane = threadIdx.x % 64;
+    asm volatile("" : "+v"(lane));  // computed here, not kept in registers meanwhile
 #pragma unroll
     for (int i = 0; i < kXLoads; ++i) {
-      // rows that do not exist stay as they are (with more stages the wait counts all loads)
-      if (kStages == 2 && (i * kWaves + wave) * 8 >= stage_rows) continue;
-      load_to_lds(base[i] + stage_kt * kRowBytes, offset[i] - back(i), to + i * kWaves * 1024);
+      const int j = (i * kWaves + wave) * 8 + lane / 8;
+      base[i] = uniform(a.x + t.row * row_bytes);
+      offset[i] = static_cast<uint32_t>(min(j, t.rows - 1) * row_bytes) + chunk_of(i) * 16;
     }
 #pragma unroll
-    for (int i = 0; i < kWLoads; ++i)
-      load_to_lds(base[kXLoads + i] + stage_kt * kRowBytes, offset[kXLoads + i] - back(i),
-                  to + kBM * kRowBytes + i * kWaves * 1024);
+    for (int i = 0; i < kWLoads; ++i) {
+      const int j0 = (i * kWaves + wave) * 8;
+      const int64_t row0 = static_cast<int64_t>(t.expert) * a.N + n0 + (part_of(j0) ? half_n : 0);
+      base[kXLoads + i] = uniform(a.w + row0 * row_bytes);
+      offset[kXLoads + i] = static_cast<uint32_t>((col_of(j0 + lane / 8, n0) - n0) * row_bytes) + chunk_of(i) * 16;
+    }
+  };
+  auto stage_load = [&](int i) {  // load i of the K tile
+    const int in_operand = i < kXLoads ? i : i - kXLoads;
+    const uint32_t to = lds0 + stage_slot * kStage + (i < kXLoads ? 0 : kBM * kRowBytes) +
+                        (in_operand * kWaves + wave) * 1024;
+    load_to_lds(base[i] + stage_kt * kRowBytes, offset[i] - back[in_operand % 2 * kParity], to);
+  };
+  auto stage_end = [&]() {
     stage_slot = stage_slot + 1 == kStages ? 0 : stage_slot + 1;
-    if (++stage_kt == k_tiles) {
+    if (stage_tile < tiles.count && ++stage_kt == k_tiles) {
       stage_kt = 0;
       ++stage_tile;
     }
   };
+  constexpr int kLoads = kXLoads + kWLoads;
 
   // The scales of this thread's rows for two K tiles.
   const uint8_t* s_row[kOwn];
@@ -352,47 +406,62 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedAr
       ++scale_tile;
     }
   };
+  int scale_slot = 0;
   auto keep_scales = [&]() {
+    uint32_t* to = lds_scales + scale_slot * 4 * kRows;
+    scale_slot ^= 1;
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
       const int j = threadIdx.x + i * kWgThreads;
       if (kRows % kWgThreads != 0 && j >= kRows) continue;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) lds_scales[c * kRows + j] = held[i][c];
+      for (int c = 0; c < 4; ++c) to[c * kRows + j] = held[i][c];
     }
   };
 
   f32x16 acc[kFN][kFM];
   const int at0 = r32 * kRowBytes + (((half * 4) ^ swizzle(r32)) * 16);
-  auto multiply = [&](int kt, int slot) {
+  // One K tile: a step's operands are read while the step before is multiplied,
+  // and the next stage's loads are spread among the products.
+  auto multiply = [&](int pair_tile, int scale_slot, int slot) {
     const uint8_t* xt = lds + slot * kStage + wm * kFM * 32 * kRowBytes;
     const uint8_t* wt = lds + slot * kStage + (kBM + wn * kFN * 32) * kRowBytes;
-    const uint32_t* st = lds_scales + (kt % 2 * 2 + half) * kRows + r32;
+    const uint32_t* st = lds_scales + ((scale_slot * 2 + pair_tile) * 2 + half) * kRows + r32;
     int sx[kFM], sw[kFN];
+    u32x4 xf[2][kFM], wf[2][kFN];
+    auto read = [&](int s) {
+      const int at = at0 ^ (s * 16);
+#pragma unroll
+      for (int i = 0; i < kFN; ++i) wf[s % 2][i] = *reinterpret_cast<const u32x4*>(wt + i * 32 * kRowBytes + at);
+#pragma unroll
+      for (int j = 0; j < kFM; ++j) xf[s % 2][j] = *reinterpret_cast<const u32x4*>(xt + j * 32 * kRowBytes + at);
+    };
 #pragma unroll
     for (int j = 0; j < kFM; ++j) sx[j] = static_cast<int>(st[(wm * kFM + j) * 32]);
 #pragma unroll
     for (int i = 0; i < kFN; ++i) sw[i] = static_cast<int>(st[kBM + (wn * kFN + i) * 32]);
+    read(0);
+    constexpr int kProducts = kFN * kFM;
     auto step = [&](auto s_) {
       constexpr int s = decltype(s_)::value;
-      const int at = at0 ^ (s * 16);
-      i32x8 xf[kFM], wf[kFN];
+      if (s < 3) read(s + 1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int j = 0; j < kFM; ++j) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(xt + j * 32 * kRowBytes + at);
-        xf[j] = i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+      for (int n = 0; n < kProducts; ++n) {
+        const int i = n / kFM, j = n % kFM;
+        const u32x4 w = wf[s % 2][i], x = xf[s % 2][j];
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            i32x8{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0},
+            i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0}, acc[i][j], kMxFp4, kMxFp4, s, sw[i], s, sx[j]);
+        // load l follows product l * (4 kProducts) / kLoads of the K tile
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l)
+          if (l * 4 * kProducts / kLoads == s * kProducts + n) {
+            __builtin_amdgcn_sched_barrier(0);
+            stage_load(l);
+            __builtin_amdgcn_sched_barrier(0);
+          }
       }
-#pragma unroll
-      for (int i = 0; i < kFN; ++i) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(wt + i * 32 * kRowBytes + at);
-        wf[i] = i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
-      }
-#pragma unroll
-      for (int i = 0; i < kFN; ++i)
-#pragma unroll
-        for (int j = 0; j < kFM; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wf[i], xf[j], acc[i][j], kMxFp4, kMxFp4, s, sw[i],
-                                                                      s, sx[j]);
     };
     step(std::integral_constant<int, 0>{});
     step(std::integral_constant<int, 1>{});
@@ -401,9 +470,16 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedAr
   };
 
   fetch_scales();
+  keep_scales();
+  fetch_scales();
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) stage_next();
-  int slot = 0;
+  for (int i = 0; i < kStages - 1; ++i) {
+    stage_begin();
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) stage_load(l);
+    stage_end();
+  }
+  int slot = 0, read_slot = 1;
   for (uint32_t tile = 0; tile < tiles.count; ++tile) {
     const Tile t = tiles.find(a, tile);
     const bool works = wm * kFM * 32 < t.rows;  // a wave without rows only stages
@@ -414,16 +490,15 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedAr
 #pragma unroll
         for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.0f;
     for (int kt = 0; kt < k_tiles; ++kt) {
-      // this K tile has arrived for the wave, and after the barrier for all of
-      // them (the last ones of all tiles are not followed by enough others)
-      if (kt > 0 || tile == 0) wait_loads<(kXLoads + kWLoads) * (kStages - 2)>(stage_tile < tiles.count);
+      // this K tile has arrived for the wave, and after the barrier for all of them
+      if (kt > 0 || tile == 0) wait_loads<kLoads * (kStages - 2)>();
       workgroup_barrier();
-      if (kt % 2 == 0) {  // no wave reads the last two K tiles' scales any more
+      if (kt % 2 == 0) {  // the next two K tiles' scales, where no wave reads any more
+        read_slot ^= 1;
         keep_scales();
-        workgroup_barrier();
         fetch_scales();
       }
-      stage_next();
+      stage_begin();
       const int left = a.blocks - kt * kTileBlocks;
       if (left < kTileBlocks) {  // no products past the row's end: zeros for the tokens' values there
         for (int i = threadIdx.x; i < kBM * 8; i += kWgThreads)
@@ -431,46 +506,37 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedAr
             *reinterpret_cast<u32x4*>(lds + slot * kStage + i * 16) = u32x4{0, 0, 0, 0};
         workgroup_barrier();
       }
-      if (works) multiply(kt, slot);
+      if (works) {
+        multiply(kt % 2, read_slot, slot);
+      } else {
+#pragma unroll
+        for (int l = 0; l < kLoads; ++l) stage_load(l);
+      }
+      stage_end();
       slot = slot + 1 == kStages ? 0 : slot + 1;
     }
     // what the next tile begins with is here before the stores are on their way,
     // which it need not wait for
-    wait_loads<0>(false);
+    wait_loads<0>();
+    workgroup_barrier();
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) asm volatile("" : "+v"(held[i]));
 
-    // A lane holds one token row of each fragment and, of its 32 weight rows,
-    // four times four neighbours.
-    constexpr int kOutFN = kGated ? kFN / 2 : kFN;
-#pragma unroll
-    for (int j = 0; j < kFM; ++j) {
-      const int m = (wm * kFM + j) * 32 + r32;
-      if (m >= t.rows) continue;
-      const int64_t row = t.row + m;
-      const float rw = a.row_weight != nullptr ? a.row_weight[row] : 1.0f;
-#pragma unroll
-      for (int i = 0; i < kOutFN; ++i) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int col = t.n * kCols + (wn * kOutFN + i) * 32 + q * 8 + half * 4;
-          if (col >= n_end) continue;
-          float v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            v[k] = acc[i][j][q * 4 + k];
-            if constexpr (kGated) v[k] = silu(v[k]) * acc[i + kOutFN][j][q * 4 + k];
-            v[k] *= rw;
-          }
-          const int64_t o = row * n_end + col;
-          if (a.out_dtype == MRR_BF16)
-            store4(static_cast<__bf16*>(a.out) + o, v, n_end - col);
-          else if (a.out_dtype == MRR_F16)
-            store4(static_cast<_Float16*>(a.out) + o, v, n_end - col);
-          else
-            store4(static_cast<float*>(a.out) + o, v, n_end - col);
-        }
-      }
+    // The results go to memory by way of the K tile that was multiplied last, so
+    // that a row's neighbouring columns are stored together.
+    if (works) {
+      auto store = [&](auto* type) {
+        using T = std::remove_pointer_t<decltype(type)>;
+        store_tile<T, kFM, kFN, kGated>(acc, lds + (slot == 0 ? kStages - 1 : slot - 1) * kStage + wave * (kStage / kWaves),
+                                        static_cast<T*>(a.out), a.row_weight, t.row, wm * kFM * 32, t.rows,
+                                        t.n * kCols + wn * (kCols / kWN), n_end);
+      };
+      if (a.out_dtype == MRR_BF16)
+        store(static_cast<__bf16*>(nullptr));
+      else if (a.out_dtype == MRR_F16)
+        store(static_cast<_Float16*>(nullptr));
+      else
+        store(static_cast<float*>(nullptr));
     }
   }
 }
@@ -484,7 +550,7 @@ __global__ void check_counts_kernel(GroupedArgs a) {
 template <int kFM, int kFN, int kWM, int kWN, int kStages>
 mrr_status launch_grouped(GroupedArgs a, bool gated, hipStream_t stream) {
   constexpr int kBM = 32 * kFM * kWM, kBN = 32 * kFN * kWN;
-  constexpr int kLdsBytes = (kBM + kBN) * (kStages * kRowBytes + 16);
+  constexpr int kLdsBytes = (kBM + kBN) * (kStages * kRowBytes + 32);
   a.n_tiles = gated ? (a.N / 2 + kBN / 2 - 1) / (kBN / 2) : (a.N + kBN - 1) / kBN;
   // the most row tiles there can be: every expert may end in a partial one
   const int64_t m_tiles = a.A / kBM + (a.E < a.A ? a.E : a.A);
