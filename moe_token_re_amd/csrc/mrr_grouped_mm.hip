@@ -209,18 +209,26 @@ __device__ __forceinline__ void workgroup_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
+// g / (1 + exp(-g)) with the chip's own exponential and reciprocal (an ulp each;
+// a division would cost more than all else that is done to a result).
+__device__ __forceinline__ float silu(float g) {
+  constexpr float kLog2E = 1.44269504f;
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2E * g));
+}
 
 // A wave's results, kFM x kFN fragments, to rows m0 + ... of the tile's `rows`
 // and columns col0 on of `cols`. A lane has one token row of each fragment and,
-// of its 32 weight rows, four times four neighbours; by way of LDS (of the wave
-// alone: 8 KiB, rows' 16-byte chunks permuted) it stores 16 bytes of a row, and
+// of its 32 weight rows, four times four neighbours; by way of LDS (kLdsBytes of
+// the wave alone, rows' 16-byte chunks permuted) it stores 16 bytes of a row, and
 // its neighbours the next ones.
-template <typename T, int kFM, int kFN, bool kGated>
+template <typename T, int kFM, int kFN, bool kGated, int kLdsBytes>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[kFN][kFM], uint8_t* lds, T* out, const float* row_weight,
                                            int64_t row0, int m0, int rows, int col0, int cols) {
   constexpr int kOutFN = kGated ? kFN / 2 : kFN;
-  constexpr int kPerPass = kOutFN * 32 * sizeof(T) > 256 ? 256 / 32 / sizeof(T) : kOutFN;  // fragments of a pass
+  constexpr int kRowMost = kLdsBytes >= 32 * 256 ? 256 : 128;  // bytes of a row that a pass can take
+  static_assert(kLdsBytes >= 32 * kRowMost, "32 rows");
+  constexpr int kMost = kRowMost / 32 / static_cast<int>(sizeof(T));
+  constexpr int kPerPass = kOutFN < kMost ? kOutFN : kMost;     // fragments of a pass
   constexpr int kChunks = kPerPass * 32 * sizeof(T) / 16;  // of a row
   constexpr int kValues = 16 / sizeof(T);
   constexpr int kLineRows = 64 / kChunks;                  // rows that the wave stores at a time
@@ -453,10 +461,10 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedAr
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
             i32x8{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0},
             i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0}, acc[i][j], kMxFp4, kMxFp4, s, sw[i], s, sx[j]);
-        // load l follows product l * (4 kProducts) / kLoads of the K tile
+        // a load after each of the first products: the later ones are the time they have
 #pragma unroll
         for (int l = 0; l < kLoads; ++l)
-          if (l * 4 * kProducts / kLoads == s * kProducts + n) {
+          if (l % (4 * kProducts) == s * kProducts + n) {
             __builtin_amdgcn_sched_barrier(0);
             stage_load(l);
             __builtin_amdgcn_sched_barrier(0);
@@ -527,7 +535,7 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedAr
     if (works) {
       auto store = [&](auto* type) {
         using T = std::remove_pointer_t<decltype(type)>;
-        store_tile<T, kFM, kFN, kGated>(acc, lds + (slot == 0 ? kStages - 1 : slot - 1) * kStage + wave * (kStage / kWaves),
+        store_tile<T, kFM, kFN, kGated, kStage / kWaves>(acc, lds + (slot == 0 ? kStages - 1 : slot - 1) * kStage + wave * (kStage / kWaves),
                                         static_cast<T*>(a.out), a.row_weight, t.row, wm * kFM * 32, t.rows,
                                         t.n * kCols + wn * (kCols / kWN), n_end);
       };
@@ -547,24 +555,58 @@ __global__ void check_counts_kernel(GroupedArgs a) {
   t.scan(a);
 }
 
-template <int kFM, int kFN, int kWM, int kWN, int kStages>
-mrr_status launch_grouped(GroupedArgs a, bool gated, hipStream_t stream) {
-  constexpr int kBM = 32 * kFM * kWM, kBN = 32 * kFN * kWN;
-  constexpr int kLdsBytes = (kBM + kBN) * (kStages * kRowBytes + 32);
-  a.n_tiles = gated ? (a.N / 2 + kBN / 2 - 1) / (kBN / 2) : (a.N + kBN - 1) / kBN;
-  // the most row tiles there can be: every expert may end in a partial one
-  const int64_t m_tiles = a.A / kBM + (a.E < a.A ? a.E : a.A);
-  if (m_tiles * a.n_tiles > INT32_MAX) return MRR_ERROR_INVALID_SHAPE;  // tiles are numbered in 32 bits
-  // as many workgroups as the chip holds at once, each taking its tiles in turn
-  const int64_t resident = 256 * (kLdsBytes * 2 <= 160 * 1024 ? 2 : 1);
-  const int64_t grid = m_tiles * a.n_tiles < resident ? m_tiles * a.n_tiles : resident;
-  const dim3 g(static_cast<unsigned>(grid)), b(64 * kWM * kWN);
-  if (gated)
-    hipLaunchKernelGGL((grouped_mm_kernel<kFM, kFN, kWM, kWN, kStages, true>), g, b, 0, stream, a);
-  else
-    hipLaunchKernelGGL((grouped_mm_kernel<kFM, kFN, kWM, kWN, kStages, false>), g, b, 0, stream, a);
-  return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
-}
+// A shape of tiles: kFN x kFM fragments a wave, kWN x kWM waves, and what it
+// costs, in nanoseconds measured on the chip: a K tile of a workgroup that has
+// its CU to itself, one beside as many others as the CU holds, and what comes
+// on top for a tile of the output (its first loads, its stores).
+template <int kFM_, int kFN_, int kWM_, int kWN_, int kAlone, int kFull, int kOutput>
+struct Shape {
+  static constexpr int kFM = kFM_, kFN = kFN_, kWM = kWM_, kWN = kWN_;
+  static constexpr int kBM = 32 * kFM * kWM, kBN = 32 * kFN * kWN;
+  static constexpr int kStages = 2;
+  static constexpr int kLdsBytes = (kBM + kBN) * (kStages * kRowBytes + 32);
+  static constexpr int kByLds = 160 * 1024 / kLdsBytes, kByWaves = 8 / (kWM * kWN);
+  static constexpr int64_t kResident = 256 * (kByLds < kByWaves ? kByLds : kByWaves);  // workgroups the chip holds
+
+  static int64_t n_tiles(const GroupedArgs& a, bool gated) {
+    return gated ? (a.N / 2 + kBN / 2 - 1) / (kBN / 2) : (a.N + kBN - 1) / kBN;
+  }
+
+  // The call's time as far as the host can know it: rows spread evenly over
+  // the experts, half a tile of each expert's rows empty.
+  static int64_t cost(const GroupedArgs& a, bool gated) {
+    const int64_t used = a.E < a.A ? a.E : a.A;
+    const int64_t rows = a.A / kBM + (used + 1) / 2;
+    const int64_t tiles = (rows > used ? rows : used) * n_tiles(a, gated);
+    const int64_t rounds = (tiles + kResident - 1) / kResident;
+    const int64_t k_tiles = (a.blocks + kTileBlocks - 1) / kTileBlocks;
+    return rounds * (k_tiles * (tiles <= 256 ? kAlone : kFull) + kOutput);
+  }
+
+  static mrr_status launch(GroupedArgs a, bool gated, hipStream_t stream) {
+    a.n_tiles = static_cast<int32_t>(n_tiles(a, gated));
+    // the most row tiles there can be: every expert may end in a partial one
+    const int64_t m_tiles = a.A / kBM + (a.E < a.A ? a.E : a.A);
+    if (m_tiles * a.n_tiles > INT32_MAX) return MRR_ERROR_INVALID_SHAPE;  // tiles are numbered in 32 bits
+    // as many workgroups as the chip holds at once, each taking its tiles in turn
+    const int64_t grid = m_tiles * a.n_tiles < kResident ? m_tiles * a.n_tiles : kResident;
+    const dim3 g(static_cast<unsigned>(grid)), b(64 * kWM * kWN);
+    if (gated)
+      hipLaunchKernelGGL((grouped_mm_kernel<kFM, kFN, kWM, kWN, kStages, true>), g, b, 0, stream, a);
+    else
+      hipLaunchKernelGGL((grouped_mm_kernel<kFM, kFN, kWM, kWN, kStages, false>), g, b, 0, stream, a);
+    return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
+  }
+};
+
+// Large tiles bring each operand row from L2 fewer times, small ones fill the
+// chip with fewer rows. Measured (us) as 256 x 256, 128 x 128, 64 x 128 (rows x
+// weight rows): 16384 rows of 16 experts, K 2048, N 7168: 171, 197, 272; 1024
+// rows of 8 experts, K 4096, N 4096: 30, 24, 32; 64 rows of 16 experts, K 2048,
+// N 4096: 18.1, 14.8, 14.4; 256 rows of one expert, K 7168, N 1024: 42, 20, 17.
+using Large = Shape<2, 4, 4, 2, 1500, 2000, 6000>;
+using Medium = Shape<2, 2, 2, 2, 720, 1400, 4000>;
+using Small = Shape<1, 2, 2, 2, 610, 1100, 3000>;
 
 }  // namespace
 }  // namespace mrr
@@ -596,6 +638,8 @@ extern "C" mrr_status mrr_mx_grouped_mm(const mrr_grouped_mm_args* args, void* w
     return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
   }
   const bool gated = args->gated == 1;
-  if (args->A <= 32 * args->E) return mrr::launch_grouped<1, 2, 1, 4, 2>(a, gated, stream);
-  return mrr::launch_grouped<2, 4, 4, 2, 2>(a, gated, stream);
+  const int64_t large = mrr::Large::cost(a, gated), medium = mrr::Medium::cost(a, gated);
+  const int64_t small = mrr::Small::cost(a, gated);
+  if (small <= medium && small <= large) return mrr::Small::launch(a, gated, stream);
+  return medium <= large ? mrr::Medium::launch(a, gated, stream) : mrr::Large::launch(a, gated, stream);
 }
