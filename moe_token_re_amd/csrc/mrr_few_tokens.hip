@@ -1,17 +1,17 @@
-// mrr_few_tokens.hip -- a whole mixture-of-experts layer for a few tokens in
-// two kernels:
+// mrr_few_tokens.hip -- a whole mixture-of-experts layer for a few tokens:
 //     h[t, j] = p[t, j] silu(Wg[e] x[t]) * (Wu[e] x[t])   for e = ids[t, j],
 //     y[t]    = sum over j of Wd[e] h[t, j].
-// Bound by reading the chosen experts' weights, once each. The first kernel
-// also finds the routing (softmax and top-k of the router's logits, or given
-// ids): every workgroup does it for itself, as it needs it to know its work.
-// The second adds an output row's experts in one workgroup, in a fixed order,
-// so no sum crosses workgroups and results do not depend on timing.
+// Bound by reading the chosen experts' weights, once each. Two kernels, one a
+// product; for more than a few tokens a third before them finds the routing
+// (softmax and top-k of the router's logits), which every workgroup of the first
+// would otherwise find for itself. The second adds an output row's experts in one
+// workgroup, in a fixed order, so no sum crosses workgroups and results do not
+// depend on timing.
 //
-// Both feed the 16x16x32 matrix instruction with 16 weight rows and up to 16
-// tokens. A lane reads 16 bytes of a weight row at a time: eight 16-bit values
-// (one product), or a block of 32 4-bit values (four products), widened to
-// bf16 with their scale, which is exact.
+// Both feed the 16x16x32 matrix instruction with 16 weight rows and up to 16 of
+// the tokens that chose the expert. A lane reads 32 bytes of a weight row at a
+// time: 16 16-bit values, or two blocks of 32 4-bit values, widened to bf16 with
+// their scale, which is exact.
 #include "mrr_device.h"
 #include "mrr_experts.h"
 
@@ -25,10 +25,15 @@ using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
 
 constexpr int kMaxExperts = static_cast<int>(kFewMaxExperts);
+#ifndef UPB
+#define UPB 2
+#define DNB 2
+#endif
 constexpr int kUpWaves = 4;       // first kernel: they share a unit's rows, each a part of their length
 constexpr int kDownWaves = 8;     // second kernel: each takes experts, or parts of them
 constexpr int kRows = 16;         // weight rows of a fragment
 constexpr int kDownTokens = 64;   // tokens of a workgroup of the second kernel
+constexpr int kSelfRouted = 4;    // so many tokens, a wave each, the first kernel routes itself
 
 struct FewArgs {
   const uint8_t* x;
@@ -41,10 +46,14 @@ struct FewArgs {
   const uint8_t* down_scales;
   uint8_t* y;
   int32_t* ws_ids;
+  float* ws_weight;
   uint8_t* ws_h;
   int32_t T, H, E, I, k;
   int32_t renormalize;
 };
+
+inline __host__ __device__ size_t up_part_bytes(int tiles) { return sizeof(f32x4) * kUpWaves * 2 * tiles * 64; }
+inline __host__ __device__ size_t down_sum_bytes(int tokens) { return sizeof(f32x4) * kDownWaves * tokens * 4; }
 
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   constexpr int kRowShr1 = 0x111, kRowShr2 = 0x112, kRowShr4 = 0x114, kRowShr8 = 0x118;
@@ -134,93 +143,172 @@ __device__ __forceinline__ void choose(const FewArgs& a, int token, int lane, in
   *weight = p / wave_sum_f32(sum);
 }
 
-struct Routing {
-  float* weight;  // [T][k]
-  int16_t* id;    // [T][k], -1: none
-};
+// The routing of token t by one wave: its experts (-1: none) and their weights.
+__device__ __forceinline__ void route_token(const FewArgs& a, int t, int lane, int* id, float* weight) {
+  if (a.E <= 64)
+    choose<1>(a, t, lane, id, weight);
+  else if (a.E <= 256)
+    choose<4>(a, t, lane, id, weight);
+  else
+    choose<kMaxExperts / 64>(a, t, lane, id, weight);
+}
 
-// The routing of all tokens into LDS, by all waves of the workgroup.
-template <int kWaves>
-__device__ void find_routing(const FewArgs& a, const Routing& r) {
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  if (a.logits != nullptr) {
-    for (int t = wave; t < a.T; t += kWaves) {
-      int id;
-      float weight;
-      if (a.E <= 64)
-        choose<1>(a, t, lane, &id, &weight);
-      else if (a.E <= 256)
-        choose<4>(a, t, lane, &id, &weight);
-      else
-        choose<kMaxExperts / 64>(a, t, lane, &id, &weight);
-      if (lane < a.k) {
-        r.id[t * a.k + lane] = static_cast<int16_t>(id);
-        r.weight[t * a.k + lane] = weight;
-      }
-    }
-  } else {
-    // An expert that a token names again counts at its first place, with the
-    // sum of the weights.
-    for (int s = threadIdx.x; s < a.T * a.k; s += kWaves * 64) {
-      const int t = s / a.k, j = s - t * a.k;
-      const int id = a.ids[s];
-      float weight = a.weight[s];
-      bool keep = id >= 0 && id < a.E;
-      for (int i = 0; i < a.k; ++i) {
-        if (i == j || a.ids[t * a.k + i] != id) continue;
-        if (i < j)
-          keep = false;
-        else
-          weight += a.weight[t * a.k + i];
-      }
-      r.id[s] = static_cast<int16_t>(keep ? id : -1);
-      r.weight[s] = weight;
-    }
+// For more than kSelfRouted tokens: a wave a token, once for the other kernels.
+__global__ __launch_bounds__(64) void few_route_kernel(FewArgs a) {
+  int id;
+  float weight;
+  route_token(a, blockIdx.x, threadIdx.x, &id, &weight);
+  if (static_cast<int>(threadIdx.x) < a.k) {
+    a.ws_ids[blockIdx.x * a.k + threadIdx.x] = id;
+    a.ws_weight[blockIdx.x * a.k + threadIdx.x] = weight;
   }
 }
+
+// Which tokens an expert has, in LDS sized by the call.
+struct Plan {
+  int32_t* count;     // [E]: tokens of an expert, then the place of its next one
+  int32_t* wave_sum;  // [16]
+  float* weight;      // [slots] (first kernel)
+  int16_t* id;        // [slots]: the expert of token t's choice j, at t k + j; -1: none
+  int16_t* slot;      // [slots]: the slots by expert
+  int16_t* active;    // [E]: the experts that have tokens
+  int16_t* first;     // [E + 1]: of an active expert: its first place in `slot`
+  int experts;        // that have tokens
+};
+
+inline __host__ __device__ size_t plan_bytes(int slots, int E) {
+  return (4 * (E + 16 + slots) + 2 * (2 * slots + 2 * E + 1) + 15) / 16 * 16;
+}
+
+__device__ __forceinline__ Plan carve(uint8_t* lds, int slots, int E) {
+  Plan p;
+  p.count = reinterpret_cast<int32_t*>(lds);
+  p.wave_sum = p.count + E;
+  p.weight = reinterpret_cast<float*>(p.wave_sum + 16);
+  p.id = reinterpret_cast<int16_t*>(p.weight + slots);
+  p.slot = p.id + slots;
+  p.active = p.slot + slots;
+  p.first = p.active + E;
+  p.experts = 0;
+  return p;
+}
+
+// From p.id (written, not yet waited for) the rest of the plan, by all kWaves
+// waves of the workgroup.
+template <int kWaves>
+__device__ __forceinline__ void make_plan(Plan& p, int slots, int E) {
+  constexpr int kThreads = kWaves * 64;
+  const int tid = threadIdx.x;
+  for (int e = tid; e < E; e += kThreads) p.count[e] = 0;
+  __syncthreads();
+  for (int i = tid; i < slots; i += kThreads)
+    if (p.id[i] >= 0) atomicAdd(&p.count[p.id[i]], 1);
+  __syncthreads();
+  const int per = (E + kThreads - 1) / kThreads;
+  uint32_t used = 0, tokens = 0;
+  for (int i = 0; i < per; ++i) {
+    const int e = tid * per + i;
+    const int c = e < E ? p.count[e] : 0;
+    used += c > 0;
+    tokens += c;
+  }
+  // both sums in one word: at most 1024 experts and 2048 slots
+  const uint32_t in = wave_scan_u32(used << 16 | tokens);
+  if (tid % 64 == 63) p.wave_sum[tid / 64] = static_cast<int>(in);
+  __syncthreads();
+  uint32_t before = in - (used << 16 | tokens), all = 0;
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < tid / 64) before += p.wave_sum[w];
+    all += p.wave_sum[w];
+  }
+  int next = before >> 16, place = before & 0xffff;
+  for (int i = 0; i < per; ++i) {
+    const int e = tid * per + i;
+    const int c = e < E ? p.count[e] : 0;
+    if (c > 0) {
+      p.active[next] = static_cast<int16_t>(e);
+      p.first[next++] = static_cast<int16_t>(place);
+      p.count[e] = place;
+      place += c;
+    }
+  }
+  p.experts = __builtin_amdgcn_readfirstlane(all >> 16);
+  if (tid == 0) p.first[p.experts] = static_cast<int16_t>(all & 0xffff);
+  __syncthreads();
+  // the order within an expert does not matter: a token's sums are its own
+  for (int i = tid; i < slots; i += kThreads) {
+    const int e = p.id[i];
+    if (e >= 0) p.slot[atomicAdd(&p.count[e], 1)] = static_cast<int16_t>(i);
+  }
+  __syncthreads();
+}
+
+// A chunk is 128 bytes of a weight row, a whole line of the caches. Lane group g
+// of four takes 32 bytes of it, two pieces of 16: 32 4-bit values each, whose two
+// scales are neighbours, or 8 values of 16 bits.
+template <bool kMx>
+struct Weights {
+  u32x4 v[2];
+  uint32_t scale;  // of the two pieces, a byte each
+};
+
+template <bool kMx, int kTiles>
+struct Tokens {
+  u32x4 v[kTiles][2][kMx ? 4 : 1];
+};
 
 template <bool kMx>
 __device__ __forceinline__ int row_bytes(int n) { return kMx ? n / 2 : n * 2; }
 
-// What a lane reads of a weight row for one chunk (64 bytes of the row over
-// the four lane groups).
+// Chunk c of a weight row of `pieces`; zeros past the row's end.
 template <bool kMx>
-struct WeightPiece {
-  u32x4 v;
-  uint32_t scale;
-};
-
-template <bool kMx>
-__device__ __forceinline__ WeightPiece<kMx> load_weight(const uint8_t* row, const uint8_t* scales, int piece,
-                                                        bool valid) {
-  WeightPiece<kMx> w;
-  w.v = u32x4{0, 0, 0, 0};
-  w.scale = 127;
-  if (valid) {
-    w.v = *reinterpret_cast<const u32x4*>(row + static_cast<int64_t>(piece) * 16);
-    if constexpr (kMx) w.scale = scales[piece];
+__device__ __forceinline__ void load_weights(Weights<kMx>& w, const uint8_t* row, const uint8_t* scales, int c,
+                                             int group, int pieces) {
+  const int p = c * 8 + group * 2;
+  if (c * 8 + 8 <= pieces) {
+    const u32x4* from = reinterpret_cast<const u32x4*>(row) + p;
+    w.v[0] = from[0];
+    w.v[1] = from[1];
+    if constexpr (kMx) {
+      uint16_t s;
+      __builtin_memcpy(&s, scales + p, 2);
+      w.scale = s;
+    }
+  } else {
+    const int p0 = min(p, pieces - 1), p1 = min(p + 1, pieces - 1);
+    const u32x4 v0 = reinterpret_cast<const u32x4*>(row)[p0], v1 = reinterpret_cast<const u32x4*>(row)[p1];
+    w.v[0] = p < pieces ? v0 : u32x4{0, 0, 0, 0};
+    w.v[1] = p + 1 < pieces ? v1 : u32x4{0, 0, 0, 0};
+    if constexpr (kMx) {
+      const uint32_t s0 = scales[p0], s1 = scales[p1];
+      w.scale = (p < pieces ? s0 : 127u) | (p + 1 < pieces ? s1 : 127u) << 8;
+    }
   }
-  return w;
 }
 
-// The token's values that go with a weight piece: 32 (4-bit weights) or 8.
-template <bool kMx>
-struct TokenPiece {
-  u32x4 v[kMx ? 4 : 1];
-};
-
-template <bool kMx>
-__device__ __forceinline__ TokenPiece<kMx> load_token(const uint8_t* row, int piece, bool valid) {
+// The tokens' values that go with it; zeros past the row's end. A lane without a
+// token keeps what it has: it computes a column that nobody reads.
+template <bool kMx, int kTiles>
+__device__ __forceinline__ void load_tokens(Tokens<kMx, kTiles>& x, const uint8_t* const (&rows)[kTiles],
+                                            const bool (&has)[kTiles], int c, int group, int pieces) {
   constexpr int n = kMx ? 4 : 1;
-  TokenPiece<kMx> t;
+  const int p = c * 8 + group * 2;
+  const bool whole = c * 8 + 8 <= pieces;
 #pragma unroll
-  for (int i = 0; i < n; ++i) t.v[i] = u32x4{0, 0, 0, 0};
-  if (valid) {
-    const u32x4* p = reinterpret_cast<const u32x4*>(row) + static_cast<int64_t>(piece) * n;
+  for (int t = 0; t < kTiles; ++t) {
+    if (!has[t]) continue;
+    const u32x4* from = reinterpret_cast<const u32x4*>(rows[t]);
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < n; ++i) t.v[i] = p[i];
+      for (int i = 0; i < 2 * n; ++i) x.v[t][i / n][i % n] = from[p * n + i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * n; ++i) {
+        const u32x4 v = from[min(p + i / n, pieces - 1) * n + i % n];
+        x.v[t][i / n][i % n] = p + i / n < pieces ? v : u32x4{0, 0, 0, 0};
+      }
+    }
   }
-  return t;
 }
 
 template <bool kBf16>
@@ -233,25 +321,29 @@ __device__ __forceinline__ f32x4 product(u32x4 w, u32x4 x, f32x4 c) {
                                                   0);
 }
 
-// acc[n] += the products of a weight piece with kTiles tiles of tokens.
+// acc[n] += the products of a chunk with kTiles tiles of tokens.
 template <bool kMx, bool kBf16, int kTiles>
-__device__ __forceinline__ void multiply(const WeightPiece<kMx>& w, const TokenPiece<kMx> (&x)[kTiles],
-                                         f32x4 (&acc)[kTiles]) {
-  if constexpr (kMx) {
-    const float s = __uint_as_float(w.scale << 23);  // the conversion reads the exponent alone
+__device__ __forceinline__ void multiply(const Weights<kMx>& w, const Tokens<kMx, kTiles>& x, f32x4 (&acc)[kTiles]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      u32x4 wide;
-      wide[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w.v[i], s, 0));
-      wide[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w.v[i], s, 1));
-      wide[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w.v[i], s, 2));
-      wide[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w.v[i], s, 3));
+  for (int p = 0; p < 2; ++p) {
+    if constexpr (kMx) {
+      // the conversion reads the scale's exponent alone
+      const float s = __uint_as_float((p == 0 ? w.scale & 0xff : w.scale >> 8) << 23);
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n) acc[n] = product<kBf16>(wide, x[n].v[i], acc[n]);
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t v = w.v[p][i];
+        u32x4 wide;
+        wide[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, 0));
+        wide[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, 1));
+        wide[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, 2));
+        wide[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, 3));
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) acc[n] = product<kBf16>(wide, x.v[n][p][i], acc[n]);
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) acc[n] = product<kBf16>(w.v[p], x.v[n][p][0], acc[n]);
     }
-  } else {
-#pragma unroll
-    for (int n = 0; n < kTiles; ++n) acc[n] = product<kBf16>(w.v, x[n].v[0], acc[n]);
   }
 }
 
@@ -266,98 +358,89 @@ __device__ __forceinline__ void store_row4(uint8_t* p, f32x4 v) {
   }
 }
 
-// The first kernel's LDS, sized by the call (a few KiB for one token, so that
-// several workgroups share a CU).
-struct UpShared {
-  f32x4* part;        // [waves][2][tiles][64]: partial sums of a unit
-  int32_t* count;     // [E]: tokens of an expert, then the place of its next one
-  int32_t* wave_sum;  // [waves]
-  Routing routing;
-  int16_t* slot;      // [T k]: token * 16 + choice, by expert
-  int16_t* active;    // [E]: the experts that have tokens
-  int16_t* first;     // [E + 1]: of an active expert: its first place in `slot`
-};
-
-inline __host__ __device__ size_t up_shared_bytes(int slots, int E, int tiles) {
-  return sizeof(f32x4) * kUpWaves * 2 * tiles * 64 + 4 * (E + kUpWaves + slots) + 2 * (2 * slots + 2 * E + 1);
-}
-
-__device__ __forceinline__ UpShared carve(uint8_t* lds, int slots, int E, int tiles) {
-  UpShared s;
-  s.part = reinterpret_cast<f32x4*>(lds);
-  s.count = reinterpret_cast<int32_t*>(s.part + kUpWaves * 2 * tiles * 64);
-  s.wave_sum = s.count + E;
-  s.routing.weight = reinterpret_cast<float*>(s.wave_sum + kUpWaves);
-  s.routing.id = reinterpret_cast<int16_t*>(s.routing.weight + slots);
-  s.slot = s.routing.id + slots;
-  s.active = s.slot + slots;
-  s.first = s.active + E;
-  return s;
+// A wave's sums over chunks c0, c0 + step, ... below `end` of kParts rows of
+// weights at once. The next chunk is on its way while one is multiplied.
+template <bool kMx, bool kBf16, int kTiles, int kParts>
+__device__ __forceinline__ void sum_chunks(f32x4 (&acc)[kParts][kTiles], const uint8_t* const (&rows)[kParts],
+                                           const uint8_t* const (&scales)[kParts], const uint8_t* const (&x_rows)[kTiles],
+                                           const bool (&has)[kTiles], int c0, int end, int step, int pieces) {
+  const int group = threadIdx.x % 64 / 16;
+  Weights<kMx> w[2][kParts];
+  Tokens<kMx, kTiles> x[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int i = 0; i < (kMx ? 4 : 1); ++i) x[b].v[t][p][i] = u32x4{0, 0, 0, 0};
+  auto load = [&](int b, int c) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) load_weights<kMx>(w[b][i], rows[i], scales[i], c, group, pieces);
+    load_tokens<kMx, kTiles>(x[b], x_rows, has, c, group, pieces);
+  };
+  auto use = [&](int b) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) multiply<kMx, kBf16, kTiles>(w[b][i], x[b], acc[i]);
+  };
+  int c = c0;
+  if (c >= end) return;
+  load(0, c);
+  for (;; c += 2 * step) {
+    if (c + step < end) load(1, c + step);
+    use(0);
+    if (c + step >= end) return;
+    if (c + 2 * step < end) load(0, c + 2 * step);
+    use(1);
+    if (c + 2 * step >= end) return;
+  }
 }
 
 // One unit of the first kernel: 16 gate rows and the same 16 up rows of an
 // expert, for kTiles * 16 of its tokens from place `at` on. The waves share
 // the rows' length, chunk by chunk.
 template <bool kMx, bool kBf16, int kTiles>
-__device__ __forceinline__ void up_unit(const FewArgs& a, const UpShared& s, int expert, int tile, int at, int end) {
-  constexpr int kUnroll = kMx ? 2 : 4;
+__device__ __forceinline__ void up_unit(const FewArgs& a, const Plan& s, f32x4* part, int expert, int tile, int at,
+                                        int end) {
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int r = lane % 16, group = lane / 16;
   const int bytes = row_bytes<kMx>(a.H);
   const int pieces = bytes / 16;
-  const int chunks = (pieces + 3) / 4;
-  const int64_t row = static_cast<int64_t>(expert) * 2 * a.I + tile * kRows + r;
-  const uint8_t* g_row = a.gate_up + row * bytes;
-  const uint8_t* u_row = g_row + static_cast<int64_t>(a.I) * bytes;
   const int scale_bytes = 2 * ((a.H + 63) / 64);
-  const uint8_t* g_scale = a.gate_up_scales + (kMx ? row * scale_bytes : 0);
-  const uint8_t* u_scale = g_scale + (kMx ? static_cast<int64_t>(a.I) * scale_bytes : 0);
+  const int64_t row = static_cast<int64_t>(expert) * 2 * a.I + tile * kRows + r;
+  const uint8_t* rows[2] = {a.gate_up + row * bytes, a.gate_up + (row + a.I) * bytes};
+  const uint8_t* scales[2] = {a.gate_up_scales + row * scale_bytes, a.gate_up_scales + (row + a.I) * scale_bytes};
   const uint8_t* x_row[kTiles];
   bool has[kTiles];
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) {
     const int place = at + n * 16 + r;
     has[n] = place < end;
-    x_row[n] = a.x + (has[n] ? static_cast<int64_t>(s.slot[place] / 16) * a.H * 2 : 0);
+    x_row[n] = a.x + (has[n] ? static_cast<int64_t>(s.slot[place] / a.k) * a.H * 2 : 0);
   }
-  f32x4 g[kTiles], u[kTiles];
+  f32x4 acc[2][kTiles];
 #pragma unroll
-  for (int n = 0; n < kTiles; ++n) g[n] = u[n] = f32x4{0, 0, 0, 0};
-  for (int c0 = wave; c0 < chunks; c0 += kUpWaves * kUnroll) {
-    WeightPiece<kMx> wg[kUnroll], wu[kUnroll];
-    TokenPiece<kMx> x[kUnroll][kTiles];
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int piece = (c0 + i * kUpWaves) * 4 + group;
-      wg[i] = load_weight<kMx>(g_row, g_scale, piece, piece < pieces);
-      wu[i] = load_weight<kMx>(u_row, u_scale, piece, piece < pieces);
-#pragma unroll
-      for (int n = 0; n < kTiles; ++n) x[i][n] = load_token<kMx>(x_row[n], piece, has[n] && piece < pieces);
-    }
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      multiply<kMx, kBf16, kTiles>(wg[i], x[i], g);
-      multiply<kMx, kBf16, kTiles>(wu[i], x[i], u);
-    }
-  }
+  for (int n = 0; n < kTiles; ++n) acc[0][n] = acc[1][n] = f32x4{0, 0, 0, 0};
+  sum_chunks<kMx, kBf16, kTiles, 2>(acc, rows, scales, x_row, has, wave, (pieces + 7) / 8, kUpWaves, pieces);
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) {
-    s.part[((wave * 2 + 0) * kTiles + n) * 64 + lane] = g[n];
-    s.part[((wave * 2 + 1) * kTiles + n) * 64 + lane] = u[n];
+    part[((wave * 2 + 0) * kTiles + n) * 64 + lane] = acc[0][n];
+    part[((wave * 2 + 1) * kTiles + n) * 64 + lane] = acc[1][n];
   }
   __syncthreads();
   // a wave finishes a tile of tokens: a lane has four rows of one token
   for (int n = wave; n < kTiles; n += kUpWaves) {
-    f32x4 gs = s.part[n * 64 + lane], us = s.part[(kTiles + n) * 64 + lane];
+    f32x4 gs = part[n * 64 + lane], us = part[(kTiles + n) * 64 + lane];
 #pragma unroll
     for (int w = 1; w < kUpWaves; ++w) {
-      gs += s.part[(w * 2 * kTiles + n) * 64 + lane];
-      us += s.part[((w * 2 + 1) * kTiles + n) * 64 + lane];
+      gs += part[(w * 2 * kTiles + n) * 64 + lane];
+      us += part[((w * 2 + 1) * kTiles + n) * 64 + lane];
     }
     const int place = at + n * 16 + r;
     if (place < end) {
-      const int slot = s.slot[place] / 16 * a.k + s.slot[place] % 16;
-      const float p = s.routing.weight[slot];
+      const int slot = s.slot[place];
+      const float p = s.weight[slot];
       f32x4 h;
 #pragma unroll
       for (int i = 0; i < 4; ++i) h[i] = p * (gs[i] / (1.0f + __expf(-gs[i]))) * us[i];
@@ -367,199 +450,156 @@ __device__ __forceinline__ void up_unit(const FewArgs& a, const UpShared& s, int
   __syncthreads();
 }
 
-// kMaxTiles: tiles of 16 tokens that all tokens fill.
-template <bool kMx, bool kBf16, int kMaxTiles>
-__global__ __launch_bounds__(kUpWaves * 64) void few_up_kernel(FewArgs a) {
+template <bool kMx, bool kBf16, int kTiles>
+__global__ __launch_bounds__(kUpWaves * 64, UPB) void few_up_kernel(FewArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
-  const UpShared s = carve(lds, a.T * a.k, a.E, kMaxTiles);
-  const int tid = threadIdx.x;
   constexpr int kThreads = kUpWaves * 64;
-  for (int e = tid; e < a.E; e += kThreads) s.count[e] = 0;
-  find_routing<kUpWaves>(a, s.routing);
-  __syncthreads();
-  const int slots = a.T * a.k;
-  if (blockIdx.x == 0)
-    for (int i = tid; i < slots; i += kThreads) a.ws_ids[i] = s.routing.id[i];
-  for (int i = tid; i < slots; i += kThreads)
-    if (s.routing.id[i] >= 0) atomicAdd(&s.count[s.routing.id[i]], 1);
-  __syncthreads();
-  // the experts that have tokens, and where their tokens start
-  constexpr int kPer = kMaxExperts / kThreads;
-  uint32_t used = 0, tokens = 0;
-  for (int i = 0; i < kPer; ++i) {
-    const int e = tid * kPer + i;
-    const int c = e < a.E ? s.count[e] : 0;
-    used += c > 0;
-    tokens += c;
-  }
-  // both sums in one word: at most 1024 experts and 2048 slots
-  const uint32_t in = wave_scan_u32(used << 16 | tokens);
-  if (tid % 64 == 63) s.wave_sum[tid / 64] = static_cast<int>(in);
-  __syncthreads();
-  uint32_t before = in - (used << 16 | tokens), all = 0;
-  for (int w = 0; w < kUpWaves; ++w) {
-    if (w < tid / 64) before += s.wave_sum[w];
-    all += s.wave_sum[w];
-  }
-  int next = before >> 16, place = before & 0xffff;
-  for (int i = 0; i < kPer; ++i) {
-    const int e = tid * kPer + i;
-    const int c = e < a.E ? s.count[e] : 0;
-    if (c > 0) {
-      s.active[next] = static_cast<int16_t>(e);
-      s.first[next++] = static_cast<int16_t>(place);
-      s.count[e] = place;
-      place += c;
+  const int slots = a.T * a.k, tid = threadIdx.x, lane = tid % 64;
+  f32x4* part = reinterpret_cast<f32x4*>(lds);  // [waves][2][tiles][64]: partial sums of a unit
+  Plan s = carve(lds + up_part_bytes(kTiles), slots, a.E);
+  if (a.logits != nullptr && a.T <= kSelfRouted) {
+    for (int t = tid / 64; t < a.T; t += kUpWaves) {
+      int id;
+      float weight;
+      route_token(a, t, lane, &id, &weight);
+      if (lane < a.k) {
+        s.id[t * a.k + lane] = static_cast<int16_t>(id);
+        s.weight[t * a.k + lane] = weight;
+      }
+    }
+  } else if (a.logits != nullptr) {  // by few_route_kernel
+    for (int i = tid; i < slots; i += kThreads) {
+      s.id[i] = static_cast<int16_t>(a.ws_ids[i]);
+      s.weight[i] = a.ws_weight[i];
+    }
+  } else {
+    // An expert that a token names again counts at its first place, with the
+    // sum of the weights.
+    for (int i = tid; i < slots; i += kThreads) {
+      const int t = i / a.k, j = i - t * a.k;
+      const int id = a.ids[i];
+      float weight = a.weight[i];
+      bool keep = id >= 0 && id < a.E;
+      for (int n = 0; n < a.k; ++n) {
+        if (n == j || a.ids[t * a.k + n] != id) continue;
+        if (n < j)
+          keep = false;
+        else
+          weight += a.weight[t * a.k + n];
+      }
+      s.id[i] = static_cast<int16_t>(keep ? id : -1);
+      s.weight[i] = weight;
     }
   }
-  const int active = all >> 16;
-  if (tid == 0) s.first[active] = static_cast<int16_t>(all & 0xffff);
-  __syncthreads();
-  // the order within an expert does not matter: a token's sums are its own
-  for (int i = tid; i < slots; i += kThreads) {
-    const int e = s.routing.id[i];
-    if (e >= 0) s.slot[atomicAdd(&s.count[e], 1)] = static_cast<int16_t>(i / a.k * 16 + i % a.k);
-  }
-  __syncthreads();
+  make_plan<kUpWaves>(s, slots, a.E);
+  if (blockIdx.x == 0 && (a.logits == nullptr || a.T <= kSelfRouted))  // for the second kernel
+    for (int i = tid; i < slots; i += kThreads) a.ws_ids[i] = s.id[i];
 
   const int tiles = a.I / kRows;
-  const int units = active * tiles;
+  const int units = s.experts * tiles;
   for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int n = unit / tiles, tile = unit - n * tiles;
     const int expert = s.active[n], end = s.first[n + 1];
     for (int at = s.first[n]; at < end;) {
-      if (kMaxTiles == 1 || end - at <= 16) {
-        up_unit<kMx, kBf16, 1>(a, s, expert, tile, at, end);
+      if (kTiles == 1 || end - at <= 16) {
+        up_unit<kMx, kBf16, 1>(a, s, part, expert, tile, at, end);
         at += 16;
-      } else if (kMaxTiles == 2 || end - at <= 32) {
-        up_unit<kMx, kBf16, kMaxTiles < 2 ? 1 : 2>(a, s, expert, tile, at, end);
-        at += 32;
       } else {
-        up_unit<kMx, kBf16, kMaxTiles>(a, s, expert, tile, at, end);
-        at += 64;
+        up_unit<kMx, kBf16, kTiles>(a, s, part, expert, tile, at, end);
+        at += kTiles * 16;
       }
     }
   }
 }
 
 // The second kernel: a workgroup computes 16 rows of y for up to 64 tokens.
-// Its waves take the tokens' experts in turn, or parts of their rows when the
-// experts are few; a wave's sums cover all tokens, the ones that do not use an
-// expert entering as zeros.
+// Its waves take the experts in turn, or parts of their rows when the experts
+// are few, for 16 kTiles of the expert's tokens at a time, and add the results
+// to sums of their own in LDS: each in its fixed order, so that nothing depends
+// on timing.
 template <bool kMx, bool kBf16, int kTiles>
-__global__ __launch_bounds__(kDownWaves * 64) void few_down_kernel(FewArgs a) {
+__global__ __launch_bounds__(kDownWaves * 64, DNB) void few_down_kernel(FewArgs a) {
+  extern __shared__ __align__(16) uint8_t lds[];
   constexpr int kThreads = kDownWaves * 64;
-  constexpr int kUnroll = kMx ? 2 : 4;
-  __shared__ int16_t s_id[kDownTokens * static_cast<int>(kFewMaxTopK)];
-  __shared__ int32_t s_used[kMaxExperts];
-  __shared__ int16_t s_active[kMaxExperts];
-  __shared__ int32_t s_sum[kDownWaves];
-  __shared__ f32x4 s_part[kDownWaves][kTiles][64];
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   const int r = lane % 16, group = lane / 16;
-  const int t0 = blockIdx.y * kDownTokens, tokens = min(a.T - t0, kDownTokens);
-  for (int e = tid; e < a.E; e += kThreads) s_used[e] = 0;
-  __syncthreads();
-  for (int i = tid; i < tokens * a.k; i += kThreads) {
-    const int id = a.ws_ids[t0 * a.k + i];
-    s_id[i] = static_cast<int16_t>(id);
-    if (id >= 0) s_used[id] = 1;
-  }
-  __syncthreads();
-  constexpr int kPer = kMaxExperts / kThreads;
-  uint32_t used = 0;
-  for (int i = 0; i < kPer; ++i) {
-    const int e = tid * kPer + i;
-    used += e < a.E ? s_used[e] : 0;
-  }
-  const uint32_t in = wave_scan_u32(used);
-  if (lane == 63) s_sum[wave] = static_cast<int>(in);
-  __syncthreads();
-  int next = static_cast<int>(in - used), active = 0;
-  for (int w = 0; w < kDownWaves; ++w) {
-    if (w < wave) next += s_sum[w];
-    active += s_sum[w];
-  }
-  for (int i = 0; i < kPer; ++i) {
-    const int e = tid * kPer + i;
-    if (e < a.E && s_used[e]) s_active[next++] = static_cast<int16_t>(e);
-  }
-  __syncthreads();
+  const int t0 = blockIdx.y * kDownTokens, tokens = min(a.T - t0, kDownTokens), slots = tokens * a.k;
+  f32x4* sums = reinterpret_cast<f32x4*>(lds);  // [waves][tokens][4 groups]
+  f32x4* mine = sums + wave * tokens * 4;
+  Plan s = carve(lds + down_sum_bytes(tokens), slots, a.E);
+  for (int i = tid; i < slots; i += kThreads) s.id[i] = static_cast<int16_t>(a.ws_ids[t0 * a.k + i]);
+  for (int i = lane; i < tokens * 4; i += 64) mine[i] = f32x4{0, 0, 0, 0};
+  make_plan<kDownWaves>(s, slots, a.E);
 
   const int bytes = row_bytes<kMx>(a.I);
-  const int pieces = bytes / 16, chunks = (pieces + 3) / 4;
+  const int pieces = bytes / 16, chunks = (pieces + 7) / 8;
   const int scale_bytes = 2 * ((a.I + 63) / 64);
   const int row = blockIdx.x * kRows + r;
-  // parts of an expert's rows: enough for two a wave, of four chunks at least
-  const int parts = max(1, min((chunks + 3) / 4, (2 * kDownWaves + active - 1) / max(active, 1)));
-  const int part_chunks = (chunks + parts - 1) / parts;
-  f32x4 acc[kTiles];
-#pragma unroll
-  for (int n = 0; n < kTiles; ++n) acc[n] = f32x4{0, 0, 0, 0};
-  for (int unit = wave; unit < active * parts; unit += kDownWaves) {
+  // parts of an expert's rows: enough for two a wave, of two chunks at least
+  const int wanted = (2 * kDownWaves + s.experts - 1) / max(s.experts, 1);
+  const int part_chunks = max(2, (chunks + wanted - 1) / wanted);
+  const int parts = (chunks + part_chunks - 1) / part_chunks;
+  for (int unit = wave; unit < s.experts * parts; unit += kDownWaves) {
     const int which = unit / parts, part = unit - which * parts;
-    const int expert = s_active[which];
-    const uint8_t* w_row = a.down + (static_cast<int64_t>(expert) * a.H + row) * bytes;
-    const uint8_t* w_scale = a.down_scales + (kMx ? (static_cast<int64_t>(expert) * a.H + row) * scale_bytes : 0);
-    const uint8_t* h_row[kTiles];
-    bool has[kTiles];
+    const int expert = s.active[which];
+    const int64_t w_row = static_cast<int64_t>(expert) * a.H + row;
+    const uint8_t* rows[1] = {a.down + w_row * bytes};
+    const uint8_t* scales[1] = {a.down_scales + w_row * scale_bytes};
+    const int end = s.first[which + 1];
+    for (int at = s.first[which]; at < end; at += 16 * kTiles) {
+      const uint8_t* h_row[kTiles];
+      bool has[kTiles];
+      int token[kTiles];
 #pragma unroll
-    for (int n = 0; n < kTiles; ++n) {
-      const int t = n * 16 + r;
-      int choice = -1;
-      if (t < tokens)
-        for (int j = 0; j < a.k; ++j)
-          if (s_id[t * a.k + j] == expert) choice = j;
-      has[n] = choice >= 0;
-      h_row[n] = a.ws_h + (has[n] ? (static_cast<int64_t>(t0 + t) * a.k + choice) * a.I * 2 : 0);
-    }
-    const int end = min(chunks, (part + 1) * part_chunks);
-    for (int c0 = part * part_chunks; c0 < end; c0 += kUnroll) {
-      WeightPiece<kMx> w[kUnroll];
-      TokenPiece<kMx> h[kUnroll][kTiles];
-#pragma unroll
-      for (int i = 0; i < kUnroll; ++i) {
-        const int piece = (c0 + i) * 4 + group;
-        const bool valid = c0 + i < end && piece < pieces;
-        w[i] = load_weight<kMx>(w_row, w_scale, piece, valid);
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n) h[i][n] = load_token<kMx>(h_row[n], piece, has[n] && valid);
+      for (int n = 0; n < kTiles; ++n) {
+        const int place = at + n * 16 + r;
+        has[n] = place < end;
+        const int slot = has[n] ? s.slot[place] : 0;
+        token[n] = slot / a.k;
+        h_row[n] = a.ws_h + (static_cast<int64_t>(t0) * a.k + slot) * a.I * 2;
       }
+      f32x4 acc[1][kTiles];
 #pragma unroll
-      for (int i = 0; i < kUnroll; ++i) multiply<kMx, kBf16, kTiles>(w[i], h[i], acc);
+      for (int n = 0; n < kTiles; ++n) acc[0][n] = f32x4{0, 0, 0, 0};
+      sum_chunks<kMx, kBf16, kTiles, 1>(acc, rows, scales, h_row, has, part * part_chunks,
+                                        min(chunks, (part + 1) * part_chunks), 1, pieces);
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n)
+        if (has[n]) mine[token[n] * 4 + group] += acc[0][n];
     }
   }
-#pragma unroll
-  for (int n = 0; n < kTiles; ++n) s_part[wave][n][lane] = acc[n];
   __syncthreads();
-  for (int n = wave; n < kTiles; n += kDownWaves) {
-    const int t = n * 16 + r;
-    f32x4 sum = s_part[0][n][lane];
+  for (int i = tid; i < tokens * 4; i += kThreads) {
+    f32x4 sum = sums[i];
 #pragma unroll
-    for (int w = 1; w < kDownWaves; ++w) sum += s_part[w][n][lane];
-    if (t < tokens)
-      store_row4<kBf16>(a.y + (static_cast<int64_t>(t0 + t) * a.H + blockIdx.x * kRows + group * 4) * 2, sum);
+    for (int w = 1; w < kDownWaves; ++w) sum += sums[w * tokens * 4 + i];
+    store_row4<kBf16>(a.y + (static_cast<int64_t>(t0 + i / 4) * a.H + blockIdx.x * kRows + i % 4 * 4) * 2, sum);
   }
 }
 
 template <bool kMx, bool kBf16, int kTiles>
 mrr_status launch_few_tiles(const FewArgs& a, hipStream_t stream) {
-  const int64_t slots = static_cast<int64_t>(a.T) * a.k;
-  const int64_t units = (slots < a.E ? slots : a.E) * (a.I / kRows);
+  const int slots = a.T * a.k;
+  if (a.logits != nullptr && a.T > kSelfRouted) {
+    hipLaunchKernelGGL(few_route_kernel, dim3(a.T), dim3(64), 0, stream, a);
+    if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
+  }
+  const int64_t units = static_cast<int64_t>(slots < a.E ? slots : a.E) * (a.I / kRows);
   const int64_t most = 256 * 4;
   hipLaunchKernelGGL((few_up_kernel<kMx, kBf16, kTiles>), dim3(static_cast<unsigned>(units < most ? units : most)),
-                     dim3(kUpWaves * 64), up_shared_bytes(static_cast<int>(slots), a.E, kTiles), stream, a);
+                     dim3(kUpWaves * 64), up_part_bytes(kTiles) + plan_bytes(slots, a.E), stream, a);
   if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
+  const int tokens = a.T < kDownTokens ? a.T : kDownTokens;
   hipLaunchKernelGGL((few_down_kernel<kMx, kBf16, kTiles>), dim3(a.H / kRows, (a.T + kDownTokens - 1) / kDownTokens),
-                     dim3(kDownWaves * 64), 0, stream, a);
+                     dim3(kDownWaves * 64), down_sum_bytes(tokens) + plan_bytes(tokens * a.k, a.E), stream, a);
   return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
 }
 
 template <bool kMx, bool kBf16>
 mrr_status launch_few(const FewArgs& a, hipStream_t stream) {
-  return a.T <= 16   ? launch_few_tiles<kMx, kBf16, 1>(a, stream)
-         : a.T <= 32 ? launch_few_tiles<kMx, kBf16, 2>(a, stream)
-                     : launch_few_tiles<kMx, kBf16, 4>(a, stream);
+  // two tiles of tokens at once where an expert has more than one, on average
+  return a.T * a.k > 16 * a.E ? launch_few_tiles<kMx, kBf16, 2>(a, stream)
+                              : launch_few_tiles<kMx, kBf16, 1>(a, stream);
 }
 
 }  // namespace
@@ -582,6 +622,7 @@ extern "C" mrr_status mrr_few_tokens(const mrr_few_tokens_args* args, void* work
   a.down_scales = static_cast<const uint8_t*>(args->down_scales);
   a.y = static_cast<uint8_t*>(args->y);
   a.ws_ids = reinterpret_cast<int32_t*>(ws + l.ids);
+  a.ws_weight = reinterpret_cast<float*>(ws + l.weight);
   a.ws_h = ws + l.h;
   a.T = static_cast<int32_t>(args->T);
   a.H = static_cast<int32_t>(args->H);
