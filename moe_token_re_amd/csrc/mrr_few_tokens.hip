@@ -243,15 +243,17 @@ __device__ __forceinline__ void make_plan(Plan& p, int slots, int E) {
   __syncthreads();
 }
 
-// A chunk is 128 bytes of a weight row, a whole line of the caches. Lane group g
-// of four takes 32 bytes of it, two pieces of 16: 32 4-bit values each, whose two
-// scales are neighbours, or 8 values of 16 bits.
+// A chunk is 128 bytes of a weight row, a whole line of the caches, eight pieces
+// of 16 bytes: 32 4-bit values each, which share a scale, or 8 values of 16 bits.
+// Lane group g of four takes pieces g and 4 + g, so that what the wave reads of a
+// row at once is 64 bytes.
 template <bool kMx>
 struct Weights {
   u32x4 v[2];
-  uint32_t scale;  // of the two pieces, a byte each
+  uint32_t scale[2];
 };
 
+// The tokens' values that go with them, by products of 8 values a lane.
 template <bool kMx, int kTiles>
 struct Tokens {
   u32x4 v[kTiles][2][kMx ? 4 : 1];
@@ -260,55 +262,81 @@ struct Tokens {
 template <bool kMx>
 __device__ __forceinline__ int row_bytes(int n) { return kMx ? n / 2 : n * 2; }
 
-// Chunk c of a weight row of `pieces`; zeros past the row's end.
-template <bool kMx>
+// Chunk c of a weight row of `pieces`; if kTail, with zeros past the row's end.
+template <bool kMx, bool kTail>
 __device__ __forceinline__ void load_weights(Weights<kMx>& w, const uint8_t* row, const uint8_t* scales, int c,
                                              int group, int pieces) {
-  const int p = c * 8 + group * 2;
-  if (c * 8 + 8 <= pieces) {
-    const u32x4* from = reinterpret_cast<const u32x4*>(row) + p;
-    w.v[0] = from[0];
-    w.v[1] = from[1];
+  const u32x4* from = reinterpret_cast<const u32x4*>(row);
+  if constexpr (!kTail) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) w.v[p] = from[c * 8 + p * 4 + group];
     if constexpr (kMx) {
-      uint16_t s;
-      __builtin_memcpy(&s, scales + p, 2);
-      w.scale = s;
+      uint32_t s[2];
+      __builtin_memcpy(s, scales + c * 8, 8);
+#pragma unroll
+      for (int p = 0; p < 2; ++p) w.scale[p] = s[p];
     }
   } else {
-    const int p0 = min(p, pieces - 1), p1 = min(p + 1, pieces - 1);
-    const u32x4 v0 = reinterpret_cast<const u32x4*>(row)[p0], v1 = reinterpret_cast<const u32x4*>(row)[p1];
-    w.v[0] = p < pieces ? v0 : u32x4{0, 0, 0, 0};
-    w.v[1] = p + 1 < pieces ? v1 : u32x4{0, 0, 0, 0};
-    if constexpr (kMx) {
-      const uint32_t s0 = scales[p0], s1 = scales[p1];
-      w.scale = (p < pieces ? s0 : 127u) | (p + 1 < pieces ? s1 : 127u) << 8;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int piece = c * 8 + p * 4 + group;
+      const u32x4 v = from[min(piece, pieces - 1)];
+      w.v[p] = piece < pieces ? v : u32x4{0, 0, 0, 0};
+      if constexpr (kMx) {
+        const uint32_t s = scales[min(piece, pieces - 1)];
+        w.scale[p] = (piece < pieces ? s : 127u) << 8 * group;  // where a whole chunk's would be
+      }
     }
   }
 }
 
-// The tokens' values that go with it; zeros past the row's end. A lane without a
-// token keeps what it has: it computes a column that nobody reads.
-template <bool kMx, int kTiles>
-__device__ __forceinline__ void load_tokens(Tokens<kMx, kTiles>& x, const uint8_t* const (&rows)[kTiles],
-                                            const bool (&has)[kTiles], int c, int group, int pieces) {
-  constexpr int n = kMx ? 4 : 1;
-  const int p = c * 8 + group * 2;
-  const bool whole = c * 8 + 8 <= pieces;
+// Rows of tokens as a buffer: what lies outside reads as zeros, without traffic.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const uint8_t* p, uint32_t bytes) {
+  constexpr int kRaw = 0x00027000;  // 32-bit data, no swizzle, no stride
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, bytes, kRaw);
+}
+constexpr uint32_t kNoRow = 0x80000000u;  // an offset outside, with any within a row added to it
+
+// The same of the tokens' rows, given by their offsets (kNoRow: a lane without a
+// token). Of 16-bit values a piece of 4-bit weights takes 64 bytes; the lane
+// groups read them together, 16 bytes each, and spread_tokens() gives each group
+// its own piece.
+template <bool kMx, int kTiles, bool kTail>
+__device__ __forceinline__ void load_tokens(Tokens<kMx, kTiles>& x, __amdgpu_buffer_rsrc_t from,
+                                            const uint32_t (&rows)[kTiles], int c, int group, int pieces) {
 #pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    if (!has[t]) continue;
-    const u32x4* from = reinterpret_cast<const u32x4*>(rows[t]);
-    if (whole) {
+  for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-      for (int i = 0; i < 2 * n; ++i) x.v[t][i / n][i % n] = from[p * n + i];
-    } else {
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int i = 0; i < 2 * n; ++i) {
-        const u32x4 v = from[min(p + i / n, pieces - 1) * n + i % n];
-        x.v[t][i / n][i % n] = p + i / n < pieces ? v : u32x4{0, 0, 0, 0};
+      for (int i = 0; i < (kMx ? 4 : 1); ++i) {
+        const int piece = c * 8 + p * 4 + (kMx ? i : group);
+        uint32_t at = rows[t] + (kMx ? piece * 4 + group : piece) * 16;
+        if (kTail && piece >= pieces) at = kNoRow;
+        x.v[t][p][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, at, 0, 0));
       }
-    }
-  }
+}
+
+// Register i of lane group g and register g of lane group i change places: a
+// transposition of 4 x 4 by two rounds of swaps between groups.
+template <int kTiles>
+__device__ __forceinline__ void spread_tokens(Tokens<true, kTiles>& x) {
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) {
+        u32x4* v = x.v[t][p];
+        const auto a = __builtin_amdgcn_permlane16_swap(v[0][d], v[1][d], false, false);
+        const auto b = __builtin_amdgcn_permlane16_swap(v[2][d], v[3][d], false, false);
+        const auto e = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+        const auto f = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+        v[0][d] = e[0];
+        v[1][d] = f[0];
+        v[2][d] = e[1];
+        v[3][d] = f[1];
+      }
 }
 
 template <bool kBf16>
@@ -328,7 +356,7 @@ __device__ __forceinline__ void multiply(const Weights<kMx>& w, const Tokens<kMx
   for (int p = 0; p < 2; ++p) {
     if constexpr (kMx) {
       // the conversion reads the scale's exponent alone
-      const float s = __uint_as_float((p == 0 ? w.scale & 0xff : w.scale >> 8) << 23);
+      const float s = __uint_as_float((w.scale[p] >> 8 * (threadIdx.x % 64 / 16) & 0xff) << 23);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const uint32_t v = w.v[p][i];
@@ -359,41 +387,48 @@ __device__ __forceinline__ void store_row4(uint8_t* p, f32x4 v) {
 }
 
 // A wave's sums over chunks c0, c0 + step, ... below `end` of kParts rows of
-// weights at once. The next chunk is on its way while one is multiplied.
+// weights at once. The next chunk is on its way while one is multiplied; there is
+// no branch between a load and its use, so that the wait for one does not wait
+// for the next (the last chunk is loaded once more, from the cache).
 template <bool kMx, bool kBf16, int kTiles, int kParts>
 __device__ __forceinline__ void sum_chunks(f32x4 (&acc)[kParts][kTiles], const uint8_t* const (&rows)[kParts],
-                                           const uint8_t* const (&scales)[kParts], const uint8_t* const (&x_rows)[kTiles],
-                                           const bool (&has)[kTiles], int c0, int end, int step, int pieces) {
+                                           const uint8_t* const (&scales)[kParts], __amdgpu_buffer_rsrc_t x_from,
+                                           const uint32_t (&x_rows)[kTiles], int c0, int end, int step, int pieces) {
   const int group = threadIdx.x % 64 / 16;
   Weights<kMx> w[2][kParts];
   Tokens<kMx, kTiles> x[2];
+  auto load = [&](int b, int c, auto tail) {
+    constexpr bool kTail = decltype(tail)::value;
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
-#pragma unroll
-    for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int i = 0; i < (kMx ? 4 : 1); ++i) x[b].v[t][p][i] = u32x4{0, 0, 0, 0};
-  auto load = [&](int b, int c) {
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) load_weights<kMx>(w[b][i], rows[i], scales[i], c, group, pieces);
-    load_tokens<kMx, kTiles>(x[b], x_rows, has, c, group, pieces);
+    for (int i = 0; i < kParts; ++i) load_weights<kMx, kTail>(w[b][i], rows[i], scales[i], c, group, pieces);
+    load_tokens<kMx, kTiles, kTail>(x[b], x_from, x_rows, c, group, pieces);
+    __builtin_amdgcn_sched_barrier(0);  // or they sink to their use
   };
   auto use = [&](int b) {
+    if constexpr (kMx) spread_tokens<kTiles>(x[b]);
 #pragma unroll
     for (int i = 0; i < kParts; ++i) multiply<kMx, kBf16, kTiles>(w[b][i], x[b], acc[i]);
+    __builtin_amdgcn_sched_barrier(0);
   };
-  int c = c0;
-  if (c >= end) return;
-  load(0, c);
-  for (;; c += 2 * step) {
-    if (c + step < end) load(1, c + step);
+  const int whole = min(end, pieces / 8);
+  int n = c0 < whole ? (whole - c0 + step - 1) / step : 0, c = c0;
+  if (n > 0) {
+    load(0, c, std::false_type{});
+    for (;;) {
+      c += n > 1 ? step : 0;
+      load(1, c, std::false_type{});
+      use(0);
+      if (--n == 0) break;
+      c += n > 1 ? step : 0;
+      load(0, c, std::false_type{});
+      use(1);
+      if (--n == 0) break;
+    }
+  }
+  const int last = pieces / 8;  // a chunk that the row ends in
+  if (pieces % 8 != 0 && c0 <= last && last < end && (last - c0) % step == 0) {
+    load(0, last, std::true_type{});
     use(0);
-    if (c + step >= end) return;
-    if (c + 2 * step < end) load(0, c + 2 * step);
-    use(1);
-    if (c + 2 * step >= end) return;
   }
 }
 
@@ -411,18 +446,17 @@ __device__ __forceinline__ void up_unit(const FewArgs& a, const Plan& s, f32x4* 
   const int64_t row = static_cast<int64_t>(expert) * 2 * a.I + tile * kRows + r;
   const uint8_t* rows[2] = {a.gate_up + row * bytes, a.gate_up + (row + a.I) * bytes};
   const uint8_t* scales[2] = {a.gate_up_scales + row * scale_bytes, a.gate_up_scales + (row + a.I) * scale_bytes};
-  const uint8_t* x_row[kTiles];
-  bool has[kTiles];
+  uint32_t x_row[kTiles];
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) {
     const int place = at + n * 16 + r;
-    has[n] = place < end;
-    x_row[n] = a.x + (has[n] ? static_cast<int64_t>(s.slot[place] / a.k) * a.H * 2 : 0);
+    x_row[n] = place < end ? static_cast<uint32_t>(s.slot[place] / a.k) * a.H * 2 : kNoRow;
   }
   f32x4 acc[2][kTiles];
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) acc[0][n] = acc[1][n] = f32x4{0, 0, 0, 0};
-  sum_chunks<kMx, kBf16, kTiles, 2>(acc, rows, scales, x_row, has, wave, (pieces + 7) / 8, kUpWaves, pieces);
+  sum_chunks<kMx, kBf16, kTiles, 2>(acc, rows, scales, rows_buffer(a.x, a.T * a.H * 2), x_row, wave,
+                                      (pieces + 7) / 8, kUpWaves, pieces);
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) {
     part[((wave * 2 + 0) * kTiles + n) * 64 + lane] = acc[0][n];
@@ -547,7 +581,7 @@ __global__ __launch_bounds__(kDownWaves * 64, DNB) void few_down_kernel(FewArgs 
     const uint8_t* scales[1] = {a.down_scales + w_row * scale_bytes};
     const int end = s.first[which + 1];
     for (int at = s.first[which]; at < end; at += 16 * kTiles) {
-      const uint8_t* h_row[kTiles];
+      uint32_t h_row[kTiles];
       bool has[kTiles];
       int token[kTiles];
 #pragma unroll
@@ -556,12 +590,13 @@ __global__ __launch_bounds__(kDownWaves * 64, DNB) void few_down_kernel(FewArgs 
         has[n] = place < end;
         const int slot = has[n] ? s.slot[place] : 0;
         token[n] = slot / a.k;
-        h_row[n] = a.ws_h + (static_cast<int64_t>(t0) * a.k + slot) * a.I * 2;
+        h_row[n] = has[n] ? static_cast<uint32_t>(t0 * a.k + slot) * a.I * 2 : kNoRow;
       }
       f32x4 acc[1][kTiles];
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) acc[0][n] = f32x4{0, 0, 0, 0};
-      sum_chunks<kMx, kBf16, kTiles, 1>(acc, rows, scales, h_row, has, part * part_chunks,
+      sum_chunks<kMx, kBf16, kTiles, 1>(acc, rows, scales, rows_buffer(a.ws_h, a.T * a.k * a.I * 2), h_row,
+                                        part * part_chunks,
                                         min(chunks, (part + 1) * part_chunks), 1, pieces);
 #pragma unroll
       for (int n = 0; n < kTiles; ++n)
