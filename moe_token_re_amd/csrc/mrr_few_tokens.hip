@@ -243,20 +243,23 @@ __device__ __forceinline__ void make_plan(Plan& p, int slots, int E) {
   __syncthreads();
 }
 
-// A chunk is 128 bytes of a weight row, a whole line of the caches, eight pieces
-// of 16 bytes: 32 4-bit values each, which share a scale, or 8 values of 16 bits.
-// Lane group g of four takes pieces g and 4 + g, so that what the wave reads of a
-// row at once is 64 bytes.
+// A chunk is 128 bytes of a weight row, a whole line of the caches: eight pieces
+// of 16 bytes, 32 4-bit values each, which share a scale, or 8 values of 16 bits.
+// The matrix instruction wants lane 16 g + r to have row r. Read like that, no
+// two neighbouring lanes would read neighbouring bytes, and each lane's 16 bytes
+// would take a cycle of the address unit of their own. So lane 4 r + g reads piece
+// g or 4 + g of row r, and sort_lanes() moves it to lane 16 g + r afterwards
+// (64 tokens of 4-bit experts, first kernel: 107 us like that).
 template <bool kMx>
 struct Weights {
   u32x4 v[2];
-  uint32_t scale[2];
+  uint32_t scale[2];  // of the row's eight pieces
 };
 
-// The tokens' values that go with them, by products of 8 values a lane.
+// The tokens' values that go with a chunk, by products of 8 values a lane.
 template <bool kMx, int kTiles>
 struct Tokens {
-  u32x4 v[kTiles][2][kMx ? 4 : 1];
+  u32x4 v[kTiles][kMx ? 8 : 2];
 };
 
 template <bool kMx>
@@ -265,26 +268,23 @@ __device__ __forceinline__ int row_bytes(int n) { return kMx ? n / 2 : n * 2; }
 // Chunk c of a weight row of `pieces`; if kTail, with zeros past the row's end.
 template <bool kMx, bool kTail>
 __device__ __forceinline__ void load_weights(Weights<kMx>& w, const uint8_t* row, const uint8_t* scales, int c,
-                                             int group, int pieces) {
+                                             int pieces) {
   const u32x4* from = reinterpret_cast<const u32x4*>(row);
-  if constexpr (!kTail) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p) w.v[p] = from[c * 8 + p * 4 + group];
-    if constexpr (kMx) {
-      uint32_t s[2];
-      __builtin_memcpy(s, scales + c * 8, 8);
+  for (int p = 0; p < 2; ++p) {
+    const int piece = c * 8 + p * 4 + threadIdx.x % 4;
+    const u32x4 v = from[kTail ? min(piece, pieces - 1) : piece];
+    w.v[p] = !kTail || piece < pieces ? v : u32x4{0, 0, 0, 0};
+  }
+  if constexpr (kMx) {
+    if constexpr (!kTail) {
+      __builtin_memcpy(w.scale, scales + c * 8, 8);
+    } else {
+      w.scale[0] = w.scale[1] = 0x7f7f7f7fu;
 #pragma unroll
-      for (int p = 0; p < 2; ++p) w.scale[p] = s[p];
-    }
-  } else {
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const int piece = c * 8 + p * 4 + group;
-      const u32x4 v = from[min(piece, pieces - 1)];
-      w.v[p] = piece < pieces ? v : u32x4{0, 0, 0, 0};
-      if constexpr (kMx) {
-        const uint32_t s = scales[min(piece, pieces - 1)];
-        w.scale[p] = (piece < pieces ? s : 127u) << 8 * group;  // where a whole chunk's would be
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t s = scales[min(c * 8 + i, pieces - 1)], at = 8 * (i % 4);
+        if (c * 8 + i < pieces) w.scale[i / 4] = (w.scale[i / 4] & ~(0xffu << at)) | s << at;
       }
     }
   }
@@ -297,46 +297,40 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const uint8_t* p, 
 }
 constexpr uint32_t kNoRow = 0x80000000u;  // an offset outside, with any within a row added to it
 
-// The same of the tokens' rows, given by their offsets (kNoRow: a lane without a
-// token). Of 16-bit values a piece of 4-bit weights takes 64 bytes; the lane
-// groups read them together, 16 bytes each, and spread_tokens() gives each group
-// its own piece.
+// The same of the tokens' rows, given by their offsets (kNoRow: none). Of 16-bit
+// values a piece of 4-bit weights takes 64 bytes: four lanes' worth.
 template <bool kMx, int kTiles, bool kTail>
 __device__ __forceinline__ void load_tokens(Tokens<kMx, kTiles>& x, __amdgpu_buffer_rsrc_t from,
-                                            const uint32_t (&rows)[kTiles], int c, int group, int pieces) {
+                                            const uint32_t (&rows)[kTiles], int c, int pieces) {
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int i = 0; i < (kMx ? 4 : 1); ++i) {
-        const int piece = c * 8 + p * 4 + (kMx ? i : group);
-        uint32_t at = rows[t] + (kMx ? piece * 4 + group : piece) * 16;
-        if (kTail && piece >= pieces) at = kNoRow;
-        x.v[t][p][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, at, 0, 0));
-      }
+    for (int i = 0; i < (kMx ? 8 : 2); ++i) {
+      const int unit = c * (kMx ? 32 : 8) + i * 4 + threadIdx.x % 4;
+      uint32_t at = rows[t] + unit * 16;
+      if (kTail && unit >= pieces * (kMx ? 4 : 1)) at = kNoRow;
+      x.v[t][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, at, 0, 0));
+    }
 }
 
-// Register i of lane group g and register g of lane group i change places: a
+// From lane 4 r + g to lane 16 g + r.
+__device__ __forceinline__ uint32_t sort_lanes(uint32_t v) {
+  const int lane = threadIdx.x % 64;
+  return static_cast<uint32_t>(
+      __builtin_amdgcn_ds_bpermute((lane % 16 * 4 + lane / 16) * 4, static_cast<int>(v)));
+}
+__device__ __forceinline__ u32x4 sort_lanes(u32x4 v) {
+  return u32x4{sort_lanes(v[0]), sort_lanes(v[1]), sort_lanes(v[2]), sort_lanes(v[3])};
+}
+
+// Dword i of lane group g and dword g of lane group i change places: a
 // transposition of 4 x 4 by two rounds of swaps between groups.
-template <int kTiles>
-__device__ __forceinline__ void spread_tokens(Tokens<true, kTiles>& x) {
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t)
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        u32x4* v = x.v[t][p];
-        const auto a = __builtin_amdgcn_permlane16_swap(v[0][d], v[1][d], false, false);
-        const auto b = __builtin_amdgcn_permlane16_swap(v[2][d], v[3][d], false, false);
-        const auto e = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
-        const auto f = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
-        v[0][d] = e[0];
-        v[1][d] = f[0];
-        v[2][d] = e[1];
-        v[3][d] = f[1];
-      }
+__device__ __forceinline__ u32x4 transpose_groups(u32x4 v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(v[0], v[1], false, false);
+  const auto b = __builtin_amdgcn_permlane16_swap(v[2], v[3], false, false);
+  const auto e = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+  const auto f = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+  return u32x4{e[0], f[0], e[1], f[1]};
 }
 
 template <bool kBf16>
@@ -349,28 +343,36 @@ __device__ __forceinline__ f32x4 product(u32x4 w, u32x4 x, f32x4 c) {
                                                   0);
 }
 
-// acc[n] += the products of a chunk with kTiles tiles of tokens.
+// acc[n] += the products of a chunk with kTiles tiles of tokens, whose lanes are
+// sorted already. Of 16-bit values lane group g of a tokens' register has those of
+// dword g of a piece of 4-bit weights, so the weights' dwords are brought there.
 template <bool kMx, bool kBf16, int kTiles>
 __device__ __forceinline__ void multiply(const Weights<kMx>& w, const Tokens<kMx, kTiles>& x, f32x4 (&acc)[kTiles]) {
+  uint32_t scale[2];
+  if constexpr (kMx) {
+    scale[0] = sort_lanes(w.scale[0]);
+    scale[1] = sort_lanes(w.scale[1]);
+  }
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
+    u32x4 v = sort_lanes(w.v[p]);
     if constexpr (kMx) {
-      // the conversion reads the scale's exponent alone
-      const float s = __uint_as_float((w.scale[p] >> 8 * (threadIdx.x % 64 / 16) & 0xff) << 23);
+      v = transpose_groups(v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t v = w.v[p][i];
+        // the conversion reads the scale's exponent alone
+        const float s = __uint_as_float((scale[p] >> 8 * i & 0xff) << 23);
         u32x4 wide;
-        wide[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, 0));
-        wide[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, 1));
-        wide[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, 2));
-        wide[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v, s, 3));
+        wide[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[i], s, 0));
+        wide[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[i], s, 1));
+        wide[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[i], s, 2));
+        wide[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(v[i], s, 3));
 #pragma unroll
-        for (int n = 0; n < kTiles; ++n) acc[n] = product<kBf16>(wide, x.v[n][p][i], acc[n]);
+        for (int n = 0; n < kTiles; ++n) acc[n] = product<kBf16>(wide, x.v[n][p * 4 + i], acc[n]);
       }
     } else {
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n) acc[n] = product<kBf16>(w.v[p], x.v[n][p][0], acc[n]);
+      for (int n = 0; n < kTiles; ++n) acc[n] = product<kBf16>(v, x.v[n][p], acc[n]);
     }
   }
 }
@@ -394,18 +396,20 @@ template <bool kMx, bool kBf16, int kTiles, int kParts>
 __device__ __forceinline__ void sum_chunks(f32x4 (&acc)[kParts][kTiles], const uint8_t* const (&rows)[kParts],
                                            const uint8_t* const (&scales)[kParts], __amdgpu_buffer_rsrc_t x_from,
                                            const uint32_t (&x_rows)[kTiles], int c0, int end, int step, int pieces) {
-  const int group = threadIdx.x % 64 / 16;
   Weights<kMx> w[2][kParts];
   Tokens<kMx, kTiles> x[2];
   auto load = [&](int b, int c, auto tail) {
     constexpr bool kTail = decltype(tail)::value;
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) load_weights<kMx, kTail>(w[b][i], rows[i], scales[i], c, group, pieces);
-    load_tokens<kMx, kTiles, kTail>(x[b], x_from, x_rows, c, group, pieces);
+    for (int i = 0; i < kParts; ++i) load_weights<kMx, kTail>(w[b][i], rows[i], scales[i], c, pieces);
+    load_tokens<kMx, kTiles, kTail>(x[b], x_from, x_rows, c, pieces);
     __builtin_amdgcn_sched_barrier(0);  // or they sink to their use
   };
   auto use = [&](int b) {
-    if constexpr (kMx) spread_tokens<kTiles>(x[b]);
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int i = 0; i < (kMx ? 8 : 2); ++i) x[b].v[t][i] = sort_lanes(x[b].v[t][i]);
 #pragma unroll
     for (int i = 0; i < kParts; ++i) multiply<kMx, kBf16, kTiles>(w[b][i], x[b], acc[i]);
     __builtin_amdgcn_sched_barrier(0);
@@ -443,13 +447,13 @@ __device__ __forceinline__ void up_unit(const FewArgs& a, const Plan& s, f32x4* 
   const int bytes = row_bytes<kMx>(a.H);
   const int pieces = bytes / 16;
   const int scale_bytes = 2 * ((a.H + 63) / 64);
-  const int64_t row = static_cast<int64_t>(expert) * 2 * a.I + tile * kRows + r;
+  const int64_t row = static_cast<int64_t>(expert) * 2 * a.I + tile * kRows + lane / 4;  // as the loads have it
   const uint8_t* rows[2] = {a.gate_up + row * bytes, a.gate_up + (row + a.I) * bytes};
   const uint8_t* scales[2] = {a.gate_up_scales + row * scale_bytes, a.gate_up_scales + (row + a.I) * scale_bytes};
   uint32_t x_row[kTiles];
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) {
-    const int place = at + n * 16 + r;
+    const int place = at + n * 16 + lane / 4;
     x_row[n] = place < end ? static_cast<uint32_t>(s.slot[place] / a.k) * a.H * 2 : kNoRow;
   }
   f32x4 acc[2][kTiles];
@@ -568,7 +572,7 @@ __global__ __launch_bounds__(kDownWaves * 64, DNB) void few_down_kernel(FewArgs 
   const int bytes = row_bytes<kMx>(a.I);
   const int pieces = bytes / 16, chunks = (pieces + 7) / 8;
   const int scale_bytes = 2 * ((a.I + 63) / 64);
-  const int row = blockIdx.x * kRows + r;
+  const int row = blockIdx.x * kRows + lane / 4;  // as the loads have it
   // parts of an expert's rows: enough for two a wave, of two chunks at least
   const int wanted = (2 * kDownWaves + s.experts - 1) / max(s.experts, 1);
   const int part_chunks = max(2, (chunks + wanted - 1) / wanted);
@@ -586,11 +590,10 @@ __global__ __launch_bounds__(kDownWaves * 64, DNB) void few_down_kernel(FewArgs 
       int token[kTiles];
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
-        const int place = at + n * 16 + r;
+        const int place = at + n * 16 + r, loads = at + n * 16 + lane / 4;
         has[n] = place < end;
-        const int slot = has[n] ? s.slot[place] : 0;
-        token[n] = slot / a.k;
-        h_row[n] = has[n] ? static_cast<uint32_t>(t0 * a.k + slot) * a.I * 2 : kNoRow;
+        token[n] = has[n] ? s.slot[place] / a.k : 0;
+        h_row[n] = loads < end ? static_cast<uint32_t>(t0 * a.k + s.slot[loads]) * a.I * 2 : kNoRow;
       }
       f32x4 acc[1][kTiles];
 #pragma unroll
