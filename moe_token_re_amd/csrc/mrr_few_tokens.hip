@@ -25,12 +25,7 @@ using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
 
 constexpr int kMaxExperts = static_cast<int>(kFewMaxExperts);
-#ifndef UPB
-#define UPB 2
-#define DNB 2
-#endif
 constexpr int kUpWaves = 4;       // first kernel: they share a unit's rows, each a part of their length
-constexpr int kDownWaves = 8;     // second kernel: each takes experts, or parts of them
 constexpr int kRows = 16;         // weight rows of a fragment
 constexpr int kDownTokens = 64;   // tokens of a workgroup of the second kernel
 constexpr int kSelfRouted = 4;    // so many tokens, a wave each, the first kernel routes itself
@@ -53,7 +48,7 @@ struct FewArgs {
 };
 
 inline __host__ __device__ size_t up_part_bytes(int tiles) { return sizeof(f32x4) * kUpWaves * 2 * tiles * 64; }
-inline __host__ __device__ size_t down_sum_bytes(int tokens) { return sizeof(f32x4) * kDownWaves * tokens * 4; }
+inline __host__ __device__ size_t down_sum_bytes(int tokens, int waves) { return sizeof(f32x4) * waves * tokens * 4; }
 
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   constexpr int kRowShr1 = 0x111, kRowShr2 = 0x112, kRowShr4 = 0x114, kRowShr8 = 0x118;
@@ -298,15 +293,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const uint8_t* p, 
 constexpr uint32_t kNoRow = 0x80000000u;  // an offset outside, with any within a row added to it
 
 // The same of the tokens' rows, given by their offsets (kNoRow: none). Of 16-bit
-// values a piece of 4-bit weights takes 64 bytes: four lanes' worth.
+// values a piece of 4-bit weights takes 64 bytes: four lanes' worth. Of one token
+// four lanes read, in whichever order: `group` is the lane's place in a row.
 template <bool kMx, int kTiles, bool kTail>
 __device__ __forceinline__ void load_tokens(Tokens<kMx, kTiles>& x, __amdgpu_buffer_rsrc_t from,
-                                            const uint32_t (&rows)[kTiles], int c, int pieces) {
+                                            const uint32_t (&rows)[kTiles], int c, int group, int pieces) {
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
     for (int i = 0; i < (kMx ? 8 : 2); ++i) {
-      const int unit = c * (kMx ? 32 : 8) + i * 4 + threadIdx.x % 4;
+      const int unit = c * (kMx ? 32 : 8) + i * 4 + group;
       uint32_t at = rows[t] + unit * 16;
       if (kTail && unit >= pieces * (kMx ? 4 : 1)) at = kNoRow;
       x.v[t][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, at, 0, 0));
@@ -391,25 +387,29 @@ __device__ __forceinline__ void store_row4(uint8_t* p, f32x4 v) {
 // A wave's sums over chunks c0, c0 + step, ... below `end` of kParts rows of
 // weights at once. The next chunk is on its way while one is multiplied; there is
 // no branch between a load and its use, so that the wait for one does not wait
-// for the next (the last chunk is loaded once more, from the cache).
-template <bool kMx, bool kBf16, int kTiles, int kParts>
+// for the next (the last chunk is loaded once more, from the cache). kSort: the
+// tokens are read by neighbouring lanes too; a few tokens cost less as they are.
+template <bool kMx, bool kBf16, int kTiles, bool kSort, int kParts>
 __device__ __forceinline__ void sum_chunks(f32x4 (&acc)[kParts][kTiles], const uint8_t* const (&rows)[kParts],
                                            const uint8_t* const (&scales)[kParts], __amdgpu_buffer_rsrc_t x_from,
                                            const uint32_t (&x_rows)[kTiles], int c0, int end, int step, int pieces) {
+  const int group = kSort ? threadIdx.x % 4 : threadIdx.x % 64 / 16;
   Weights<kMx> w[2][kParts];
   Tokens<kMx, kTiles> x[2];
   auto load = [&](int b, int c, auto tail) {
     constexpr bool kTail = decltype(tail)::value;
 #pragma unroll
     for (int i = 0; i < kParts; ++i) load_weights<kMx, kTail>(w[b][i], rows[i], scales[i], c, pieces);
-    load_tokens<kMx, kTiles, kTail>(x[b], x_from, x_rows, c, pieces);
+    load_tokens<kMx, kTiles, kTail>(x[b], x_from, x_rows, c, group, pieces);
     __builtin_amdgcn_sched_barrier(0);  // or they sink to their use
   };
   auto use = [&](int b) {
+    if constexpr (kSort) {
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
+      for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-      for (int i = 0; i < (kMx ? 8 : 2); ++i) x[b].v[t][i] = sort_lanes(x[b].v[t][i]);
+        for (int i = 0; i < (kMx ? 8 : 2); ++i) x[b].v[t][i] = sort_lanes(x[b].v[t][i]);
+    }
 #pragma unroll
     for (int i = 0; i < kParts; ++i) multiply<kMx, kBf16, kTiles>(w[b][i], x[b], acc[i]);
     __builtin_amdgcn_sched_barrier(0);
@@ -439,7 +439,7 @@ __device__ __forceinline__ void sum_chunks(f32x4 (&acc)[kParts][kTiles], const u
 // One unit of the first kernel: 16 gate rows and the same 16 up rows of an
 // expert, for kTiles * 16 of its tokens from place `at` on. The waves share
 // the rows' length, chunk by chunk.
-template <bool kMx, bool kBf16, int kTiles>
+template <bool kMx, bool kBf16, int kTiles, bool kSort>
 __device__ __forceinline__ void up_unit(const FewArgs& a, const Plan& s, f32x4* part, int expert, int tile, int at,
                                         int end) {
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
@@ -453,13 +453,13 @@ __device__ __forceinline__ void up_unit(const FewArgs& a, const Plan& s, f32x4* 
   uint32_t x_row[kTiles];
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) {
-    const int place = at + n * 16 + lane / 4;
+    const int place = at + n * 16 + (kSort ? lane / 4 : r);
     x_row[n] = place < end ? static_cast<uint32_t>(s.slot[place] / a.k) * a.H * 2 : kNoRow;
   }
   f32x4 acc[2][kTiles];
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) acc[0][n] = acc[1][n] = f32x4{0, 0, 0, 0};
-  sum_chunks<kMx, kBf16, kTiles, 2>(acc, rows, scales, rows_buffer(a.x, a.T * a.H * 2), x_row, wave,
+  sum_chunks<kMx, kBf16, kTiles, kSort, 2>(acc, rows, scales, rows_buffer(a.x, a.T * a.H * 2), x_row, wave,
                                       (pieces + 7) / 8, kUpWaves, pieces);
 #pragma unroll
   for (int n = 0; n < kTiles; ++n) {
@@ -488,8 +488,8 @@ __device__ __forceinline__ void up_unit(const FewArgs& a, const Plan& s, f32x4* 
   __syncthreads();
 }
 
-template <bool kMx, bool kBf16, int kTiles>
-__global__ __launch_bounds__(kUpWaves * 64, UPB) void few_up_kernel(FewArgs a) {
+template <bool kMx, bool kBf16, int kTiles, bool kSort>
+__global__ __launch_bounds__(kUpWaves * 64, 2) void few_up_kernel(FewArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int kThreads = kUpWaves * 64;
   const int slots = a.T * a.k, tid = threadIdx.x, lane = tid % 64;
@@ -540,10 +540,10 @@ __global__ __launch_bounds__(kUpWaves * 64, UPB) void few_up_kernel(FewArgs a) {
     const int expert = s.active[n], end = s.first[n + 1];
     for (int at = s.first[n]; at < end;) {
       if (kTiles == 1 || end - at <= 16) {
-        up_unit<kMx, kBf16, 1>(a, s, part, expert, tile, at, end);
+        up_unit<kMx, kBf16, 1, kSort>(a, s, part, expert, tile, at, end);
         at += 16;
       } else {
-        up_unit<kMx, kBf16, kTiles>(a, s, part, expert, tile, at, end);
+        up_unit<kMx, kBf16, kTiles, kSort>(a, s, part, expert, tile, at, end);
         at += kTiles * 16;
       }
     }
@@ -555,29 +555,29 @@ __global__ __launch_bounds__(kUpWaves * 64, UPB) void few_up_kernel(FewArgs a) {
 // are few, for 16 kTiles of the expert's tokens at a time, and add the results
 // to sums of their own in LDS: each in its fixed order, so that nothing depends
 // on timing.
-template <bool kMx, bool kBf16, int kTiles>
-__global__ __launch_bounds__(kDownWaves * 64, DNB) void few_down_kernel(FewArgs a) {
+template <bool kMx, bool kBf16, int kTiles, bool kSort, int kWaves>
+__global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
-  constexpr int kThreads = kDownWaves * 64;
+  constexpr int kThreads = kWaves * 64;
   const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
   const int r = lane % 16, group = lane / 16;
   const int t0 = blockIdx.y * kDownTokens, tokens = min(a.T - t0, kDownTokens), slots = tokens * a.k;
   f32x4* sums = reinterpret_cast<f32x4*>(lds);  // [waves][tokens][4 groups]
   f32x4* mine = sums + wave * tokens * 4;
-  Plan s = carve(lds + down_sum_bytes(tokens), slots, a.E);
+  Plan s = carve(lds + down_sum_bytes(tokens, kWaves), slots, a.E);
   for (int i = tid; i < slots; i += kThreads) s.id[i] = static_cast<int16_t>(a.ws_ids[t0 * a.k + i]);
   for (int i = lane; i < tokens * 4; i += 64) mine[i] = f32x4{0, 0, 0, 0};
-  make_plan<kDownWaves>(s, slots, a.E);
+  make_plan<kWaves>(s, slots, a.E);
 
   const int bytes = row_bytes<kMx>(a.I);
   const int pieces = bytes / 16, chunks = (pieces + 7) / 8;
   const int scale_bytes = 2 * ((a.I + 63) / 64);
   const int row = blockIdx.x * kRows + lane / 4;  // as the loads have it
   // parts of an expert's rows: enough for two a wave, of two chunks at least
-  const int wanted = (2 * kDownWaves + s.experts - 1) / max(s.experts, 1);
+  const int wanted = (2 * kWaves + s.experts - 1) / max(s.experts, 1);
   const int part_chunks = max(2, (chunks + wanted - 1) / wanted);
   const int parts = (chunks + part_chunks - 1) / part_chunks;
-  for (int unit = wave; unit < s.experts * parts; unit += kDownWaves) {
+  for (int unit = wave; unit < s.experts * parts; unit += kWaves) {
     const int which = unit / parts, part = unit - which * parts;
     const int expert = s.active[which];
     const int64_t w_row = static_cast<int64_t>(expert) * a.H + row;
@@ -590,7 +590,7 @@ __global__ __launch_bounds__(kDownWaves * 64, DNB) void few_down_kernel(FewArgs 
       int token[kTiles];
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) {
-        const int place = at + n * 16 + r, loads = at + n * 16 + lane / 4;
+        const int place = at + n * 16 + r, loads = at + n * 16 + (kSort ? lane / 4 : r);
         has[n] = place < end;
         token[n] = has[n] ? s.slot[place] / a.k : 0;
         h_row[n] = loads < end ? static_cast<uint32_t>(t0 * a.k + s.slot[loads]) * a.I * 2 : kNoRow;
@@ -598,7 +598,7 @@ __global__ __launch_bounds__(kDownWaves * 64, DNB) void few_down_kernel(FewArgs 
       f32x4 acc[1][kTiles];
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) acc[0][n] = f32x4{0, 0, 0, 0};
-      sum_chunks<kMx, kBf16, kTiles, 1>(acc, rows, scales, rows_buffer(a.ws_h, a.T * a.k * a.I * 2), h_row,
+      sum_chunks<kMx, kBf16, kTiles, kSort, 1>(acc, rows, scales, rows_buffer(a.ws_h, a.T * a.k * a.I * 2), h_row,
                                         part * part_chunks,
                                         min(chunks, (part + 1) * part_chunks), 1, pieces);
 #pragma unroll
@@ -610,34 +610,45 @@ __global__ __launch_bounds__(kDownWaves * 64, DNB) void few_down_kernel(FewArgs 
   for (int i = tid; i < tokens * 4; i += kThreads) {
     f32x4 sum = sums[i];
 #pragma unroll
-    for (int w = 1; w < kDownWaves; ++w) sum += sums[w * tokens * 4 + i];
+    for (int w = 1; w < kWaves; ++w) sum += sums[w * tokens * 4 + i];
     store_row4<kBf16>(a.y + (static_cast<int64_t>(t0 + i / 4) * a.H + blockIdx.x * kRows + i % 4 * 4) * 2, sum);
   }
 }
 
-template <bool kMx, bool kBf16, int kTiles>
+template <bool kMx, bool kBf16, int kTiles, bool kSort>
 mrr_status launch_few_tiles(const FewArgs& a, hipStream_t stream) {
   const int slots = a.T * a.k;
   if (a.logits != nullptr && a.T > kSelfRouted) {
     hipLaunchKernelGGL(few_route_kernel, dim3(a.T), dim3(64), 0, stream, a);
     if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
   }
-  const int64_t units = static_cast<int64_t>(slots < a.E ? slots : a.E) * (a.I / kRows);
-  const int64_t most = 256 * 4;
-  hipLaunchKernelGGL((few_up_kernel<kMx, kBf16, kTiles>), dim3(static_cast<unsigned>(units < most ? units : most)),
+  // the workgroups that the chip holds at once (by their registers), each taking
+  // its units in turn
+  const int64_t units = static_cast<int64_t>(slots < a.E ? slots : a.E) * (a.I / kRows), most = 256 * (kMx ? 2 : 4);
+  hipLaunchKernelGGL((few_up_kernel<kMx, kBf16, kTiles, kSort>), dim3(static_cast<unsigned>(units < most ? units : most)),
                      dim3(kUpWaves * 64), up_part_bytes(kTiles) + plan_bytes(slots, a.E), stream, a);
   if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
   const int tokens = a.T < kDownTokens ? a.T : kDownTokens;
-  hipLaunchKernelGGL((few_down_kernel<kMx, kBf16, kTiles>), dim3(a.H / kRows, (a.T + kDownTokens - 1) / kDownTokens),
-                     dim3(kDownWaves * 64), down_sum_bytes(tokens) + plan_bytes(tokens * a.k, a.E), stream, a);
+  const dim3 grid(a.H / kRows, (a.T + kDownTokens - 1) / kDownTokens);
+  const size_t plan = plan_bytes(tokens * a.k, a.E);
+  // Up to a workgroup a CU eight waves, else four, so that the chip holds them all
+  // (one token, 8 of 64 4-bit experts, H 7168: 45.6 us with eight, 42.1 with four;
+  // 64 tokens, 4 of 32, H 4096: 128.8 and 133.7).
+  if (grid.x * grid.y <= 256)
+    hipLaunchKernelGGL((few_down_kernel<kMx, kBf16, kTiles, kSort, 8>), grid, dim3(512),
+                       down_sum_bytes(tokens, 8) + plan, stream, a);
+  else
+    hipLaunchKernelGGL((few_down_kernel<kMx, kBf16, kTiles, kSort, 4>), grid, dim3(256),
+                       down_sum_bytes(tokens, 4) + plan, stream, a);
   return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
 }
 
 template <bool kMx, bool kBf16>
 mrr_status launch_few(const FewArgs& a, hipStream_t stream) {
   // two tiles of tokens at once where an expert has more than one, on average
-  return a.T * a.k > 16 * a.E ? launch_few_tiles<kMx, kBf16, 2>(a, stream)
-                              : launch_few_tiles<kMx, kBf16, 1>(a, stream);
+  return a.T <= kSelfRouted        ? launch_few_tiles<kMx, kBf16, 1, false>(a, stream)
+         : a.T * a.k <= 16 * a.E ? launch_few_tiles<kMx, kBf16, 1, true>(a, stream)
+                                   : launch_few_tiles<kMx, kBf16, 2, true>(a, stream);
 }
 
 }  // namespace
