@@ -208,6 +208,27 @@ def load() -> ctypes.CDLL:
         return _lib
 
 
+_binding = None
+
+
+def binding():
+    """The native binding of the experts' operators (_mrr_torch.so), built with
+    the library; raises RuntimeError like load()."""
+    global _binding
+    if _binding is None:
+        load()
+        try:
+            from . import _mrr_torch
+        except ImportError as e:
+            raise RuntimeError("the native binding is missing or does not fit this torch: build it with "
+                               "`python -m moe_token_re_amd.build`") from e
+        if _mrr_torch.source_hash != library_source_hash():
+            raise RuntimeError("_mrr_torch.so was built from other sources: rebuild it with "
+                               "`python -m moe_token_re_amd.build`")
+        _binding = _mrr_torch
+    return _binding
+
+
 def library_source_hash() -> str:
     """The source hash compiled into the loaded library (equal to the current
     sources' hash, or load() would have refused it)."""

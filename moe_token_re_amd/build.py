@@ -5,7 +5,8 @@ g++ with no HIP header; the kernel files (mrr_offsets.hip, mrr_gather.hip,
 mrr_fused.hip, mrr_one_launch.hip; mrr_mx_quant.hip, mrr_grouped_mm.hip,
 mrr_few_tokens.hip, with their own entry points) and the re-routing's entry
 points (mrr_entry.hip) by hipcc, in parallel. Packed-fp32 instructions are
-disabled for all device code.
+disabled for all device code. The short way from torch tensors to the experts'
+operators (mrr_torch.cpp) becomes _mrr_torch.so beside it.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import hashlib
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,10 +24,12 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libmoe_rerouting_v2.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
+BINDING_PATH = os.path.join(PKG, "_mrr_torch.so")
 BENCH_LIB_PATH = os.path.join(PKG, "libmrr_bench_copy.so")
 ARCH = "gfx950"
 
-HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
+HIPCC = os.environ.get("HIPCC", os.path.join(ROCM, "bin", "hipcc"))
 HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
              "-Wall", "-Wno-unused-command-line-argument"]
@@ -61,10 +65,29 @@ HIP_SOURCES = ("mrr_offsets.hip", "mrr_gather.hip", "mrr_fused.hip", "mrr_one_la
 HOST_SOURCES = ("mrr_validate.cpp", "mrr_experts_validate.cpp")
 
 
+def _binding_commands():
+    """(compile, link) commands of the torch binding; it has no device code."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD_DIR, "mrr_torch.o")
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-Werror", "-D__HIP_PLATFORM_AMD__",
+                "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                f'-DMRR_SOURCE_HASH="{source_hash()}"', "-I", INCLUDE, "-isystem", os.path.join(root, "include"),
+                "-isystem", os.path.join(ROCM, "include"), "-isystem", sysconfig.get_paths()["include"],
+                "-c", os.path.join(CSRC, "mrr_torch.cpp"), "-o", obj]
+    link = ["g++", "-shared", "-o", BINDING_PATH + ".tmp", obj, "-L", PKG, f"-l:{LIB_NAME}",
+            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip",
+            "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
+
+
 def build_library(verbose: bool = False) -> str:
-    """Compile and link the library; returns its path. Always recompiles."""
+    """Compile and link the library and its torch binding; returns the library's
+    path. Always recompiles."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    cmds, objs = [], []
+    compile_binding, link_binding = _binding_commands()
+    cmds, objs = [compile_binding], []
     for src in HOST_SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".cpp", ".o"))
         cmds.append(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-Werror", "-I", INCLUDE,
@@ -80,6 +103,8 @@ def build_library(verbose: bool = False) -> str:
     tmp = LIB_PATH + ".tmp"
     _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB_PATH)
+    _run(link_binding, verbose)
+    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
     return LIB_PATH
 
 

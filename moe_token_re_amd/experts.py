@@ -4,8 +4,10 @@
 
 Argument marshalling only, as in api.py: torch provides device memory and the
 current stream; every step runs in the HIP kernels of libmoe_rerouting_v2.so,
-and there is no CPU fallback. The operators serve inference: their results
-carry no gradient.
+and there is no CPU fallback. A plain call goes by the native binding
+(csrc/mrr_torch.cpp), which launches it or returns None; the code here makes
+every other call and raises every error. The operators serve inference: their
+results carry no gradient.
 
 The microscaled format is the one moe_re_routing moves: a row of H values is a
 row of float4_e2m1fn_x2 [H/2] (two values a byte, the first in the low nibble)
@@ -87,6 +89,10 @@ def mx_quantize(x: torch.Tensor, *, out: Optional[Tuple[torch.Tensor, torch.Tens
     2^(floor(log2(max |x|)) - 2); values are rounded to nearest, ties to even,
     and saturate at 6 times the scale. A block that holds a NaN or an infinity
     becomes NaN as a whole."""
+    if out is None:
+        done = _lib.binding().quantize(x)
+        if done is not None:
+            return done
     dev = _gpu("x", x)
     _check_tensor("x", x, dev)
     if x.dtype not in _WIDE:
@@ -110,6 +116,10 @@ def mx_dequantize(packed: torch.Tensor, scales: torch.Tensor, *, dtype: torch.dt
                   out: Optional[torch.Tensor] = None):
     """The values of microscaled 4-bit rows (as mx_quantize returns them), rounded
     once to `dtype` (float16, bfloat16 or float32): [..., H]."""
+    if out is None:
+        done = _lib.binding().dequantize(packed, scales, dtype)
+        if done is not None:
+            return done
     dev = _gpu("packed", packed)
     lead, H = _check_mx("packed", packed, scales, dev)
     if H == 0:
@@ -146,6 +156,11 @@ def mx_grouped_mm(tokens: torch.Tensor, scales: torch.Tensor, weight: torch.Tens
     counts are checked on the device: where they are negative or do not sum to
     A nothing is written, and with check=True the call waits for the stream and
     raises MrrValueError."""
+    if out is None and workspace is None and not check:
+        done = _lib.binding().grouped_mm(tokens, scales, weight, weight_scales, expert_token_num, gated, row_weight,
+                                         expert_token_num_type, dtype)
+        if done is not None:
+            return done
     dev = _gpu("tokens", tokens)
     (A,), K = _check_mx("tokens", tokens, scales, dev, 1)
     (E, N), wk = _check_mx("weight", weight, weight_scales, dev, 2)
@@ -216,6 +231,11 @@ def moe_few_tokens(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, *
     chosen), or expert_ids [T, k] int32 with expert_weight [T, k] float32 (an id
     outside [0, E) chooses nothing). Returns y [T, H] of x's dtype; a token
     without experts gives zeros."""
+    if out is None and workspace is None:
+        done = _lib.binding().few_tokens(x, gate_up, down, router_logits, top_k, renormalize, expert_ids,
+                                         expert_weight, gate_up_scales, down_scales)
+        if done is not None:
+            return done
     dev = _gpu("x", x)
     _check_tensor("x", x, dev)
     if x.dtype not in (torch.float16, torch.bfloat16):
