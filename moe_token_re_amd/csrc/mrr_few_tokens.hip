@@ -47,7 +47,7 @@ struct FewArgs {
   int32_t renormalize;
 };
 
-inline __host__ __device__ size_t up_part_bytes(int tiles) { return sizeof(f32x4) * kUpWaves * 2 * tiles * 64; }
+inline __host__ __device__ size_t up_part_bytes(int tiles) { return 2 * sizeof(f32x4) * kUpWaves * 2 * tiles * 64; }
 inline __host__ __device__ size_t down_sum_bytes(int tokens, int waves) { return sizeof(f32x4) * waves * tokens * 4; }
 
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
@@ -260,53 +260,75 @@ struct Tokens {
 template <bool kMx>
 __device__ __forceinline__ int row_bytes(int n) { return kMx ? n / 2 : n * 2; }
 
-// Chunk c of a weight row of `pieces`; if kTail, with zeros past the row's end.
-template <bool kMx, bool kTail>
-__device__ __forceinline__ void load_weights(Weights<kMx>& w, const uint8_t* row, const uint8_t* scales, int c,
-                                             int pieces) {
-  const u32x4* from = reinterpret_cast<const u32x4*>(row);
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const int piece = c * 8 + p * 4 + threadIdx.x % 4;
-    const u32x4 v = from[kTail ? min(piece, pieces - 1) : piece];
-    w.v[p] = !kTail || piece < pieces ? v : u32x4{0, 0, 0, 0};
-  }
-  if constexpr (kMx) {
-    if constexpr (!kTail) {
-      __builtin_memcpy(w.scale, scales + c * 8, 8);
-    } else {
-      w.scale[0] = w.scale[1] = 0x7f7f7f7fu;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t s = scales[min(c * 8 + i, pieces - 1)], at = 8 * (i % 4);
-        if (c * 8 + i < pieces) w.scale[i / 4] = (w.scale[i / 4] & ~(0xffu << at)) | s << at;
-      }
-    }
-  }
-}
+using Buffer = __amdgpu_buffer_rsrc_t;
 
-// Rows of tokens as a buffer: what lies outside reads as zeros, without traffic.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const uint8_t* p, uint32_t bytes) {
+// Memory as a buffer: what lies outside reads as zeros, without traffic. The
+// address is the same for all lanes.
+__device__ __forceinline__ Buffer buffer_at(const uint8_t* p, uint32_t bytes) {
   constexpr int kRaw = 0x00027000;  // 32-bit data, no swizzle, no stride
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, bytes, kRaw);
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t low = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
+  const uint32_t high = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(static_cast<uint64_t>(high) << 32 | low), 0, bytes,
+                                           kRaw);
 }
-constexpr uint32_t kNoRow = 0x80000000u;  // an offset outside, with any within a row added to it
+constexpr uint32_t kOutside = 0x80000000u;  // an offset outside of any buffer here, and so is a little more
 
-// The same of the tokens' rows, given by their offsets (kNoRow: none). Of 16-bit
-// values a piece of 4-bit weights takes 64 bytes: four lanes' worth. Of one token
-// four lanes read, in whichever order: `group` is the lane's place in a row.
-template <bool kMx, int kTiles, bool kTail>
-__device__ __forceinline__ void load_tokens(Tokens<kMx, kTiles>& x, __amdgpu_buffer_rsrc_t from,
-                                            const uint32_t (&rows)[kTiles], int c, int group, int pieces) {
+__device__ __forceinline__ u32x4 load16(Buffer from, uint32_t lane_offset, uint32_t offset) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, lane_offset, offset, 0));
+}
+
+// Where a wave reads: chunk `c` on of kParts runs of 16 weight rows and of
+// kTiles * 16 tokens' rows, `left` chunks of them, every `step`-th.
+template <int kTiles, int kParts>
+struct Place {
+  const uint8_t* rows[kParts];    // the first of the 16 rows; the same for all lanes
+  const uint8_t* scales[kParts];
+  uint32_t x[kTiles];             // the lane's row in the tokens' buffer; kOutside: none
+  int c, left, step;
+};
+
+// What is the same for all chunks of a kernel.
+struct Rows {
+  Buffer x;
+  int pieces, bytes, scale_bytes;  // of a weight row
+};
+
+// A chunk of 16 weight rows, by lane 4 r + g; zeros past the rows' end.
+template <bool kMx>
+__device__ __forceinline__ void load_weights(Weights<kMx>& w, const uint8_t* rows, const uint8_t* scales, const Rows& all,
+                                             int c) {
+  const int r = threadIdx.x % 64 / 4, g = threadIdx.x % 4;
+  const Buffer from = buffer_at(rows, 16 * all.bytes);
+  const int valid = all.pieces - c * 8;
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+    w.v[p] = load16(from, p * 4 + g < valid ? r * all.bytes + p * 64 + g * 16 : kOutside, c * 128);
+  if constexpr (kMx) {
+    // the eight bytes that end where the row does, or a chunk of it, but within
+    // the 16 rows; a scale of zero (2^-127) goes with the zeros
+    const int row = r * all.scale_bytes, at = max(row + min(c * 8 + 8, all.scale_bytes) - 8, 0);
+    uint64_t v;
+    __builtin_memcpy(&v, scales + static_cast<uint32_t>(at), 8);
+    v >>= 8 * (row + c * 8 - at);
+    v &= valid < 8 ? (uint64_t(1) << 8 * valid) - 1 : ~uint64_t(0);
+    w.scale[0] = static_cast<uint32_t>(v);
+    w.scale[1] = static_cast<uint32_t>(v >> 32);
+  }
+}
+
+// The same of the tokens' rows. Of 16-bit values a piece of 4-bit weights takes
+// 64 bytes: four lanes' worth.
+template <bool kMx, int kTiles, bool kSort>
+__device__ __forceinline__ void load_tokens(Tokens<kMx, kTiles>& x, const uint32_t (&rows)[kTiles], const Rows& all,
+                                            int c) {
+  const int g = kSort ? threadIdx.x % 4 : threadIdx.x % 64 / 16;
+  const int valid = all.pieces - c * 8;
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-    for (int i = 0; i < (kMx ? 8 : 2); ++i) {
-      const int unit = c * (kMx ? 32 : 8) + i * 4 + group;
-      uint32_t at = rows[t] + unit * 16;
-      if (kTail && unit >= pieces * (kMx ? 4 : 1)) at = kNoRow;
-      x.v[t][i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(from, at, 0, 0));
-    }
+    for (int i = 0; i < (kMx ? 8 : 2); ++i)
+      x.v[t][i] = load16(all.x, (kMx ? i : i * 4 + g) < valid ? rows[t] + g * 16 + i * 64 : kOutside, c * (kMx ? 512 : 128));
 }
 
 // From lane 4 r + g to lane 16 g + r.
@@ -384,26 +406,27 @@ __device__ __forceinline__ void store_row4(uint8_t* p, f32x4 v) {
   }
 }
 
-// A wave's sums over chunks c0, c0 + step, ... below `end` of kParts rows of
-// weights at once. The next chunk is on its way while one is multiplied; there is
-// no branch between a load and its use, so that the wait for one does not wait
-// for the next (the last chunk is loaded once more, from the cache). kSort: the
-// tokens are read by neighbouring lanes too; a few tokens cost less as they are.
+// A wave's stream of chunks. The next chunk is on its way while one is
+// multiplied, also the first one of the next sum; between a load and its use there
+// is no branch over other loads, so that the wait for one does not wait for the
+// next. kSort: the tokens are read by neighbouring lanes too; a few tokens cost
+// less as they are. `next` moves a place to the next sum's first chunk.
 template <bool kMx, bool kBf16, int kTiles, bool kSort, int kParts>
-__device__ __forceinline__ void sum_chunks(f32x4 (&acc)[kParts][kTiles], const uint8_t* const (&rows)[kParts],
-                                           const uint8_t* const (&scales)[kParts], __amdgpu_buffer_rsrc_t x_from,
-                                           const uint32_t (&x_rows)[kTiles], int c0, int end, int step, int pieces) {
-  const int group = kSort ? threadIdx.x % 4 : threadIdx.x % 64 / 16;
+struct Stream {
   Weights<kMx> w[2][kParts];
   Tokens<kMx, kTiles> x[2];
-  auto load = [&](int b, int c, auto tail) {
-    constexpr bool kTail = decltype(tail)::value;
+
+  template <typename Next>
+  __device__ __forceinline__ void load(int b, Place<kTiles, kParts>& at, const Rows& all, Next&& next) {
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) load_weights<kMx, kTail>(w[b][i], rows[i], scales[i], c, pieces);
-    load_tokens<kMx, kTiles, kTail>(x[b], x_from, x_rows, c, group, pieces);
+    for (int i = 0; i < kParts; ++i) load_weights<kMx>(w[b][i], at.rows[i], at.scales[i], all, at.c);
+    load_tokens<kMx, kTiles, kSort>(x[b], at.x, all, at.c);
     __builtin_amdgcn_sched_barrier(0);  // or they sink to their use
-  };
-  auto use = [&](int b) {
+    at.c += at.step;
+    if (--at.left == 0) next(at);
+  }
+
+  __device__ __forceinline__ void use(int b, f32x4 (&acc)[kParts][kTiles]) {
     if constexpr (kSort) {
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
@@ -413,90 +436,46 @@ __device__ __forceinline__ void sum_chunks(f32x4 (&acc)[kParts][kTiles], const u
 #pragma unroll
     for (int i = 0; i < kParts; ++i) multiply<kMx, kBf16, kTiles>(w[b][i], x[b], acc[i]);
     __builtin_amdgcn_sched_barrier(0);
-  };
-  const int whole = min(end, pieces / 8);
-  int n = c0 < whole ? (whole - c0 + step - 1) / step : 0, c = c0;
-  if (n > 0) {
-    load(0, c, std::false_type{});
+  }
+
+  // The sums of the next n > 0 chunks, whose first is in the first buffer.
+  template <typename Next>
+  __device__ __forceinline__ void sum(f32x4 (&acc)[kParts][kTiles], int n, Place<kTiles, kParts>& at, const Rows& all,
+                                      Next&& next) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
     for (;;) {
-      c += n > 1 ? step : 0;
-      load(1, c, std::false_type{});
-      use(0);
-      if (--n == 0) break;
-      c += n > 1 ? step : 0;
-      load(0, c, std::false_type{});
-      use(1);
-      if (--n == 0) break;
+      load(1, at, all, next);
+      use(0, acc);
+      if (--n == 0) {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) w[0][i] = w[1][i];
+        x[0] = x[1];
+        return;
+      }
+      load(0, at, all, next);
+      use(1, acc);
+      if (--n == 0) return;
     }
   }
-  const int last = pieces / 8;  // a chunk that the row ends in
-  if (pieces % 8 != 0 && c0 <= last && last < end && (last - c0) % step == 0) {
-    load(0, last, std::true_type{});
-    use(0);
-  }
-}
+};
 
-// One unit of the first kernel: 16 gate rows and the same 16 up rows of an
-// expert, for kTiles * 16 of its tokens from place `at` on. The waves share
-// the rows' length, chunk by chunk.
-template <bool kMx, bool kBf16, int kTiles, bool kSort>
-__device__ __forceinline__ void up_unit(const FewArgs& a, const Plan& s, f32x4* part, int expert, int tile, int at,
-                                        int end) {
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int r = lane % 16, group = lane / 16;
-  const int bytes = row_bytes<kMx>(a.H);
-  const int pieces = bytes / 16;
-  const int scale_bytes = 2 * ((a.H + 63) / 64);
-  const int64_t row = static_cast<int64_t>(expert) * 2 * a.I + tile * kRows + lane / 4;  // as the loads have it
-  const uint8_t* rows[2] = {a.gate_up + row * bytes, a.gate_up + (row + a.I) * bytes};
-  const uint8_t* scales[2] = {a.gate_up_scales + row * scale_bytes, a.gate_up_scales + (row + a.I) * scale_bytes};
-  uint32_t x_row[kTiles];
-#pragma unroll
-  for (int n = 0; n < kTiles; ++n) {
-    const int place = at + n * 16 + (kSort ? lane / 4 : r);
-    x_row[n] = place < end ? static_cast<uint32_t>(s.slot[place] / a.k) * a.H * 2 : kNoRow;
-  }
-  f32x4 acc[2][kTiles];
-#pragma unroll
-  for (int n = 0; n < kTiles; ++n) acc[0][n] = acc[1][n] = f32x4{0, 0, 0, 0};
-  sum_chunks<kMx, kBf16, kTiles, kSort, 2>(acc, rows, scales, rows_buffer(a.x, a.T * a.H * 2), x_row, wave,
-                                      (pieces + 7) / 8, kUpWaves, pieces);
-#pragma unroll
-  for (int n = 0; n < kTiles; ++n) {
-    part[((wave * 2 + 0) * kTiles + n) * 64 + lane] = acc[0][n];
-    part[((wave * 2 + 1) * kTiles + n) * 64 + lane] = acc[1][n];
-  }
-  __syncthreads();
-  // a wave finishes a tile of tokens: a lane has four rows of one token
-  for (int n = wave; n < kTiles; n += kUpWaves) {
-    f32x4 gs = part[n * 64 + lane], us = part[(kTiles + n) * 64 + lane];
-#pragma unroll
-    for (int w = 1; w < kUpWaves; ++w) {
-      gs += part[(w * 2 * kTiles + n) * 64 + lane];
-      us += part[((w * 2 + 1) * kTiles + n) * 64 + lane];
-    }
-    const int place = at + n * 16 + r;
-    if (place < end) {
-      const int slot = s.slot[place];
-      const float p = s.weight[slot];
-      f32x4 h;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = p * (gs[i] / (1.0f + __expf(-gs[i]))) * us[i];
-      store_row4<kBf16>(a.ws_h + (static_cast<int64_t>(slot) * a.I + tile * kRows + group * 4) * 2, h);
-    }
-  }
-  __syncthreads();
-}
+// A barrier of LDS alone: loads from memory stay on their way.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// The first kernel. A unit is 16 gate rows and the same 16 up rows of an expert,
+// for kTiles * 16 of its tokens; the waves share the rows' length, chunk by chunk.
 template <bool kMx, bool kBf16, int kTiles, bool kSort>
 __global__ __launch_bounds__(kUpWaves * 64, 2) void few_up_kernel(FewArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int kThreads = kUpWaves * 64;
   const int slots = a.T * a.k, tid = threadIdx.x, lane = tid % 64;
-  f32x4* part = reinterpret_cast<f32x4*>(lds);  // [waves][2][tiles][64]: partial sums of a unit
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
   Plan s = carve(lds + up_part_bytes(kTiles), slots, a.E);
   if (a.logits != nullptr && a.T <= kSelfRouted) {
-    for (int t = tid / 64; t < a.T; t += kUpWaves) {
+    for (int t = wave; t < a.T; t += kUpWaves) {
       int id;
       float weight;
       route_token(a, t, lane, &id, &weight);
@@ -533,20 +512,107 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void few_up_kernel(FewArgs a) {
   if (blockIdx.x == 0 && (a.logits == nullptr || a.T <= kSelfRouted))  // for the second kernel
     for (int i = tid; i < slots; i += kThreads) a.ws_ids[i] = s.id[i];
 
-  const int tiles = a.I / kRows;
-  const int units = s.experts * tiles;
-  for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
-    const int n = unit / tiles, tile = unit - n * tiles;
-    const int expert = s.active[n], end = s.first[n + 1];
-    for (int at = s.first[n]; at < end;) {
-      if (kTiles == 1 || end - at <= 16) {
-        up_unit<kMx, kBf16, 1, kSort>(a, s, part, expert, tile, at, end);
-        at += 16;
-      } else {
-        up_unit<kMx, kBf16, kTiles, kSort>(a, s, part, expert, tile, at, end);
-        at += kTiles * 16;
+  // This workgroup's units: row tile `tile` of active expert `n`, its tokens from
+  // place `at` on.
+  struct Unit {
+    int unit, n, tile, at, end;
+  };
+  const int tiles = a.I / kRows, units = s.experts * tiles;
+  auto begin = [&](Unit& u) {
+    if (u.unit >= units) return;
+    u.n = u.unit / tiles;
+    u.tile = u.unit - u.n * tiles;
+    u.at = __builtin_amdgcn_readfirstlane(s.first[u.n]);
+    u.end = __builtin_amdgcn_readfirstlane(s.first[u.n + 1]);
+  };
+  auto advance = [&](Unit& u) {
+    u.at += 16 * kTiles;
+    if (u.at < u.end) return;
+    u.unit += gridDim.x;
+    begin(u);
+  };
+  Unit u{static_cast<int>(blockIdx.x), 0, 0, 0, 0};
+  if (u.unit >= units) return;
+  begin(u);
+
+  Rows all;
+  all.x = buffer_at(a.x, a.T * a.H * 2);
+  all.bytes = row_bytes<kMx>(a.H);
+  all.pieces = all.bytes / 16;
+  all.scale_bytes = 2 * ((a.H + 63) / 64);
+  const int chunks = (all.pieces + 7) / 8;
+  const int n = wave < chunks ? (chunks - wave + kUpWaves - 1) / kUpWaves : 0;  // of this wave
+  using Where = Place<kTiles, 2>;
+  auto set = [&](Where& p, const Unit& u) {
+    const int expert = __builtin_amdgcn_readfirstlane(s.active[u.n]);
+    const int64_t row = static_cast<int64_t>(expert) * 2 * a.I + u.tile * kRows;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {  // the gate's rows and the up projection's
+      p.rows[i] = a.gate_up + (row + i * a.I) * all.bytes;
+      p.scales[i] = a.gate_up_scales + (row + i * a.I) * all.scale_bytes;
+    }
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      const int place = u.at + t * 16 + (kSort ? lane / 4 : lane % 16);
+      p.x[t] = place < u.end ? static_cast<uint32_t>(s.slot[place] / a.k) * a.H * 2 : kOutside;
+    }
+    p.c = wave;
+    p.left = n;
+    p.step = kUpWaves;
+  };
+  Unit ahead = u;
+  Where where;
+  auto next = [&](Where& p) {  // behind the last unit: its first chunk again
+    if (ahead.unit < units) advance(ahead);
+    if (ahead.unit < units) {
+      set(p, ahead);
+    } else {
+      p.c = wave;
+      p.left = 1 << 30;
+      p.step = 0;
+    }
+  };
+  set(where, u);
+  Stream<kMx, kBf16, kTiles, kSort, 2> stream;
+  if (n > 0) stream.load(0, where, all, next);
+  f32x4* part = reinterpret_cast<f32x4*>(lds);  // two of [waves][2][tiles][64]: partial sums of a unit
+  constexpr int kPart = kUpWaves * 2 * kTiles * 64;
+  int finisher = 0;
+  for (; u.unit < units; advance(u)) {
+    f32x4 acc[2][kTiles];
+    if (n > 0) {
+      stream.sum(acc, n, where, all, next);
+    } else {
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) acc[0][t] = acc[1][t] = f32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) part[((wave * 2 + i) * kTiles + t) * 64 + lane] = acc[i][t];
+    lds_barrier();
+    // a wave finishes a tile of tokens, each its turn: a lane has four rows of one
+    // token. Meanwhile the others go on, in the other half of `part`.
+    for (int t = 0; t < kTiles; ++t, finisher = (finisher + 1) % kUpWaves) {
+      if (wave != finisher) continue;
+      f32x4 gs = part[t * 64 + lane], us = part[(kTiles + t) * 64 + lane];
+#pragma unroll
+      for (int w = 1; w < kUpWaves; ++w) {
+        gs += part[(w * 2 * kTiles + t) * 64 + lane];
+        us += part[((w * 2 + 1) * kTiles + t) * 64 + lane];
+      }
+      const int place = u.at + t * 16 + lane % 16;
+      if (place < u.end) {
+        const int slot = s.slot[place];
+        const float p = s.weight[slot];
+        f32x4 h;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = p * (gs[i] / (1.0f + __expf(-gs[i]))) * us[i];
+        const int col = u.tile * kRows + lane / 16 * 4;
+        store_row4<kBf16>(a.ws_h + (static_cast<int64_t>(slot) * a.I + col) * 2, h);
       }
     }
+    part = part == reinterpret_cast<f32x4*>(lds) ? part + kPart : reinterpret_cast<f32x4*>(lds);
   }
 }
 
@@ -559,7 +625,7 @@ template <bool kMx, bool kBf16, int kTiles, bool kSort, int kWaves>
 __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int kThreads = kWaves * 64;
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
+  const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int r = lane % 16, group = lane / 16;
   const int t0 = blockIdx.y * kDownTokens, tokens = min(a.T - t0, kDownTokens), slots = tokens * a.k;
   f32x4* sums = reinterpret_cast<f32x4*>(lds);  // [waves][tokens][4 groups]
@@ -569,41 +635,77 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
   for (int i = lane; i < tokens * 4; i += 64) mine[i] = f32x4{0, 0, 0, 0};
   make_plan<kWaves>(s, slots, a.E);
 
-  const int bytes = row_bytes<kMx>(a.I);
-  const int pieces = bytes / 16, chunks = (pieces + 7) / 8;
-  const int scale_bytes = 2 * ((a.I + 63) / 64);
-  const int row = blockIdx.x * kRows + lane / 4;  // as the loads have it
+  Rows all;
+  all.x = buffer_at(a.ws_h, a.T * a.k * a.I * 2);
+  all.bytes = row_bytes<kMx>(a.I);
+  all.pieces = all.bytes / 16;
+  all.scale_bytes = 2 * ((a.I + 63) / 64);
+  const int chunks = (all.pieces + 7) / 8;
   // parts of an expert's rows: enough for two a wave, of two chunks at least
   const int wanted = (2 * kWaves + s.experts - 1) / max(s.experts, 1);
   const int part_chunks = max(2, (chunks + wanted - 1) / wanted);
   const int parts = (chunks + part_chunks - 1) / part_chunks;
-  for (int unit = wave; unit < s.experts * parts; unit += kWaves) {
-    const int which = unit / parts, part = unit - which * parts;
-    const int expert = s.active[which];
-    const int64_t w_row = static_cast<int64_t>(expert) * a.H + row;
-    const uint8_t* rows[1] = {a.down + w_row * bytes};
-    const uint8_t* scales[1] = {a.down_scales + w_row * scale_bytes};
-    const int end = s.first[which + 1];
-    for (int at = s.first[which]; at < end; at += 16 * kTiles) {
-      uint32_t h_row[kTiles];
-      bool has[kTiles];
-      int token[kTiles];
+  // This wave's units: part `part` of active expert `n`, its tokens from place
+  // `at` on.
+  struct Unit {
+    int unit, n, part, at, end;
+  };
+  const int units = s.experts * parts;
+  auto begin = [&](Unit& u) {
+    if (u.unit >= units) return;
+    u.n = u.unit / parts;
+    u.part = u.unit - u.n * parts;
+    u.at = __builtin_amdgcn_readfirstlane(s.first[u.n]);
+    u.end = __builtin_amdgcn_readfirstlane(s.first[u.n + 1]);
+  };
+  auto advance = [&](Unit& u) {
+    u.at += 16 * kTiles;
+    if (u.at < u.end) return;
+    u.unit += kWaves;
+    begin(u);
+  };
+  auto length = [&](const Unit& u) { return min(part_chunks, chunks - u.part * part_chunks); };
+  using Where = Place<kTiles, 1>;
+  auto set = [&](Where& p, const Unit& u) {
+    const int expert = __builtin_amdgcn_readfirstlane(s.active[u.n]);
+    const int64_t row = static_cast<int64_t>(expert) * a.H + blockIdx.x * kRows;
+    p.rows[0] = a.down + row * all.bytes;
+    p.scales[0] = a.down_scales + row * all.scale_bytes;
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n) {
-        const int place = at + n * 16 + r, loads = at + n * 16 + (kSort ? lane / 4 : r);
-        has[n] = place < end;
-        token[n] = has[n] ? s.slot[place] / a.k : 0;
-        h_row[n] = loads < end ? static_cast<uint32_t>(t0 * a.k + s.slot[loads]) * a.I * 2 : kNoRow;
+    for (int t = 0; t < kTiles; ++t) {
+      const int place = u.at + t * 16 + (kSort ? lane / 4 : r);
+      p.x[t] = place < u.end ? static_cast<uint32_t>(t0 * a.k + s.slot[place]) * a.I * 2 : kOutside;
+    }
+    p.c = u.part * part_chunks;
+    p.left = length(u);
+    p.step = 1;
+  };
+  Unit u{wave, 0, 0, 0, 0};
+  if (u.unit < units) {
+    begin(u);
+    Unit ahead = u;
+    Where where;
+    auto next = [&](Where& p) {  // behind the last unit: its last chunk again
+      if (ahead.unit < units) advance(ahead);
+      if (ahead.unit < units) {
+        set(p, ahead);
+      } else {
+        p.c -= p.step;
+        p.left = 1 << 30;
+        p.step = 0;
       }
+    };
+    set(where, u);
+    Stream<kMx, kBf16, kTiles, kSort, 1> stream;
+    stream.load(0, where, all, next);
+    for (; u.unit < units; advance(u)) {
       f32x4 acc[1][kTiles];
+      stream.sum(acc, length(u), where, all, next);
 #pragma unroll
-      for (int n = 0; n < kTiles; ++n) acc[0][n] = f32x4{0, 0, 0, 0};
-      sum_chunks<kMx, kBf16, kTiles, kSort, 1>(acc, rows, scales, rows_buffer(a.ws_h, a.T * a.k * a.I * 2), h_row,
-                                        part * part_chunks,
-                                        min(chunks, (part + 1) * part_chunks), 1, pieces);
-#pragma unroll
-      for (int n = 0; n < kTiles; ++n)
-        if (has[n]) mine[token[n] * 4 + group] += acc[0][n];
+      for (int t = 0; t < kTiles; ++t) {
+        const int place = u.at + t * 16 + r;
+        if (place < u.end) mine[s.slot[place] / a.k * 4 + group] += acc[0][t];
+      }
     }
   }
   __syncthreads();
