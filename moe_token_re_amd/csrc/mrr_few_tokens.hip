@@ -282,9 +282,9 @@ __device__ __forceinline__ u32x4 load16(Buffer from, uint32_t lane_offset, uint3
 // kTiles * 16 tokens' rows, `left` chunks of them, every `step`-th.
 template <int kTiles, int kParts>
 struct Place {
-  const uint8_t* rows[kParts];    // the first of the 16 rows; the same for all lanes
-  const uint8_t* scales[kParts];
-  uint32_t x[kTiles];             // the lane's row in the tokens' buffer; kOutside: none
+  Buffer rows[kParts];            // the 16 rows
+  const uint8_t* scales[kParts];  // of the 16 rows; the same for all lanes
+  uint32_t x[kTiles];             // what the lane reads of a chunk 0 in the tokens' buffer; kOutside: nothing
   int c, left, step;
 };
 
@@ -292,43 +292,70 @@ struct Place {
 struct Rows {
   Buffer x;
   int pieces, bytes, scale_bytes;  // of a weight row
+  uint32_t at, scales_at;          // what the lane reads of a chunk 0 of 16 rows, and their scales
+  int scales_shift;                // bits that it read too early (rows of fewer than 8 scales alone)
 };
 
-// A chunk of 16 weight rows, by lane 4 r + g; zeros past the rows' end.
 template <bool kMx>
-__device__ __forceinline__ void load_weights(Weights<kMx>& w, const uint8_t* rows, const uint8_t* scales, const Rows& all,
-                                             int c) {
+__device__ __forceinline__ Rows make_rows(const uint8_t* x, uint32_t x_bytes, int n) {
   const int r = threadIdx.x % 64 / 4, g = threadIdx.x % 4;
-  const Buffer from = buffer_at(rows, 16 * all.bytes);
-  const int valid = all.pieces - c * 8;
+  Rows a;
+  a.x = buffer_at(x, x_bytes);
+  a.bytes = row_bytes<kMx>(n);
+  a.pieces = a.bytes / 16;
+  a.scale_bytes = 2 * ((n + 63) / 64);
+  a.at = r * a.bytes + g * 16;
+  const int scales_at = min(r * a.scale_bytes, 16 * a.scale_bytes - 8);
+  a.scales_at = scales_at;
+  a.scales_shift = 8 * (r * a.scale_bytes - scales_at);
+  return a;
+}
+
+// Eight pieces of 16 weight rows from piece `q` on, by lane 4 r + g. Where rows
+// are shorter, other rows' bytes follow, or zeros behind the last one.
+template <bool kMx>
+__device__ __forceinline__ void load_weights(Weights<kMx>& w, Buffer rows, const uint8_t* scales, const Rows& all, int q) {
 #pragma unroll
-  for (int p = 0; p < 2; ++p)
-    w.v[p] = load16(from, p * 4 + g < valid ? r * all.bytes + p * 64 + g * 16 : kOutside, c * 128);
-  if constexpr (kMx) {
-    // the eight bytes that end where the row does, or a chunk of it, but within
-    // the 16 rows; a scale of zero (2^-127) goes with the zeros
-    const int row = r * all.scale_bytes, at = max(row + min(c * 8 + 8, all.scale_bytes) - 8, 0);
-    uint64_t v;
-    __builtin_memcpy(&v, scales + static_cast<uint32_t>(at), 8);
-    v >>= 8 * (row + c * 8 - at);
-    v &= valid < 8 ? (uint64_t(1) << 8 * valid) - 1 : ~uint64_t(0);
-    w.scale[0] = static_cast<uint32_t>(v);
-    w.scale[1] = static_cast<uint32_t>(v >> 32);
-  }
+  for (int p = 0; p < 2; ++p) w.v[p] = load16(rows, all.at + p * 64, q * 16);
+  if constexpr (kMx) __builtin_memcpy(w.scale, scales + q + all.scales_at, 8);
 }
 
 // The same of the tokens' rows. Of 16-bit values a piece of 4-bit weights takes
 // 64 bytes: four lanes' worth.
-template <bool kMx, int kTiles, bool kSort>
-__device__ __forceinline__ void load_tokens(Tokens<kMx, kTiles>& x, const uint32_t (&rows)[kTiles], const Rows& all,
-                                            int c) {
-  const int g = kSort ? threadIdx.x % 4 : threadIdx.x % 64 / 16;
-  const int valid = all.pieces - c * 8;
+template <bool kMx, int kTiles>
+__device__ __forceinline__ void load_tokens(Tokens<kMx, kTiles>& x, const uint32_t (&at)[kTiles], const Rows& all, int q) {
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-    for (int i = 0; i < (kMx ? 8 : 2); ++i)
-      x.v[t][i] = load16(all.x, (kMx ? i : i * 4 + g) < valid ? rows[t] + g * 16 + i * 64 : kOutside, c * (kMx ? 512 : 128));
+    for (int i = 0; i < (kMx ? 8 : 2); ++i) x.v[t][i] = load16(all.x, at[t] + i * 64, q * (kMx ? 64 : 16));
+}
+
+// Zeros for what is not in pieces lo .. hi - 1 of the eight; a scale of zero
+// (2^-127) goes with zeros.
+template <bool kMx>
+__device__ __forceinline__ void cut_weights(Weights<kMx>& w, int lo, int hi, int scales_shift) {
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int piece = p * 4 + threadIdx.x % 4;
+    if (piece < lo || piece >= hi) w.v[p] = u32x4{0, 0, 0, 0};
+  }
+  if constexpr (kMx) {
+    uint64_t v = (static_cast<uint64_t>(w.scale[1]) << 32 | w.scale[0]) >> scales_shift;
+    if (hi < 8) v &= (uint64_t(1) << 8 * hi) - 1;
+    v = v >> 8 * lo << 8 * lo;
+    w.scale[0] = static_cast<uint32_t>(v);
+    w.scale[1] = static_cast<uint32_t>(v >> 32);
+  }
+}
+template <bool kMx, int kTiles>
+__device__ __forceinline__ void cut_tokens(Tokens<kMx, kTiles>& x, int lo, int hi, int g) {
+#pragma unroll
+  for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+    for (int i = 0; i < (kMx ? 8 : 2); ++i) {
+      const int piece = kMx ? i : i * 4 + g;
+      if (piece < lo || piece >= hi) x.v[t][i] = u32x4{0, 0, 0, 0};
+    }
 }
 
 // From lane 4 r + g to lane 16 g + r.
@@ -407,26 +434,35 @@ __device__ __forceinline__ void store_row4(uint8_t* p, f32x4 v) {
 }
 
 // A wave's stream of chunks. The next chunk is on its way while one is
-// multiplied, also the first one of the next sum; between a load and its use there
-// is no branch over other loads, so that the wait for one does not wait for the
-// next. kSort: the tokens are read by neighbouring lanes too; a few tokens cost
+// multiplied, also the first one of the next sum; there is no branch over loads, so
+// that the wait for one chunk does not wait for the next. The chunk that a row ends
+// in is read as its last eight pieces, and those that were counted before are cut
+// (rows of fewer than eight pieces: those that follow). kSort: the tokens are read by neighbouring lanes too; a few tokens cost
 // less as they are. `next` moves a place to the next sum's first chunk.
 template <bool kMx, bool kBf16, int kTiles, bool kSort, int kParts>
 struct Stream {
   Weights<kMx> w[2][kParts];
   Tokens<kMx, kTiles> x[2];
+  int low[2];  // the chunk's first piece that counts
 
   template <typename Next>
   __device__ __forceinline__ void load(int b, Place<kTiles, kParts>& at, const Rows& all, Next&& next) {
+    const int q = max(min(at.c * 8, all.pieces - 8), 0);
+    low[b] = at.c * 8 - q;
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) load_weights<kMx>(w[b][i], at.rows[i], at.scales[i], all, at.c);
-    load_tokens<kMx, kTiles, kSort>(x[b], at.x, all, at.c);
+    for (int i = 0; i < kParts; ++i) load_weights<kMx>(w[b][i], at.rows[i], at.scales[i], all, q);
+    load_tokens<kMx, kTiles>(x[b], at.x, all, q);
     __builtin_amdgcn_sched_barrier(0);  // or they sink to their use
     at.c += at.step;
     if (--at.left == 0) next(at);
   }
 
-  __device__ __forceinline__ void use(int b, f32x4 (&acc)[kParts][kTiles]) {
+  __device__ __forceinline__ void use(int b, f32x4 (&acc)[kParts][kTiles], const Rows& all) {
+    if (low[b] > 0 || all.pieces < 8) {
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) cut_weights<kMx>(w[b][i], low[b], all.pieces, all.scales_shift);
+      cut_tokens<kMx, kTiles>(x[b], low[b], all.pieces, kSort ? threadIdx.x % 4 : threadIdx.x % 64 / 16);
+    }
     if constexpr (kSort) {
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
@@ -448,15 +484,16 @@ struct Stream {
       for (int t = 0; t < kTiles; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
     for (;;) {
       load(1, at, all, next);
-      use(0, acc);
+      use(0, acc, all);
       if (--n == 0) {
 #pragma unroll
         for (int i = 0; i < kParts; ++i) w[0][i] = w[1][i];
         x[0] = x[1];
+        low[0] = low[1];
         return;
       }
       load(0, at, all, next);
-      use(1, acc);
+      use(1, acc, all);
       if (--n == 0) return;
     }
   }
@@ -535,11 +572,7 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void few_up_kernel(FewArgs a) {
   if (u.unit >= units) return;
   begin(u);
 
-  Rows all;
-  all.x = buffer_at(a.x, a.T * a.H * 2);
-  all.bytes = row_bytes<kMx>(a.H);
-  all.pieces = all.bytes / 16;
-  all.scale_bytes = 2 * ((a.H + 63) / 64);
+  const Rows all = make_rows<kMx>(a.x, a.T * a.H * 2, a.H);
   const int chunks = (all.pieces + 7) / 8;
   const int n = wave < chunks ? (chunks - wave + kUpWaves - 1) / kUpWaves : 0;  // of this wave
   using Where = Place<kTiles, 2>;
@@ -548,13 +581,13 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void few_up_kernel(FewArgs a) {
     const int64_t row = static_cast<int64_t>(expert) * 2 * a.I + u.tile * kRows;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {  // the gate's rows and the up projection's
-      p.rows[i] = a.gate_up + (row + i * a.I) * all.bytes;
+      p.rows[i] = buffer_at(a.gate_up + (row + i * a.I) * all.bytes, kRows * all.bytes);
       p.scales[i] = a.gate_up_scales + (row + i * a.I) * all.scale_bytes;
     }
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      const int place = u.at + t * 16 + (kSort ? lane / 4 : lane % 16);
-      p.x[t] = place < u.end ? static_cast<uint32_t>(s.slot[place] / a.k) * a.H * 2 : kOutside;
+      const int place = u.at + t * 16 + (kSort ? lane / 4 : lane % 16), g = kSort ? lane % 4 : lane / 16;
+      p.x[t] = place < u.end ? static_cast<uint32_t>(s.slot[place] / a.k) * a.H * 2 + g * 16 : kOutside;
     }
     p.c = wave;
     p.left = n;
@@ -635,11 +668,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
   for (int i = lane; i < tokens * 4; i += 64) mine[i] = f32x4{0, 0, 0, 0};
   make_plan<kWaves>(s, slots, a.E);
 
-  Rows all;
-  all.x = buffer_at(a.ws_h, a.T * a.k * a.I * 2);
-  all.bytes = row_bytes<kMx>(a.I);
-  all.pieces = all.bytes / 16;
-  all.scale_bytes = 2 * ((a.I + 63) / 64);
+  const Rows all = make_rows<kMx>(a.ws_h, a.T * a.k * a.I * 2, a.I);
   const int chunks = (all.pieces + 7) / 8;
   // parts of an expert's rows: enough for two a wave, of two chunks at least
   const int wanted = (2 * kWaves + s.experts - 1) / max(s.experts, 1);
@@ -669,12 +698,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
   auto set = [&](Where& p, const Unit& u) {
     const int expert = __builtin_amdgcn_readfirstlane(s.active[u.n]);
     const int64_t row = static_cast<int64_t>(expert) * a.H + blockIdx.x * kRows;
-    p.rows[0] = a.down + row * all.bytes;
+    p.rows[0] = buffer_at(a.down + row * all.bytes, kRows * all.bytes);
     p.scales[0] = a.down_scales + row * all.scale_bytes;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      const int place = u.at + t * 16 + (kSort ? lane / 4 : r);
-      p.x[t] = place < u.end ? static_cast<uint32_t>(t0 * a.k + s.slot[place]) * a.I * 2 : kOutside;
+      const int place = u.at + t * 16 + (kSort ? lane / 4 : r), g = kSort ? lane % 4 : group;
+      p.x[t] = place < u.end ? static_cast<uint32_t>(t0 * a.k + s.slot[place]) * a.I * 2 + g * 16 : kOutside;
     }
     p.c = u.part * part_chunks;
     p.left = length(u);
