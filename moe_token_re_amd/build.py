@@ -77,7 +77,7 @@ def _binding_commands():
                 "-isystem", os.path.join(ROCM, "include"), "-isystem", sysconfig.get_paths()["include"],
                 "-c", os.path.join(CSRC, "mrr_torch.cpp"), "-o", obj]
     link = ["g++", "-shared", "-o", BINDING_PATH + ".tmp", obj, "-L", PKG, f"-l:{LIB_NAME}",
-            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip",
+            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch_hip", "-lc10", "-lc10_hip",
             "-Wl,-rpath,$ORIGIN"]
     return compile_, link
 

@@ -6,6 +6,7 @@
 // of that kind or that the library refuses, without having launched anything;
 // experts.py then makes the call itself and raises what there is to raise.
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
@@ -67,7 +68,7 @@ struct Call {
   }
 
   at::Tensor empty(at::IntArrayRef shape, at::ScalarType t) const {
-    return at::empty(shape, at::TensorOptions().device(device).dtype(t));
+    return at::detail::empty_cuda(shape, t, device, std::nullopt);  // what at::empty comes to, without its dispatch
   }
   ihipStream_t* stream() const { return c10::hip::getCurrentHIPStream(device.index()).stream(); }
 };
