@@ -162,7 +162,37 @@ __device__ __forceinline__ Place place_of(const MxArgs& a, uint32_t u) {
   return p;
 }
 
-template <int kDtype, bool kFlat, int kIter>
+using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+using loose4 = u32x4 __attribute__((aligned(2)));
+
+// A lane's eight wide values; kStream: past the caches.
+template <bool kStream, typename W, int n>
+__device__ __forceinline__ void load_unit(W (&w)[n], const uint8_t* p) {
+  if constexpr (kStream) {
+#pragma unroll
+    for (int i = 0; i < n / 4; ++i) {
+      const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const loose4*>(p) + i);
+      __builtin_memcpy(&w[i * 4], &v, 16);
+    }
+  } else {
+    __builtin_memcpy(w, p, sizeof(w));
+  }
+}
+template <bool kStream, typename W, int n>
+__device__ __forceinline__ void store_unit(uint8_t* p, const W (&w)[n]) {
+  if constexpr (kStream) {
+#pragma unroll
+    for (int i = 0; i < n / 4; ++i) {
+      u32x4 v;
+      __builtin_memcpy(&v, &w[i * 4], 16);
+      __builtin_nontemporal_store(v, reinterpret_cast<loose4*>(p) + i);
+    }
+  } else {
+    __builtin_memcpy(p, w, sizeof(w));
+  }
+}
+
+template <int kDtype, bool kFlat, int kIter, bool kStream>
 __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(MxArgs a) {
   using V = Eight<kDtype>;
   const uint32_t u0 = blockIdx.x * static_cast<uint32_t>(kThreads * kIter) + threadIdx.x;
@@ -176,7 +206,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(MxArgs a) {
     if (u >= a.units) p[i].count = 0;
     const uint8_t* src = a.wide + p[i].wide * V::kBytes;
     if (p[i].count == kUnit) {
-      __builtin_memcpy(&v[i].w, src, sizeof(v[i].w));
+      load_unit<kStream>(v[i].w, src);
     } else {
       for (int k = 0; k < kUnit; ++k)
         if (k < p[i].count) v[i].set(k, src + k * V::kBytes);
@@ -199,7 +229,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(MxArgs a) {
   }
 }
 
-template <int kDtype, bool kFlat, int kIter>
+template <int kDtype, bool kFlat, int kIter, bool kStream>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxArgs a) {
   using V = Eight<kDtype>;
   const uint32_t u0 = blockIdx.x * static_cast<uint32_t>(kThreads * kIter) + threadIdx.x;
@@ -227,7 +257,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxArgs a) {
     v.unpack(c[i], scale_float(s[i]));  // s = 255: the scale is an infinity, every value a NaN
     uint8_t* dst = a.wide + p[i].wide * V::kBytes;
     if (p[i].count == kUnit) {
-      __builtin_memcpy(dst, &v.w, sizeof(v.w));
+      store_unit<kStream && kDtype != MRR_F32>(dst, v.w);
     } else {
       for (int k = 0; k < kUnit; ++k)
         if (k < p[i].count) v.get(k, dst + k * V::kBytes);
@@ -239,22 +269,30 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxArgs a) {
 constexpr int64_t kMaxUnits = int64_t(1) << 30;
 // From this many units on a lane takes four of them.
 constexpr int64_t kManyUnits = int64_t(kThreads) * 2048;
+// From so many bytes of wide rows on they are read, and written, past the caches,
+// which would not hold them for a reader anyway: 16384 x 7168 bf16 rows quantised
+// and read back in 131 us by way of the caches and 89 past them (6.6 TB/s), 30000 x
+// 3000 fp32 in 220 and 191; but 4096 x 2048 fp32 in 16.5 and 20. Stores of fp32
+// stay: a lane has two vectors of them, so a store writes half lines.
+constexpr int64_t kStreamBytes = int64_t(64) << 20;
+
+template <int kDtype, bool kFlat, int kIter, bool kStream>
+void launch_kernel(const MxArgs& a, bool quantize, hipStream_t stream) {
+  const dim3 grid((a.units + kThreads * kIter - 1) / (kThreads * kIter));
+  if (quantize)
+    mx_quantize_kernel<kDtype, kFlat, kIter, kStream><<<grid, kThreads, 0, stream>>>(a);
+  else
+    mx_dequantize_kernel<kDtype, kFlat, kIter, kStream><<<grid, kThreads, 0, stream>>>(a);
+}
 
 template <int kDtype, bool kFlat>
-void launch_mx(const MxArgs& a, bool quantize, hipStream_t stream) {
-  if (a.units >= kManyUnits) {
-    const dim3 grid((a.units + kThreads * 4 - 1) / (kThreads * 4));
-    if (quantize)
-      mx_quantize_kernel<kDtype, kFlat, 4><<<grid, kThreads, 0, stream>>>(a);
-    else
-      mx_dequantize_kernel<kDtype, kFlat, 4><<<grid, kThreads, 0, stream>>>(a);
-  } else {
-    const dim3 grid((a.units + kThreads - 1) / kThreads);
-    if (quantize)
-      mx_quantize_kernel<kDtype, kFlat, 1><<<grid, kThreads, 0, stream>>>(a);
-    else
-      mx_dequantize_kernel<kDtype, kFlat, 1><<<grid, kThreads, 0, stream>>>(a);
-  }
+void launch_mx(const MxArgs& a, bool quantize, bool large, hipStream_t stream) {
+  if (a.units < kManyUnits)
+    launch_kernel<kDtype, kFlat, 1, false>(a, quantize, stream);
+  else if (large)
+    launch_kernel<kDtype, kFlat, 4, true>(a, quantize, stream);
+  else
+    launch_kernel<kDtype, kFlat, 4, false>(a, quantize, stream);
 }
 
 mrr_status run_mx(const mrr_mx_args* args, bool quantize, hipStream_t stream) {
@@ -262,7 +300,7 @@ mrr_status run_mx(const mrr_mx_args* args, bool quantize, hipStream_t stream) {
   if (st != MRR_SUCCESS || args->rows == 0) return st;
   const int64_t w = args->wide_dtype == MRR_F32 ? 4 : 2;
   const int64_t per_row = 4 * mx_scale_bytes(args->H);
-  const bool flat = args->H % 64 == 0;
+  const bool flat = args->H % 64 == 0, large = args->rows * args->H * w >= kStreamBytes;
   const int64_t step = kMaxUnits / per_row;  // rows of a launch
   for (int64_t row = 0; row < args->rows; row += step) {
     const int64_t rows = args->rows - row < step ? args->rows - row : step;
@@ -274,9 +312,9 @@ mrr_status run_mx(const mrr_mx_args* args, bool quantize, hipStream_t stream) {
     a.units_per_row = static_cast<uint32_t>(per_row);
     a.H = static_cast<uint32_t>(args->H);
     switch (args->wide_dtype) {
-      case MRR_F16: flat ? launch_mx<MRR_F16, true>(a, quantize, stream) : launch_mx<MRR_F16, false>(a, quantize, stream); break;
-      case MRR_BF16: flat ? launch_mx<MRR_BF16, true>(a, quantize, stream) : launch_mx<MRR_BF16, false>(a, quantize, stream); break;
-      default: flat ? launch_mx<MRR_F32, true>(a, quantize, stream) : launch_mx<MRR_F32, false>(a, quantize, stream); break;
+      case MRR_F16: flat ? launch_mx<MRR_F16, true>(a, quantize, large, stream) : launch_mx<MRR_F16, false>(a, quantize, large, stream); break;
+      case MRR_BF16: flat ? launch_mx<MRR_BF16, true>(a, quantize, large, stream) : launch_mx<MRR_BF16, false>(a, quantize, large, stream); break;
+      default: flat ? launch_mx<MRR_F32, true>(a, quantize, large, stream) : launch_mx<MRR_F32, false>(a, quantize, large, stream); break;
     }
     if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
   }
