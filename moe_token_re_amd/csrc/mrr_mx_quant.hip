@@ -6,9 +6,11 @@
 // Per block of 32 values: s = max(exponent field of max |x| - 2, 0), so that
 // 2^(s - 127) = 2^(floor(log2 max |x|) - 2), and q = round(x / 2^(s - 127)) to
 // e2m1. Bound by memory: a value costs its 2 or 4 bytes and 17/32 byte. A lane
-// takes 8 values (16 bytes of fp16 or bf16), the 4 lanes of a quad share a
-// block and find its maximum by two DPP steps, and the conversions are the
-// chip's scaled ones (division by the scale, round to nearest even, saturating).
+// takes 16 bytes of a row, so that what a wave reads or writes of it at once is
+// 1 KiB without gaps (with 8 fp32 values a lane 30000 x 3000 of them took 190 us
+// there and back, with 4 they take 147); the 4 or 8 lanes of a block find its maximum by
+// two or three DPP steps, and the conversions are the chip's scaled ones (division
+// by the scale, round to nearest even, saturating).
 #include "mrr_device.h"
 #include "mrr_experts.h"
 
@@ -19,7 +21,6 @@ using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
 using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 using f32x2 = float __attribute__((ext_vector_type(2)));
 
-constexpr int kUnit = 8;  // values of a lane
 constexpr int kThreads = 256;
 
 // The scale as the conversions take it: 2^(s - 127). They read the exponent
@@ -28,21 +29,27 @@ __device__ __forceinline__ float scale_float(uint32_t s) {
   return __uint_as_float(s == 0 ? 0x00400000u : s << 23);
 }
 
-__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+// The largest of the lanes of a block: 4 or 8 neighbours.
+template <int kLanes>
+__device__ __forceinline__ uint32_t block_max(uint32_t v) {
   constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E;  // quad_perm [1,0,3,2] and [2,3,0,1]
+  constexpr int kMirror8 = 0x141;              // lane i of eight takes lane 7 - i's
   v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), kSwap1, 0xf, 0xf, false)));
-  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), kSwap2, 0xf, 0xf, false)));
+  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), kSwap2, 0xf, 0xf, false)));
+  if constexpr (kLanes == 8)
+    v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), kMirror8, 0xf, 0xf, false)));
+  return v;
 }
 
-// Eight values of one type: loading, the largest |x| as fp32 bits (so that
+// A lane's values of one type, a unit: loading, the largest |x| as fp32 bits (so that
 // infinities and NaN compare above every finite value), and both conversions.
 template <int kDtype>
-struct Eight;
+struct Unit;
 
 template <>
-struct Eight<MRR_BF16> {
+struct Unit<MRR_BF16> {
   uint32_t w[4];
-  static constexpr int kBytes = 2;
+  static constexpr int kBytes = 2, kValues = 8;
   __device__ void set(int i, const uint8_t* p) {
     uint16_t v;
     __builtin_memcpy(&v, p, 2);
@@ -74,7 +81,7 @@ struct Eight<MRR_BF16> {
 };
 
 template <>
-struct Eight<MRR_F16> : Eight<MRR_BF16> {
+struct Unit<MRR_F16> : Unit<MRR_BF16> {
   __device__ uint32_t top() const {
     uint32_t m = 0;
 #pragma unroll
@@ -101,29 +108,24 @@ struct Eight<MRR_F16> : Eight<MRR_BF16> {
 };
 
 template <>
-struct Eight<MRR_F32> {
-  float w[8];
-  static constexpr int kBytes = 4;
+struct Unit<MRR_F32> {
+  float w[4];
+  static constexpr int kBytes = 4, kValues = 4;
   __device__ void set(int i, const uint8_t* p) { __builtin_memcpy(&w[i], p, 4); }
   __device__ uint32_t top() const {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(w[i]) & 0x7fffffffu);
+    for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(w[i]) & 0x7fffffffu);
     return m;
   }
   __device__ uint32_t pack(float s) const {
-    uint32_t r = 0;
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, w[0], w[1], s, 0);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, w[2], w[3], s, 1);
-    r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, w[4], w[5], s, 2);
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, w[6], w[7], s, 3);
+    const uint32_t r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0, w[0], w[1], s, 0);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, w[2], w[3], s, 1);
   }
   __device__ void unpack(uint32_t c, float s) {
     const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 0);
     const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 1);
-    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 2);
-    const f32x2 e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, s, 3);
-    w[0] = a[0], w[1] = a[1], w[2] = b[0], w[3] = b[1], w[4] = d[0], w[5] = d[1], w[6] = e[0], w[7] = e[1];
+    w[0] = a[0], w[1] = a[1], w[2] = b[0], w[3] = b[1];
   }
   __device__ void get(int i, uint8_t* p) const { __builtin_memcpy(p, &w[i], 4); }
 };
@@ -133,7 +135,7 @@ struct MxArgs {
   uint8_t* packed;
   uint8_t* scales;
   uint32_t units;          // of this launch, padding included
-  uint32_t units_per_row;  // 4 per scale byte; unused when kFlat
+  uint32_t units_per_row;  // unused when kFlat
   uint32_t H;              // unused when kFlat
 };
 
@@ -141,13 +143,13 @@ struct MxArgs {
 // without padding and no row number is needed.
 struct Place {
   uint64_t wide, packed, scale;  // element, byte and byte offsets
-  int count;                     // values of the unit that exist: 8, or fewer at a row's end
+  int count;                     // values of the unit that exist, fewer at a row's end
 };
 
-template <bool kFlat>
+template <bool kFlat, int kUnit>
 __device__ __forceinline__ Place place_of(const MxArgs& a, uint32_t u) {
   Place p;
-  p.scale = u / 4;
+  p.scale = u / (32 / kUnit);
   if constexpr (kFlat) {
     p.wide = static_cast<uint64_t>(u) * kUnit;
     p.packed = static_cast<uint64_t>(u) * (kUnit / 2);
@@ -165,36 +167,31 @@ __device__ __forceinline__ Place place_of(const MxArgs& a, uint32_t u) {
 using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 using loose4 = u32x4 __attribute__((aligned(2)));
 
-// A lane's eight wide values; kStream: past the caches.
-template <bool kStream, typename W, int n>
-__device__ __forceinline__ void load_unit(W (&w)[n], const uint8_t* p) {
-  if constexpr (kStream) {
-#pragma unroll
-    for (int i = 0; i < n / 4; ++i) {
-      const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const loose4*>(p) + i);
-      __builtin_memcpy(&w[i * 4], &v, 16);
-    }
-  } else {
-    __builtin_memcpy(w, p, sizeof(w));
-  }
+// A lane's wide values; kStream: past the caches.
+template <bool kStream, typename W>
+__device__ __forceinline__ void load_unit(W (&w)[4], const uint8_t* p) {
+  u32x4 v;
+  if constexpr (kStream)
+    v = __builtin_nontemporal_load(reinterpret_cast<const loose4*>(p));
+  else
+    v = *reinterpret_cast<const loose4*>(p);
+  __builtin_memcpy(w, &v, 16);
 }
-template <bool kStream, typename W, int n>
-__device__ __forceinline__ void store_unit(uint8_t* p, const W (&w)[n]) {
-  if constexpr (kStream) {
-#pragma unroll
-    for (int i = 0; i < n / 4; ++i) {
-      u32x4 v;
-      __builtin_memcpy(&v, &w[i * 4], 16);
-      __builtin_nontemporal_store(v, reinterpret_cast<loose4*>(p) + i);
-    }
-  } else {
-    __builtin_memcpy(p, w, sizeof(w));
-  }
+template <bool kStream, typename W>
+__device__ __forceinline__ void store_unit(uint8_t* p, const W (&w)[4]) {
+  u32x4 v;
+  __builtin_memcpy(&v, w, 16);
+  if constexpr (kStream)
+    __builtin_nontemporal_store(v, reinterpret_cast<loose4*>(p));
+  else
+    *reinterpret_cast<loose4*>(p) = v;
 }
 
 template <int kDtype, bool kFlat, int kIter, bool kStream>
 __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(MxArgs a) {
-  using V = Eight<kDtype>;
+  using V = Unit<kDtype>;
+  constexpr int kUnit = V::kValues, kLanes = 32 / kUnit;  // lanes of a block
+  using Packed = std::conditional_t<kUnit == 8, uint32_t, uint16_t>;
   const uint32_t u0 = blockIdx.x * static_cast<uint32_t>(kThreads * kIter) + threadIdx.x;
   V v[kIter];
   Place p[kIter];
@@ -202,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(MxArgs a) {
   for (int i = 0; i < kIter; ++i) {
     const uint32_t u = u0 + i * kThreads;
     v[i] = V{};
-    p[i] = place_of<kFlat>(a, u);
+    p[i] = place_of<kFlat, kUnit>(a, u);
     if (u >= a.units) p[i].count = 0;
     const uint8_t* src = a.wide + p[i].wide * V::kBytes;
     if (p[i].count == kUnit) {
@@ -214,40 +211,42 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(MxArgs a) {
   }
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
-    // units come in whole quads, so the lanes of a quad are in range together
-    const uint32_t e = quad_max(v[i].top()) >> 23;
+    // units come in whole blocks, so the lanes of a block are in range together
+    const uint32_t e = block_max<kLanes>(v[i].top()) >> 23;
     const uint32_t s = e == 255 ? 255 : e > 2 ? e - 2 : 0;
-    const uint32_t c = s == 255 ? 0 : v[i].pack(scale_float(s));
+    const Packed c = static_cast<Packed>(s == 255 ? 0 : v[i].pack(scale_float(s)));
     uint8_t* dst = a.packed + p[i].packed;
     if (p[i].count == kUnit) {
-      __builtin_memcpy(dst, &c, 4);
+      __builtin_memcpy(dst, &c, sizeof(c));
     } else {
       for (int k = 0; k < kUnit / 2; ++k)
         if (2 * k < p[i].count) dst[k] = static_cast<uint8_t>(c >> (8 * k));
     }
-    if (threadIdx.x % 4 == 0 && u0 + i * kThreads < a.units) a.scales[p[i].scale] = static_cast<uint8_t>(s);
+    if (threadIdx.x % kLanes == 0 && u0 + i * kThreads < a.units) a.scales[p[i].scale] = static_cast<uint8_t>(s);
   }
 }
 
 template <int kDtype, bool kFlat, int kIter, bool kStream>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxArgs a) {
-  using V = Eight<kDtype>;
+  using V = Unit<kDtype>;
+  constexpr int kUnit = V::kValues;
+  using Packed = std::conditional_t<kUnit == 8, uint32_t, uint16_t>;
   const uint32_t u0 = blockIdx.x * static_cast<uint32_t>(kThreads * kIter) + threadIdx.x;
-  uint32_t c[kIter];
+  Packed c[kIter];
   uint32_t s[kIter];
   Place p[kIter];
 #pragma unroll
   for (int i = 0; i < kIter; ++i) {
     const uint32_t u = u0 + i * kThreads;
-    p[i] = place_of<kFlat>(a, u);
+    p[i] = place_of<kFlat, kUnit>(a, u);
     if (u >= a.units) p[i].count = 0;
     c[i] = s[i] = 0;
     const uint8_t* src = a.packed + p[i].packed;
     if (p[i].count == kUnit) {
-      __builtin_memcpy(&c[i], src, 4);
+      __builtin_memcpy(&c[i], src, sizeof(c[i]));
     } else {
       for (int k = 0; k < kUnit / 2; ++k)
-        if (2 * k < p[i].count) c[i] |= static_cast<uint32_t>(src[k]) << (8 * k);
+        if (2 * k < p[i].count) c[i] |= static_cast<Packed>(src[k] << (8 * k));
     }
     if (p[i].count > 0) s[i] = a.scales[p[i].scale];
   }
@@ -257,7 +256,7 @@ __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(MxArgs a) {
     v.unpack(c[i], scale_float(s[i]));  // s = 255: the scale is an infinity, every value a NaN
     uint8_t* dst = a.wide + p[i].wide * V::kBytes;
     if (p[i].count == kUnit) {
-      store_unit<kStream && kDtype != MRR_F32>(dst, v.w);
+      store_unit<kStream>(dst, v.w);
     } else {
       for (int k = 0; k < kUnit; ++k)
         if (k < p[i].count) v.get(k, dst + k * V::kBytes);
@@ -271,9 +270,8 @@ constexpr int64_t kMaxUnits = int64_t(1) << 30;
 constexpr int64_t kManyUnits = int64_t(kThreads) * 2048;
 // From so many bytes of wide rows on they are read, and written, past the caches,
 // which would not hold them for a reader anyway: 16384 x 7168 bf16 rows quantised
-// and read back in 131 us by way of the caches and 89 past them (6.6 TB/s), 30000 x
-// 3000 fp32 in 220 and 191; but 4096 x 2048 fp32 in 16.5 and 20. Stores of fp32
-// stay: a lane has two vectors of them, so a store writes half lines.
+// and read back in 131 us by way of the caches and 89 past them (6.6 TB/s); but 4096
+// x 2048 fp32 in 15.4 and 19.
 constexpr int64_t kStreamBytes = int64_t(64) << 20;
 
 template <int kDtype, bool kFlat, int kIter, bool kStream>
@@ -299,7 +297,8 @@ mrr_status run_mx(const mrr_mx_args* args, bool quantize, hipStream_t stream) {
   const mrr_status st = check_mx(args, quantize);
   if (st != MRR_SUCCESS || args->rows == 0) return st;
   const int64_t w = args->wide_dtype == MRR_F32 ? 4 : 2;
-  const int64_t per_row = 4 * mx_scale_bytes(args->H);
+  const int64_t per_scale = args->wide_dtype == MRR_F32 ? 8 : 4;  // units
+  const int64_t per_row = per_scale * mx_scale_bytes(args->H);
   const bool flat = args->H % 64 == 0, large = args->rows * args->H * w >= kStreamBytes;
   const int64_t step = kMaxUnits / per_row;  // rows of a launch
   for (int64_t row = 0; row < args->rows; row += step) {
@@ -307,7 +306,7 @@ mrr_status run_mx(const mrr_mx_args* args, bool quantize, hipStream_t stream) {
     MxArgs a;
     a.wide = static_cast<uint8_t*>(args->wide) + row * args->H * w;
     a.packed = static_cast<uint8_t*>(args->packed) + row * (args->H / 2);
-    a.scales = static_cast<uint8_t*>(args->scales) + row * (per_row / 4);
+    a.scales = static_cast<uint8_t*>(args->scales) + row * (per_row / per_scale);
     a.units = static_cast<uint32_t>(rows * per_row);
     a.units_per_row = static_cast<uint32_t>(per_row);
     a.H = static_cast<uint32_t>(args->H);
