@@ -429,7 +429,8 @@ size_t mrr_few_tokens_workspace_size(int64_t T, int64_t top_k, int64_t I);
 /* The checks mrr_few_tokens() makes on the host; no HIP call. */
 mrr_status mrr_few_tokens_validate(const mrr_few_tokens_args* args, const void* workspace, size_t workspace_bytes);
 
-/* Runs it on `stream`: two kernels. */
+/* Runs it on `stream`: two kernels, or three with router_logits of more than
+ * four tokens. */
 mrr_status mrr_few_tokens(const mrr_few_tokens_args* args, void* workspace, size_t workspace_bytes,
                           struct ihipStream_t* stream);
 

@@ -1,12 +1,16 @@
 // mrr_few_tokens.hip -- a whole mixture-of-experts layer for a few tokens:
 //     h[t, j] = p[t, j] silu(Wg[e] x[t]) * (Wu[e] x[t])   for e = ids[t, j],
 //     y[t]    = sum over j of Wd[e] h[t, j].
-// Bound by reading the chosen experts' weights, once each. Two kernels, one a
-// product; for more than a few tokens a third before them finds the routing
-// (softmax and top-k of the router's logits), which every workgroup of the first
-// would otherwise find for itself. The second adds an output row's experts in one
-// workgroup, in a fixed order, so no sum crosses workgroups and results do not
-// depend on timing.
+// Bound by reading the chosen experts' weights, once each (6.3 TB/s is what a kernel
+// reaches that does nothing but read). Two kernels, one a product; for more than a
+// few tokens a third before them finds the routing (softmax and top-k of the
+// router's logits), which every workgroup of the first would otherwise find for
+// itself. The second adds an output row's experts in a fixed order, so results do
+// not depend on timing. What it measured, weights from memory: one token, 8 of 64
+// 4-bit experts, H 7168, I 2048 (187 MB): 52 us, 3.6 TB/s; 16 tokens, 6 of 64 fp16
+// experts, H 2048, I 1408: 145 us; 64 tokens, 4 of 32 4-bit experts, H 4096, I 2048
+// (430 MB): 117 us, 3.7 TB/s, of which half is issuing instructions: a chunk of
+// 4 KiB of weights takes 250 of them, 64 to widen the weights, 52 to sort lanes.
 //
 // Both feed the 16x16x32 matrix instruction with 16 weight rows and up to 16 of
 // the tokens that chose the expert. A lane reads 32 bytes of a weight row at a
@@ -14,6 +18,8 @@
 // their scale, which is exact.
 #include "mrr_device.h"
 #include "mrr_experts.h"
+
+#include <algorithm>
 
 namespace mrr {
 namespace {
@@ -42,6 +48,8 @@ struct FewArgs {
   uint8_t* y;
   int32_t* ws_ids;
   float* ws_weight;
+  int32_t* ws_arrived;  // of a run of output rows: the workgroups that are done
+  f32x4* ws_part;
   uint8_t* ws_h;
   int32_t T, H, E, I, k;
   int32_t renormalize;
@@ -244,7 +252,7 @@ __device__ __forceinline__ void make_plan(Plan& p, int slots, int E) {
 // two neighbouring lanes would read neighbouring bytes, and each lane's 16 bytes
 // would take a cycle of the address unit of their own. So lane 4 r + g reads piece
 // g or 4 + g of row r, and sort_lanes() moves it to lane 16 g + r afterwards
-// (64 tokens of 4-bit experts, first kernel: 107 us like that).
+// (64 tokens, 4 of 32 4-bit experts, H 4096: the layer took 172 us before, 129 so).
 template <bool kMx>
 struct Weights {
   u32x4 v[2];
@@ -548,6 +556,8 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void few_up_kernel(FewArgs a) {
   make_plan<kUpWaves>(s, slots, a.E);
   if (blockIdx.x == 0 && (a.logits == nullptr || a.T <= kSelfRouted))  // for the second kernel
     for (int i = tid; i < slots; i += kThreads) a.ws_ids[i] = s.id[i];
+  if (blockIdx.x == 0)
+    for (int i = tid; i < kFewMostRuns; i += kThreads) a.ws_arrived[i] = 0;
 
   // This workgroup's units: row tile `tile` of active expert `n`, its tokens from
   // place `at` on.
@@ -649,11 +659,32 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void few_up_kernel(FewArgs a) {
   }
 }
 
-// The second kernel: a workgroup computes 16 rows of y for up to 64 tokens.
-// Its waves take the experts in turn, or parts of their rows when the experts
-// are few, for 16 kTiles of the expert's tokens at a time, and add the results
-// to sums of their own in LDS: each in its fixed order, so that nothing depends
-// on timing.
+// Values that workgroups on different XCDs share: past the XCD's own L2 both ways.
+// (A fence of the whole L2 in their place made the kernel take 100 us more.)
+__device__ __forceinline__ void store_shared(f32x4* p, f32x4 v) {
+  uint64_t w[2];
+  __builtin_memcpy(w, &v, 16);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p) + i, w[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ f32x4 load_shared(f32x4* p) {
+  uint64_t w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    w[i] = __hip_atomic_load(reinterpret_cast<uint64_t*>(p) + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  f32x4 v;
+  __builtin_memcpy(&v, w, 16);
+  return v;
+}
+
+// The second kernel: 16 rows of y, a run, for up to 64 tokens. Its waves take the
+// experts in turn, or parts of their rows when the experts are few, for 16 kTiles
+// of the expert's tokens at a time, and add the results to sums of their own in
+// LDS: each in its fixed order. Where there are fewer runs than the chip holds
+// workgroups, a run has several (blockIdx.z), which share the experts; each leaves
+// its sums in the workspace, and the last one to arrive adds them, in their order.
+// So nothing depends on timing.
 template <bool kMx, bool kBf16, int kTiles, bool kSort, int kWaves>
 __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -671,7 +702,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
   const Rows all = make_rows<kMx>(a.ws_h, a.T * a.k * a.I * 2, a.I);
   const int chunks = (all.pieces + 7) / 8;
   // parts of an expert's rows: enough for two a wave, of two chunks at least
-  const int wanted = (2 * kWaves + s.experts - 1) / max(s.experts, 1);
+  const int waves = kWaves * static_cast<int>(gridDim.z), first_unit = blockIdx.z * kWaves + wave;
+  const int wanted = (2 * waves + s.experts - 1) / max(s.experts, 1);
   const int part_chunks = max(2, (chunks + wanted - 1) / wanted);
   const int parts = (chunks + part_chunks - 1) / part_chunks;
   // This wave's units: part `part` of active expert `n`, its tokens from place
@@ -690,7 +722,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
   auto advance = [&](Unit& u) {
     u.at += 16 * kTiles;
     if (u.at < u.end) return;
-    u.unit += kWaves;
+    u.unit += waves;
     begin(u);
   };
   auto length = [&](const Unit& u) { return min(part_chunks, chunks - u.part * part_chunks); };
@@ -709,7 +741,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
     p.left = length(u);
     p.step = 1;
   };
-  Unit u{wave, 0, 0, 0, 0};
+  Unit u{first_unit, 0, 0, 0, 0};
   if (u.unit < units) {
     begin(u);
     Unit ahead = u;
@@ -738,11 +770,33 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
     }
   }
   __syncthreads();
+  auto store = [&](int i, f32x4 sum) {
+    store_row4<kBf16>(a.y + (static_cast<int64_t>(t0 + i / 4) * a.H + blockIdx.x * kRows + i % 4 * 4) * 2, sum);
+  };
+  // [workgroups of a run][runs][tokens][4]; the last run of tokens may have fewer
+  const int run = blockIdx.y * gridDim.x + blockIdx.x, pitch = min(a.T, kDownTokens) * 4;
+  f32x4* part = a.ws_part + static_cast<int64_t>(run) * pitch;
+  const int64_t apart = static_cast<int64_t>(gridDim.y * gridDim.x) * pitch;
   for (int i = tid; i < tokens * 4; i += kThreads) {
     f32x4 sum = sums[i];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) sum += sums[w * tokens * 4 + i];
-    store_row4<kBf16>(a.y + (static_cast<int64_t>(t0 + i / 4) * a.H + blockIdx.x * kRows + i % 4 * 4) * 2, sum);
+    if (gridDim.z == 1)
+      store(i, sum);
+    else
+      store_shared(part + blockIdx.z * apart + i, sum);
+  }
+  if (gridDim.z == 1) return;
+  // the sums are where every XCD sees them before this workgroup is counted
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (tid == 0) *s.wave_sum = atomicAdd(a.ws_arrived + run, 1);
+  __syncthreads();
+  if (*s.wave_sum != static_cast<int>(gridDim.z) - 1) return;
+  for (int i = tid; i < tokens * 4; i += kThreads) {
+    f32x4 sum = load_shared(part + i);
+    for (unsigned z = 1; z < gridDim.z; ++z) sum += load_shared(part + z * apart + i);
+    store(i, sum);
   }
 }
 
@@ -760,12 +814,21 @@ mrr_status launch_few_tiles(const FewArgs& a, hipStream_t stream) {
                      dim3(kUpWaves * 64), up_part_bytes(kTiles) + plan_bytes(slots, a.E), stream, a);
   if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
   const int tokens = a.T < kDownTokens ? a.T : kDownTokens;
-  const dim3 grid(a.H / kRows, (a.T + kDownTokens - 1) / kDownTokens);
+  dim3 grid(a.H / kRows, (a.T + kDownTokens - 1) / kDownTokens);
   const size_t plan = plan_bytes(tokens * a.k, a.E);
   // Up to a workgroup a CU eight waves, else four, so that the chip holds them all
   // (one token, 8 of 64 4-bit experts, H 7168: 45.6 us with eight, 42.1 with four;
   // 64 tokens, 4 of 32, H 4096: 128.8 and 133.7).
-  if (grid.x * grid.y <= 256)
+  const int runs = static_cast<int>(grid.x * grid.y);
+  // Workgroups of a run: as many as the chip holds (two a CU, by their registers),
+  // with four chunks a wave at least, more tokens counting as more chunks (16 tokens,
+  // 6 of 64 fp16 experts, H 2048: 147 us with one, 134 with four; 16 tokens, 8 of 64
+  // 4-bit experts, H 1024: 38 and 29).
+  const int used = slots < a.E ? slots : a.E, chunks = ((kMx ? a.I / 32 : a.I / 8) + 7) / 8;
+  const int steps = used * chunks + slots * chunks / 8;
+  const int most_runs = static_cast<int>(kTiles == 1 ? kFewMostRuns : kFewMostRuns / 2);
+  grid.z = std::max(1, std::min(most_runs / runs, steps / 32));
+  if (runs <= 256)
     hipLaunchKernelGGL((few_down_kernel<kMx, kBf16, kTiles, kSort, 8>), grid, dim3(512),
                        down_sum_bytes(tokens, 8) + plan, stream, a);
   else
@@ -803,6 +866,8 @@ extern "C" mrr_status mrr_few_tokens(const mrr_few_tokens_args* args, void* work
   a.y = static_cast<uint8_t*>(args->y);
   a.ws_ids = reinterpret_cast<int32_t*>(ws + l.ids);
   a.ws_weight = reinterpret_cast<float*>(ws + l.weight);
+  a.ws_arrived = reinterpret_cast<int32_t*>(ws + l.arrived);
+  a.ws_part = reinterpret_cast<mrr::f32x4*>(ws + l.part);
   a.ws_h = ws + l.h;
   a.T = static_cast<int32_t>(args->T);
   a.H = static_cast<int32_t>(args->H);

@@ -217,8 +217,8 @@ def moe_few_tokens(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, *
                    expert_weight: Optional[torch.Tensor] = None, gate_up_scales: Optional[torch.Tensor] = None,
                    down_scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
                    workspace: Optional[torch.Tensor] = None):
-    """A whole mixture-of-experts layer for a few tokens (at most 128), in two
-    kernels: y[t] = sum over the chosen experts of p * down @ (silu(gate @ x[t]) * (up @ x[t])).
+    """A whole mixture-of-experts layer for a few tokens (at most 128), in two or
+    three kernels: y[t] = sum over the chosen experts of p * down @ (silu(gate @ x[t]) * (up @ x[t])).
 
     x is [T, H] float16 or bfloat16. gate_up [E, 2 I, H] (the gate's rows, then
     up's) and down [E, H, I] have x's dtype, or are microscaled 4-bit rows
