@@ -196,6 +196,36 @@ __device__ __forceinline__ Plan carve(uint8_t* lds, int slots, int E) {
   return p;
 }
 
+// The plan of a few slots, of which a lane has one's expert (-1: none): by every
+// wave alone, without a barrier, as all of them write the same (one token, 2 of 16
+// experts, H 1024: the layer takes 9.0 us so and 10.1 by the counting below; with 64
+// slots it is the other way, 31.7 and 25.8).
+constexpr int kSmallPlan = 16;
+static_assert(kSmallPlan >= kFewMaxTopK, "one token's slots");
+__device__ __forceinline__ void make_small_plan(Plan& p, int expert, int slots) {
+  const int lane = threadIdx.x % 64;
+  int rank = 0, lead = lane, count = 0;  // among the expert's slots; its first slot; how many it has
+  for (int i = slots - 1; i >= 0; --i) {
+    const int other = __builtin_amdgcn_readlane(expert, i);
+    const bool same = other >= 0 && other == expert;
+    rank += same && i < lane;
+    count += same;
+    if (same) lead = i;
+  }
+  const bool leads = expert >= 0 && lead == lane;
+  const uint64_t leaders = __ballot(leads);
+  const int which = __popcll(leaders & ((uint64_t(1) << lane) - 1));
+  const int first = static_cast<int>(wave_scan_u32(leads ? count : 0)) - (leads ? count : 0);
+  p.experts = __popcll(leaders);
+  const int place = __shfl(first, lead) + rank;
+  if (leads) {
+    p.active[which] = static_cast<int16_t>(expert);
+    p.first[which] = static_cast<int16_t>(first);
+    if (which == p.experts - 1) p.first[p.experts] = static_cast<int16_t>(first + count);
+  }
+  if (expert >= 0) p.slot[place] = static_cast<int16_t>(lane);
+}
+
 // From p.id (written, not yet waited for) the rest of the plan, by all kWaves
 // waves of the workgroup.
 template <int kWaves>
@@ -204,6 +234,10 @@ __device__ __forceinline__ void make_plan(Plan& p, int slots, int E) {
   const int tid = threadIdx.x;
   for (int e = tid; e < E; e += kThreads) p.count[e] = 0;
   __syncthreads();
+  if (slots <= kSmallPlan) {
+    make_small_plan(p, tid % 64 < slots ? p.id[tid % 64] : -1, slots);
+    return;
+  }
   for (int i = tid; i < slots; i += kThreads)
     if (p.id[i] >= 0) atomicAdd(&p.count[p.id[i]], 1);
   __syncthreads();
@@ -519,7 +553,16 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void few_up_kernel(FewArgs a) {
   const int slots = a.T * a.k, tid = threadIdx.x, lane = tid % 64;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
   Plan s = carve(lds + up_part_bytes(kTiles), slots, a.E);
-  if (a.logits != nullptr && a.T <= kSelfRouted) {
+  if (a.logits != nullptr && a.T == 1) {  // by every wave, so that none waits
+    int id;
+    float weight;
+    route_token(a, 0, lane, &id, &weight);
+    if (lane < a.k) {
+      s.id[lane] = static_cast<int16_t>(id);
+      s.weight[lane] = weight;
+    }
+    make_small_plan(s, lane < a.k ? id : -1, slots);
+  } else if (a.logits != nullptr && a.T <= kSelfRouted) {
     for (int t = wave; t < a.T; t += kUpWaves) {
       int id;
       float weight;
@@ -553,7 +596,7 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void few_up_kernel(FewArgs a) {
       s.weight[i] = weight;
     }
   }
-  make_plan<kUpWaves>(s, slots, a.E);
+  if (a.logits == nullptr || a.T > 1) make_plan<kUpWaves>(s, slots, a.E);
   if (blockIdx.x == 0 && (a.logits == nullptr || a.T <= kSelfRouted))  // for the second kernel
     for (int i = tid; i < slots; i += kThreads) a.ws_ids[i] = s.id[i];
   if (blockIdx.x == 0)
@@ -695,9 +738,13 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
   f32x4* sums = reinterpret_cast<f32x4*>(lds);  // [waves][tokens][4 groups]
   f32x4* mine = sums + wave * tokens * 4;
   Plan s = carve(lds + down_sum_bytes(tokens, kWaves), slots, a.E);
-  for (int i = tid; i < slots; i += kThreads) s.id[i] = static_cast<int16_t>(a.ws_ids[t0 * a.k + i]);
   for (int i = lane; i < tokens * 4; i += 64) mine[i] = f32x4{0, 0, 0, 0};
-  make_plan<kWaves>(s, slots, a.E);
+  if (slots <= kSmallPlan) {
+    make_small_plan(s, lane < slots ? a.ws_ids[t0 * a.k + lane] : -1, slots);
+  } else {
+    for (int i = tid; i < slots; i += kThreads) s.id[i] = static_cast<int16_t>(a.ws_ids[t0 * a.k + i]);
+    make_plan<kWaves>(s, slots, a.E);
+  }
 
   const Rows all = make_rows<kMx>(a.ws_h, a.T * a.k * a.I * 2, a.I);
   const int chunks = (all.pieces + 7) / 8;
