@@ -7,8 +7,8 @@
 // router's logits), which every workgroup of the first would otherwise find for
 // itself. The second adds an output row's experts in a fixed order, so results do
 // not depend on timing. What it measured, weights from memory: one token, 8 of 64
-// 4-bit experts, H 7168, I 2048 (187 MB): 52 us, 3.6 TB/s; 16 tokens, 6 of 64 fp16
-// experts, H 2048, I 1408: 145 us; 64 tokens, 4 of 32 4-bit experts, H 4096, I 2048
+// 4-bit experts, H 7168, I 2048 (187 MB): 51 us, 3.6 TB/s; 16 tokens, 6 of 64 fp16
+// experts, H 2048, I 1408: 146 us, 5.2 TB/s; 64 tokens, 4 of 32 4-bit experts, H 4096, I 2048
 // (430 MB): 117 us, 3.7 TB/s, of which half is issuing instructions: a chunk of
 // 4 KiB of weights takes 250 of them, 64 to widen the weights, 52 to sort lanes.
 //
@@ -867,14 +867,14 @@ mrr_status launch_few_tiles(const FewArgs& a, hipStream_t stream) {
   // (one token, 8 of 64 4-bit experts, H 7168: 45.6 us with eight, 42.1 with four;
   // 64 tokens, 4 of 32, H 4096: 128.8 and 133.7).
   const int runs = static_cast<int>(grid.x * grid.y);
-  // Workgroups of a run: as many as the chip holds (two a CU, by their registers),
-  // with four chunks a wave at least, more tokens counting as more chunks (16 tokens,
+  // Workgroups of a run: with fewer runs than half the CUs as many as the chip holds
+  // (two a CU, by their registers), with four chunks a wave at least, more tokens counting as more chunks (16 tokens,
   // 6 of 64 fp16 experts, H 2048: 147 us with one, 134 with four; 16 tokens, 8 of 64
   // 4-bit experts, H 1024: 38 and 29).
   const int used = slots < a.E ? slots : a.E, chunks = ((kMx ? a.I / 32 : a.I / 8) + 7) / 8;
   const int steps = used * chunks + slots * chunks / 8;
   const int most_runs = static_cast<int>(kTiles == 1 ? kFewMostRuns : kFewMostRuns / 2);
-  grid.z = std::max(1, std::min(most_runs / runs, steps / 32));
+  if (runs <= 128) grid.z = std::max(1, std::min(most_runs / runs, steps / 32));
   if (runs <= 256)
     hipLaunchKernelGGL((few_down_kernel<kMx, kBf16, kTiles, kSort, 8>), grid, dim3(512),
                        down_sum_bytes(tokens, 8) + plan, stream, a);
