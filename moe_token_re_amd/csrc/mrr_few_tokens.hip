@@ -479,8 +479,10 @@ __device__ __forceinline__ void store_row4(uint8_t* p, f32x4 v) {
 // multiplied, also the first one of the next sum; there is no branch over loads, so
 // that the wait for one chunk does not wait for the next. The chunk that a row ends
 // in is read as its last eight pieces, and those that were counted before are cut
-// (rows of fewer than eight pieces: those that follow). kSort: the tokens are read by neighbouring lanes too; a few tokens cost
-// less as they are. `next` moves a place to the next sum's first chunk.
+// (rows of fewer than eight pieces: those that follow). kSort: the tokens are read
+// by neighbouring lanes too; up to four cost less as they are (one token, 8 of 64
+// 4-bit experts, H 7168: 48.7 us so and 56.2 sorted). `next` moves a place to the
+// next sum's first chunk.
 template <bool kMx, bool kBf16, int kTiles, bool kSort, int kParts>
 struct Stream {
   Weights<kMx> w[2][kParts];
@@ -868,9 +870,9 @@ mrr_status launch_few_tiles(const FewArgs& a, hipStream_t stream) {
   // 64 tokens, 4 of 32, H 4096: 128.8 and 133.7).
   const int runs = static_cast<int>(grid.x * grid.y);
   // Workgroups of a run: with fewer runs than half the CUs as many as the chip holds
-  // (two a CU, by their registers), with four chunks a wave at least, more tokens counting as more chunks (16 tokens,
-  // 6 of 64 fp16 experts, H 2048: 147 us with one, 134 with four; 16 tokens, 8 of 64
-  // 4-bit experts, H 1024: 38 and 29).
+  // (two a CU, by their registers), with four chunks a wave at least, more tokens
+  // counting as more chunks (16 tokens, 6 of 64 fp16 experts, H 2048: 147 us with one,
+  // 134 with four; 16 tokens, 8 of 64 4-bit experts, H 1024: 38 and 29).
   const int used = slots < a.E ? slots : a.E, chunks = ((kMx ? a.I / 32 : a.I / 8) + 7) / 8;
   const int steps = used * chunks + slots * chunks / 8;
   const int most_runs = static_cast<int>(kTiles == 1 ? kFewMostRuns : kFewMostRuns / 2);
