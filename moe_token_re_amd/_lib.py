@@ -217,6 +217,8 @@ def binding():
     global _binding
     if _binding is None:
         load()
+        import torch  # noqa: F401  (the binding needs its libraries, wherever they are)
+
         try:
             from . import _mrr_torch
         except ImportError as e:

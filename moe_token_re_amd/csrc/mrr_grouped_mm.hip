@@ -545,9 +545,10 @@ __global__ __launch_bounds__(64 * kWM * kWN, 2) void grouped_mm_kernel(GroupedAr
     if (works) {
       auto store = [&](auto* type) {
         using T = std::remove_pointer_t<decltype(type)>;
-        store_tile<T, kFM, kFN, kGated, kStage / kWaves, kBM * kBN >= 65536>(acc, lds + (slot == 0 ? kStages - 1 : slot - 1) * kStage + wave * (kStage / kWaves),
-                                        static_cast<T*>(a.out), a.row_weight, t.row, wm * kFM * 32, t.rows,
-                                        t.n * kCols + wn * (kCols / kWN), n_end);
+        uint8_t* free_slot = lds + (slot == 0 ? kStages - 1 : slot - 1) * kStage;
+        store_tile<T, kFM, kFN, kGated, kStage / kWaves, kBM * kBN >= 65536>(
+            acc, free_slot + wave * (kStage / kWaves), static_cast<T*>(a.out), a.row_weight, t.row, wm * kFM * 32, t.rows,
+            t.n * kCols + wn * (kCols / kWN), n_end);
       };
       if (a.out_dtype == MRR_BF16)
         store(static_cast<__bf16*>(nullptr));

@@ -293,6 +293,14 @@ void launch_mx(const MxArgs& a, bool quantize, bool large, hipStream_t stream) {
     launch_kernel<kDtype, kFlat, 4, false>(a, quantize, stream);
 }
 
+template <int kDtype>
+void launch_dtype(const MxArgs& a, bool flat, bool quantize, bool large, hipStream_t stream) {
+  if (flat)
+    launch_mx<kDtype, true>(a, quantize, large, stream);
+  else
+    launch_mx<kDtype, false>(a, quantize, large, stream);
+}
+
 mrr_status run_mx(const mrr_mx_args* args, bool quantize, hipStream_t stream) {
   const mrr_status st = check_mx(args, quantize);
   if (st != MRR_SUCCESS || args->rows == 0) return st;
@@ -311,9 +319,9 @@ mrr_status run_mx(const mrr_mx_args* args, bool quantize, hipStream_t stream) {
     a.units_per_row = static_cast<uint32_t>(per_row);
     a.H = static_cast<uint32_t>(args->H);
     switch (args->wide_dtype) {
-      case MRR_F16: flat ? launch_mx<MRR_F16, true>(a, quantize, large, stream) : launch_mx<MRR_F16, false>(a, quantize, large, stream); break;
-      case MRR_BF16: flat ? launch_mx<MRR_BF16, true>(a, quantize, large, stream) : launch_mx<MRR_BF16, false>(a, quantize, large, stream); break;
-      default: flat ? launch_mx<MRR_F32, true>(a, quantize, large, stream) : launch_mx<MRR_F32, false>(a, quantize, large, stream); break;
+      case MRR_F16: launch_dtype<MRR_F16>(a, flat, quantize, large, stream); break;
+      case MRR_BF16: launch_dtype<MRR_BF16>(a, flat, quantize, large, stream); break;
+      default: launch_dtype<MRR_F32>(a, flat, quantize, large, stream); break;
     }
     if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
   }

@@ -1,6 +1,8 @@
 """The native binding of the experts' operators without a GPU: it is built from
 these sources, and it leaves whatever is not on the GPU to the Python code."""
 import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -22,3 +24,9 @@ def test_binding_leaves_cpu_tensors_alone():
     assert b.few_tokens(x, x, x, x, 1, True, None, None, None, None) is None
     for call in (b.quantize, b.dequantize, b.grouped_mm, b.few_tokens):
         assert call() is None and call(None) is None and call(1, 2, 3) is None
+
+
+def test_binding_loads_torch_by_itself():
+    code = "from moe_token_re_amd import _lib; _lib.binding()"
+    root = os.path.dirname(os.path.dirname(os.path.abspath(_lib.__file__)))
+    assert subprocess.run([sys.executable, "-c", code], cwd=root, timeout=120).returncode == 0
