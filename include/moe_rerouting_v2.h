@@ -397,8 +397,8 @@ mrr_status mrr_mx_grouped_mm(const mrr_grouped_mm_args* args, void* workspace, s
  *   - expert_ids and expert_weight [T, top_k]: p as given. An id outside
  *     [0, E) chooses nothing (an expert of another rank); an expert that a
  *     token names twice counts with the sum of the two weights.
- * p silu(g) u is rounded once to x's type between the two products; sums are
- * kept in 32 bits.
+ * Sums are kept in 32 bits; p silu(g) u is held as the sum of two bf16 values
+ * between the two products, off by at most 2^-15 of it.
  */
 typedef struct mrr_few_tokens_args {
   const void* x;                   /* [T, H], 16-byte aligned */

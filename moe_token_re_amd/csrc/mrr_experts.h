@@ -14,24 +14,26 @@ inline int64_t mx_scale_bytes(int64_t n) { return 2 * ((n + 63) / 64); }
 constexpr int64_t kFewMaxTopK = 16;
 constexpr int64_t kFewMaxExperts = 1024;
 
-// Most runs of 16 output rows, over all parts of the experts, that the few-token
-// layer's second kernel computes at once.
+// Most runs of 16 or 32 output rows, over all parts of the experts, that the
+// few-token layer's second kernel computes at once.
 constexpr int64_t kFewMostRuns = 512;
 
-// Workspace of the few-token layer: the routing [T, k] (int32 expert, or -1, and
-// float weight), a count for each run, 16 partial sums in fp32 for each run and
-// token, and h [T k, I]; each part rounded up to 256 bytes.
+// Workspace of the few-token layer: the routing [T, k] (int32 expert, or -1, float
+// weight, and in 32 bits where its h lies), a count for each run, 32
+// partial sums in fp32 for each run and token, and h [T k, I] of 4 bytes a value;
+// each part rounded up to 256 bytes.
 struct FewLayout {
-  size_t ids, weight, arrived, part, h, bytes;
+  size_t ids, weight, between, arrived, part, h, bytes;
 };
 inline FewLayout few_layout(int64_t T, int64_t k, int64_t I) {
   FewLayout l{};
   l.ids = 0;
   l.weight = round_up(4 * static_cast<size_t>(T * k), 256);
-  l.arrived = 2 * l.weight;
+  l.between = 2 * l.weight;
+  l.arrived = 3 * l.weight;
   l.part = l.arrived + 4 * static_cast<size_t>(kFewMostRuns);
-  l.h = l.part + static_cast<size_t>(kFewMostRuns * 16 * 4 * T);
-  l.bytes = l.h + round_up(2 * static_cast<size_t>(T * k * I), 256) + 256;
+  l.h = l.part + static_cast<size_t>(kFewMostRuns * 32 * 4 * T);
+  l.bytes = l.h + round_up(4 * static_cast<size_t>(T * k * I), 256) + 256;
   return l;
 }
 

@@ -12,10 +12,15 @@
 // (430 MB): 117 us, 3.7 TB/s, of which half is issuing instructions: a chunk of
 // 4 KiB of weights takes 250 of them, 64 to widen the weights, 52 to sort lanes.
 //
-// Both feed the 16x16x32 matrix instruction with 16 weight rows and up to 16 of
-// the tokens that chose the expert. A lane reads 32 bytes of a weight row at a
-// time: 16 16-bit values, or two blocks of 32 4-bit values, widened to bf16 with
-// their scale, which is exact.
+// Both feed the matrix instructions with 16 weight rows and up to 16 of the tokens
+// that chose the expert. A lane reads 32 bytes of a weight row at a time: 16 16-bit
+// values, or two blocks of 32 4-bit values, widened to bf16 with their scale, which
+// is exact. x has 16 bits as it comes. h has no such type, and 16 bits would round it
+// or, fp16, end at 65504: it is held as two bf16 values, hi + lo, off by at most 2^-15.
+// They take two columns of the instruction's 16, so that 8 tokens cost what 16 of one
+// column would; fp16 weights are multiplied as the two bf16 values that they are the
+// sum of. (fp32 products, 16x16x4, would need neither: 64 tokens, 8 of 16 bf16 experts,
+// H 4096, took 289 us with them and 267 so, at one run of rows a wave.)
 #include "mrr_device.h"
 #include "mrr_experts.h"
 
@@ -28,12 +33,16 @@ using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
 using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
+using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
 using f16x8 = _Float16 __attribute__((ext_vector_type(8)));
 
 constexpr int kMaxExperts = static_cast<int>(kFewMaxExperts);
+constexpr int kExpertBits = 10;   // of an expert's number
+static_assert(kMaxExperts == 1 << kExpertBits, "all of them");
 constexpr int kUpWaves = 4;       // first kernel: they share a unit's rows, each a part of their length
 constexpr int kRows = 16;         // weight rows of a fragment
 constexpr int kDownTokens = 64;   // tokens of a workgroup of the second kernel
+constexpr int kPlaces = 8;        // tokens of a tile there: a column for hi, one for lo
 constexpr int kSelfRouted = 4;    // so many tokens, a wave each, the first kernel routes itself
 
 struct FewArgs {
@@ -48,6 +57,7 @@ struct FewArgs {
   uint8_t* y;
   int32_t* ws_ids;
   float* ws_weight;
+  int32_t* ws_between;  // of a choice: where its h lies (Between)
   int32_t* ws_arrived;  // of a run of output rows: the workgroups that are done
   f32x4* ws_part;
   uint8_t* ws_h;
@@ -55,8 +65,10 @@ struct FewArgs {
   int32_t renormalize;
 };
 
-inline __host__ __device__ size_t up_part_bytes(int tiles) { return 2 * sizeof(f32x4) * kUpWaves * 2 * tiles * 64; }
-inline __host__ __device__ size_t down_sum_bytes(int tokens, int waves) { return sizeof(f32x4) * waves * tokens * 4; }
+inline __host__ __device__ constexpr size_t up_part_bytes(int tiles) { return 2 * sizeof(f32x4) * kUpWaves * 2 * tiles * 64; }
+inline __host__ __device__ constexpr size_t down_sum_bytes(int tokens, int waves, int parts) {
+  return sizeof(f32x4) * waves * tokens * 4 * parts;
+}
 
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   constexpr int kRowShr1 = 0x111, kRowShr2 = 0x112, kRowShr4 = 0x114, kRowShr8 = 0x118;
@@ -173,22 +185,34 @@ struct Plan {
   int32_t* wave_sum;  // [16]
   float* weight;      // [slots] (first kernel)
   int16_t* id;        // [slots]: the expert of token t's choice j, at t k + j; -1: none
-  int16_t* slot;      // [slots]: the slots by expert
+  int16_t* slot;      // [slots]: the slots by expert, and in their order among an expert's
+  int32_t* between;   // [slots]: where a slot's h lies (second kernel)
   int16_t* active;    // [E]: the experts that have tokens
   int16_t* first;     // [E + 1]: of an active expert: its first place in `slot`
   int experts;        // that have tokens
 };
 
-inline __host__ __device__ size_t plan_bytes(int slots, int E) {
-  return (4 * (E + 16 + slots) + 2 * (2 * slots + 2 * E + 1) + 15) / 16 * 16;
+inline __host__ __device__ constexpr size_t plan_bytes(int slots, int E) {
+  return (4 * (E + 16 + 2 * slots) + 2 * (2 * slots + 2 * E + 1) + 15) / 16 * 16;
 }
+
+// What a workgroup may have without asking for more; the first kernel takes two tiles
+// of tokens with more than 16 choices an expert alone.
+constexpr size_t kMostLds = 64 * 1024;
+constexpr int kMostSlots = MRR_FEW_TOKENS_MAX * static_cast<int>(kFewMaxTopK);
+static_assert(up_part_bytes(1) + plan_bytes(kMostSlots, kMaxExperts) <= kMostLds, "first kernel");
+static_assert(up_part_bytes(2) + plan_bytes(kMostSlots, kMostSlots / 16) <= kMostLds, "first kernel, two tiles");
+static_assert(down_sum_bytes(kDownTokens, 8, 1) + plan_bytes(kDownTokens * kFewMaxTopK, kMaxExperts) <= kMostLds &&
+                  down_sum_bytes(kDownTokens, 4, 2) <= down_sum_bytes(kDownTokens, 8, 1),
+              "second kernel");
 
 __device__ __forceinline__ Plan carve(uint8_t* lds, int slots, int E) {
   Plan p;
   p.count = reinterpret_cast<int32_t*>(lds);
   p.wave_sum = p.count + E;
   p.weight = reinterpret_cast<float*>(p.wave_sum + 16);
-  p.id = reinterpret_cast<int16_t*>(p.weight + slots);
+  p.between = reinterpret_cast<int32_t*>(p.weight + slots);
+  p.id = reinterpret_cast<int16_t*>(p.between + slots);
   p.slot = p.id + slots;
   p.active = p.slot + slots;
   p.first = p.active + E;
@@ -272,10 +296,25 @@ __device__ __forceinline__ void make_plan(Plan& p, int slots, int E) {
   p.experts = __builtin_amdgcn_readfirstlane(all >> 16);
   if (tid == 0) p.first[p.experts] = static_cast<int16_t>(all & 0xffff);
   __syncthreads();
-  // the order within an expert does not matter: a token's sums are its own
-  for (int i = tid; i < slots; i += kThreads) {
-    const int e = p.id[i];
-    if (e >= 0) p.slot[atomicAdd(&p.count[e], 1)] = static_cast<int16_t>(i);
+  // An expert's slots in their order, so that all workgroups agree on their places:
+  // one wave, 64 slots at a time. The lanes of the same expert are found by its ten
+  // bits.
+  if (tid < 64) {
+    for (int i0 = 0; i0 < slots; i0 += 64) {
+      const int i = i0 + tid, e = i < slots ? p.id[i] : -1;
+      uint64_t same = __ballot(e >= 0);
+#pragma unroll
+      for (int bit = 0; bit < kExpertBits; ++bit) {
+        const bool set = e >> bit & 1;
+        const uint64_t with = __ballot(set);
+        same &= set ? with : ~with;
+      }
+      if (e >= 0) {
+        const int rank = __popcll(same & ((uint64_t(1) << tid) - 1)), first = p.count[e];
+        p.slot[first + rank] = static_cast<int16_t>(i);
+        if (rank == 0) p.count[e] = first + __popcll(same);
+      }
+    }
   }
   __syncthreads();
 }
@@ -293,11 +332,37 @@ struct Weights {
   uint32_t scale[2];  // of the row's eight pieces
 };
 
+// The tokens' side of a product: rows of x as they are, the same read by neighbouring
+// lanes (kSorted, below), or h as the first kernel left it.
+enum class From { kRows, kSorted, kBetween };
+
 // The tokens' values that go with a chunk, by products of 8 values a lane.
-template <bool kMx, int kTiles>
+template <bool kMx, int kTiles, From kFrom>
 struct Tokens {
   u32x4 v[kTiles][kMx ? 8 : 2];
 };
+
+// Where the h of a token's choice of an expert lies in the workspace: the `count`
+// choices of an expert, from the `first` place on, are [I / 8][hi, lo][count][8] in
+// bf16, so that the lanes of its tokens read bytes that follow each other, in the
+// order in which the instruction wants them, and an expert's lines hold nothing else.
+// (With [I / 8][places][8] for all experts together two tokens have 32 bytes of a
+// line: 16 tokens, 6 of 64 fp16 experts, took 155 us then, 148 so.)
+struct Between {
+  uint32_t first, count, rank;
+
+  __device__ __forceinline__ int32_t packed() const { return static_cast<int32_t>(first | count << 12 | rank << 20); }
+  static __device__ __forceinline__ Between of(int32_t v) {
+    const uint32_t u = static_cast<uint32_t>(v);
+    return {u & 0xfff, u >> 12 & 0xff, u >> 20};
+  }
+  __device__ __forceinline__ uint32_t pitch() const { return count * 32; }  // of 8 columns
+  // The offset of columns 8 group .. 8 group + 7, of hi or lo.
+  __device__ __forceinline__ uint32_t at(int I, int group, int lo) const {
+    return first * I * 4 + group * pitch() + (lo * count + rank) * 16;
+  }
+};
+static_assert(MRR_FEW_TOKENS_MAX < 256 && MRR_FEW_TOKENS_MAX * kFewMaxTopK < 4096, "Between::packed");
 
 template <bool kMx>
 __device__ __forceinline__ int row_bytes(int n) { return kMx ? n / 2 : n * 2; }
@@ -327,6 +392,7 @@ struct Place {
   Buffer rows[kParts];            // the 16 rows
   const uint8_t* scales[kParts];  // of the 16 rows; the same for all lanes
   uint32_t x[kTiles];             // what the lane reads of a chunk 0 in the tokens' buffer; kOutside: nothing
+  uint32_t pitch;                 // h: bytes of 8 columns
   int c, left, step;
 };
 
@@ -364,12 +430,18 @@ __device__ __forceinline__ void load_weights(Weights<kMx>& w, Buffer rows, const
 
 // The same of the tokens' rows. Of 16-bit values a piece of 4-bit weights takes
 // 64 bytes: four lanes' worth.
-template <bool kMx, int kTiles>
-__device__ __forceinline__ void load_tokens(Tokens<kMx, kTiles>& x, const uint32_t (&at)[kTiles], const Rows& all, int q) {
+template <bool kMx, int kTiles, From kFrom>
+__device__ __forceinline__ void load_tokens(Tokens<kMx, kTiles, kFrom>& x, const uint32_t (&at)[kTiles], const Rows& all,
+                                            int q, uint32_t pitch) {
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
-    for (int i = 0; i < (kMx ? 8 : 2); ++i) x.v[t][i] = load16(all.x, at[t] + i * 64, q * (kMx ? 64 : 16));
+    for (int i = 0; i < (kMx ? 8 : 2); ++i) {
+      if constexpr (kFrom == From::kBetween)
+        x.v[t][i] = load16(all.x, at[t], (kMx ? (q + i) * 4 : q + i * 4) * pitch);
+      else
+        x.v[t][i] = load16(all.x, at[t] + i * 64, q * (kMx ? 64 : 16));
+    }
 }
 
 // Zeros for what is not in pieces lo .. hi - 1 of the eight; a scale of zero
@@ -389,8 +461,9 @@ __device__ __forceinline__ void cut_weights(Weights<kMx>& w, int lo, int hi, int
     w.scale[1] = static_cast<uint32_t>(v >> 32);
   }
 }
-template <bool kMx, int kTiles>
-__device__ __forceinline__ void cut_tokens(Tokens<kMx, kTiles>& x, int lo, int hi, int g) {
+template <bool kMx, int kTiles, From kFrom>
+__device__ __forceinline__ void cut_tokens(Tokens<kMx, kTiles, kFrom>& x, int lo, int hi) {
+  const int g = kFrom == From::kSorted ? threadIdx.x % 4 : threadIdx.x % 64 / 16;
 #pragma unroll
   for (int t = 0; t < kTiles; ++t)
 #pragma unroll
@@ -430,11 +503,34 @@ __device__ __forceinline__ f32x4 product(u32x4 w, u32x4 x, f32x4 c) {
                                                   0);
 }
 
+// fp16 values as the sums of two bf16 values of the same sign: `a` has the eight bits
+// on top of the next value towards zero, `b` the rest, which is never nothing. So what
+// meets an infinity meets it twice with the same sign, and an infinity is a finite
+// value and an infinity.
+__device__ __forceinline__ void split_f16(u32x4 v, u32x4& a, u32x4& b) {
+  using u16x2 = uint16_t __attribute__((ext_vector_type(2)));
+  // their eight bits, or fewer, are the upper half of fp32
+  auto bf16_pair = [](f16x2 h) {
+    return __builtin_amdgcn_perm(__float_as_uint(static_cast<float>(h[1])), __float_as_uint(static_cast<float>(h[0])),
+                                 0x07060302u);
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = v[i];  // a bit cast of an element itself takes the first one's bits
+    const u16x2 size = __builtin_bit_cast(u16x2, w & 0x7fff7fffu), one = {1, 1};
+    const uint32_t below = __builtin_bit_cast(uint32_t, __builtin_elementwise_sub_sat(size, one));
+    const f16x2 top = __builtin_bit_cast(f16x2, (below & 0x7ff87ff8u) | (w & 0x80008000u));
+    a[i] = bf16_pair(top);
+    b[i] = bf16_pair(__builtin_bit_cast(f16x2, w) - top);
+  }
+}
+
 // acc[n] += the products of a chunk with kTiles tiles of tokens, whose lanes are
 // sorted already. Of 16-bit values lane group g of a tokens' register has those of
 // dword g of a piece of 4-bit weights, so the weights' dwords are brought there.
-template <bool kMx, bool kBf16, int kTiles>
-__device__ __forceinline__ void multiply(const Weights<kMx>& w, const Tokens<kMx, kTiles>& x, f32x4 (&acc)[kTiles]) {
+template <bool kMx, bool kBf16, int kTiles, From kFrom>
+__device__ __forceinline__ void multiply(const Weights<kMx>& w, const Tokens<kMx, kTiles, kFrom>& x,
+                                         f32x4 (&acc)[kTiles]) {
   uint32_t scale[2];
   if constexpr (kMx) {
     scale[0] = sort_lanes(w.scale[0]);
@@ -457,6 +553,11 @@ __device__ __forceinline__ void multiply(const Weights<kMx>& w, const Tokens<kMx
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) acc[n] = product<kBf16>(wide, x.v[n][p * 4 + i], acc[n]);
       }
+    } else if constexpr (kFrom == From::kBetween && !kBf16) {
+      u32x4 a, b;
+      split_f16(v, a, b);
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) acc[n] = product<true>(b, x.v[n][p], product<true>(a, x.v[n][p], acc[n]));
     } else {
 #pragma unroll
       for (int n = 0; n < kTiles; ++n) acc[n] = product<kBf16>(v, x.v[n][p], acc[n]);
@@ -475,18 +576,31 @@ __device__ __forceinline__ void store_row4(uint8_t* p, f32x4 v) {
   }
 }
 
+// Four columns of h, from `col` on: hi is the next bf16 towards zero, lo what is left,
+// rounded. An infinity is a finite value and an infinity.
+__device__ __forceinline__ void store_between(uint8_t* h, const Between& to, int I, int col, f32x4 v) {
+  f32x4 hi;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t bits = __float_as_uint(v[i]), size = bits & 0x7fffffffu;
+    hi[i] = __uint_as_float(((size - (size > 0)) & 0xffff0000u) | (bits & 0x80000000u));
+  }
+  store_row4<true>(h + to.at(I, col / 8, 0) + col % 8 * 2, hi);
+  store_row4<true>(h + to.at(I, col / 8, 1) + col % 8 * 2, v - hi);
+}
+
 // A wave's stream of chunks. The next chunk is on its way while one is
 // multiplied, also the first one of the next sum; there is no branch over loads, so
 // that the wait for one chunk does not wait for the next. The chunk that a row ends
 // in is read as its last eight pieces, and those that were counted before are cut
-// (rows of fewer than eight pieces: those that follow). kSort: the tokens are read
+// (rows of fewer than eight pieces: those that follow). kSorted: the tokens are read
 // by neighbouring lanes too; up to four cost less as they are (one token, 8 of 64
-// 4-bit experts, H 7168: 48.7 us so and 56.2 sorted). `next` moves a place to the
-// next sum's first chunk.
-template <bool kMx, bool kBf16, int kTiles, bool kSort, int kParts>
+// 4-bit experts, H 7168: 48.7 us so and 56.2 sorted). `next` moves a place to the next
+// sum's first chunk.
+template <bool kMx, bool kBf16, int kTiles, From kFrom, int kParts>
 struct Stream {
   Weights<kMx> w[2][kParts];
-  Tokens<kMx, kTiles> x[2];
+  Tokens<kMx, kTiles, kFrom> x[2];
   int low[2];  // the chunk's first piece that counts
 
   template <typename Next>
@@ -495,7 +609,7 @@ struct Stream {
     low[b] = at.c * 8 - q;
 #pragma unroll
     for (int i = 0; i < kParts; ++i) load_weights<kMx>(w[b][i], at.rows[i], at.scales[i], all, q);
-    load_tokens<kMx, kTiles>(x[b], at.x, all, q);
+    load_tokens(x[b], at.x, all, q, at.pitch);
     __builtin_amdgcn_sched_barrier(0);  // or they sink to their use
     at.c += at.step;
     if (--at.left == 0) next(at);
@@ -505,16 +619,16 @@ struct Stream {
     if (low[b] > 0 || all.pieces < 8) {
 #pragma unroll
       for (int i = 0; i < kParts; ++i) cut_weights<kMx>(w[b][i], low[b], all.pieces, all.scales_shift);
-      cut_tokens<kMx, kTiles>(x[b], low[b], all.pieces, kSort ? threadIdx.x % 4 : threadIdx.x % 64 / 16);
+      cut_tokens(x[b], low[b], all.pieces);
     }
-    if constexpr (kSort) {
+    if constexpr (kFrom == From::kSorted) {
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int i = 0; i < (kMx ? 8 : 2); ++i) x[b].v[t][i] = sort_lanes(x[b].v[t][i]);
     }
 #pragma unroll
-    for (int i = 0; i < kParts; ++i) multiply<kMx, kBf16, kTiles>(w[b][i], x[b], acc[i]);
+    for (int i = 0; i < kParts; ++i) multiply<kMx, kBf16>(w[b][i], x[b], acc[i]);
     __builtin_amdgcn_sched_barrier(0);
   }
 
@@ -601,8 +715,14 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void few_up_kernel(FewArgs a) {
   if (a.logits == nullptr || a.T > 1) make_plan<kUpWaves>(s, slots, a.E);
   if (blockIdx.x == 0 && (a.logits == nullptr || a.T <= kSelfRouted))  // for the second kernel
     for (int i = tid; i < slots; i += kThreads) a.ws_ids[i] = s.id[i];
-  if (blockIdx.x == 0)
+  if (blockIdx.x == 0) {
     for (int i = tid; i < kFewMostRuns; i += kThreads) a.ws_arrived[i] = 0;
+    for (int n = tid; n < s.experts; n += kThreads) {
+      const int first = s.first[n], count = s.first[n + 1] - first;
+      for (int i = 0; i < count; ++i)
+        a.ws_between[s.slot[first + i]] = Between{uint32_t(first), uint32_t(count), uint32_t(i)}.packed();
+    }
+  }
 
   // This workgroup's units: row tile `tile` of active expert `n`, its tokens from
   // place `at` on.
@@ -661,7 +781,7 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void few_up_kernel(FewArgs a) {
     }
   };
   set(where, u);
-  Stream<kMx, kBf16, kTiles, kSort, 2> stream;
+  Stream<kMx, kBf16, kTiles, kSort ? From::kSorted : From::kRows, 2> stream;
   if (n > 0) stream.load(0, where, all, next);
   f32x4* part = reinterpret_cast<f32x4*>(lds);  // two of [waves][2][tiles][64]: partial sums of a unit
   constexpr int kPart = kUpWaves * 2 * kTiles * 64;
@@ -689,19 +809,30 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void few_up_kernel(FewArgs a) {
         gs += part[(w * 2 * kTiles + t) * 64 + lane];
         us += part[((w * 2 + 1) * kTiles + t) * 64 + lane];
       }
-      const int place = u.at + t * 16 + lane % 16;
+      const int place = u.at + t * 16 + lane % 16, first = s.first[u.n];
       if (place < u.end) {
-        const int slot = s.slot[place];
-        const float p = s.weight[slot];
+        const float p = s.weight[s.slot[place]];
         f32x4 h;
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[i] = p * (gs[i] / (1.0f + __expf(-gs[i]))) * us[i];
         const int col = u.tile * kRows + lane / 16 * 4;
-        store_row4<kBf16>(a.ws_h + (static_cast<int64_t>(slot) * a.I + col) * 2, h);
+        const Between to{uint32_t(first), uint32_t(u.end - first), uint32_t(place - first)};
+        store_between(a.ws_h, to, a.I, col, h);
       }
     }
     part = part == reinterpret_cast<f32x4*>(lds) ? part + kPart : reinterpret_cast<f32x4*>(lds);
   }
+}
+
+// What the lane eight away, of sixteen, has.
+__device__ __forceinline__ f32x4 eighth_lane(f32x4 v) {
+  constexpr int kRotate8 = 0x128;  // row_ror:8
+  f32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    r[i] = __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_update_dpp(
+        0, static_cast<int>(__float_as_uint(v[i])), kRotate8, 0xf, 0xf, false)));
+  return r;
 }
 
 // Values that workgroups on different XCDs share: past the XCD's own L2 both ways.
@@ -723,32 +854,37 @@ __device__ __forceinline__ f32x4 load_shared(f32x4* p) {
   return v;
 }
 
-// The second kernel: 16 rows of y, a run, for up to 64 tokens. Its waves take the
-// experts in turn, or parts of their rows when the experts are few, for 16 kTiles
+// The second kernel: 16 kParts rows of y, a run, for up to 64 tokens. Its waves take the
+// experts in turn, or parts of their rows when the experts are few, for 8 kTiles
 // of the expert's tokens at a time, and add the results to sums of their own in
 // LDS: each in its fixed order. Where there are fewer runs than the chip holds
 // workgroups, a run has several (blockIdx.z), which share the experts; each leaves
 // its sums in the workspace, and the last one to arrive adds them, in their order.
 // So nothing depends on timing.
-template <bool kMx, bool kBf16, int kTiles, bool kSort, int kWaves>
+template <bool kMx, bool kBf16, int kTiles, int kParts, int kWaves>
 __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
   extern __shared__ __align__(16) uint8_t lds[];
   constexpr int kThreads = kWaves * 64;
   const int tid = threadIdx.x, lane = tid % 64, wave = __builtin_amdgcn_readfirstlane(tid / 64);
   const int r = lane % 16, group = lane / 16;
   const int t0 = blockIdx.y * kDownTokens, tokens = min(a.T - t0, kDownTokens), slots = tokens * a.k;
-  f32x4* sums = reinterpret_cast<f32x4*>(lds);  // [waves][tokens][4 groups]
-  f32x4* mine = sums + wave * tokens * 4;
-  Plan s = carve(lds + down_sum_bytes(tokens, kWaves), slots, a.E);
-  for (int i = lane; i < tokens * 4; i += 64) mine[i] = f32x4{0, 0, 0, 0};
+  constexpr int kGroups = 4 * kParts;  // of four rows
+  f32x4* sums = reinterpret_cast<f32x4*>(lds);  // [waves][tokens][groups]
+  f32x4* mine = sums + wave * tokens * kGroups;
+  Plan s = carve(lds + down_sum_bytes(tokens, kWaves, kParts), slots, a.E);
+  for (int i = lane; i < tokens * kGroups; i += 64) mine[i] = f32x4{0, 0, 0, 0};
   if (slots <= kSmallPlan) {
+    if (lane < slots) s.between[lane] = a.ws_between[t0 * a.k + lane];
     make_small_plan(s, lane < slots ? a.ws_ids[t0 * a.k + lane] : -1, slots);
   } else {
-    for (int i = tid; i < slots; i += kThreads) s.id[i] = static_cast<int16_t>(a.ws_ids[t0 * a.k + i]);
+    for (int i = tid; i < slots; i += kThreads) {
+      s.id[i] = static_cast<int16_t>(a.ws_ids[t0 * a.k + i]);
+      s.between[i] = a.ws_between[t0 * a.k + i];
+    }
     make_plan<kWaves>(s, slots, a.E);
   }
 
-  const Rows all = make_rows<kMx>(a.ws_h, a.T * a.k * a.I * 2, a.I);
+  const Rows all = make_rows<kMx>(a.ws_h, a.T * a.k * a.I * 4, a.I);
   const int chunks = (all.pieces + 7) / 8;
   // parts of an expert's rows: enough for two a wave, of two chunks at least
   const int waves = kWaves * static_cast<int>(gridDim.z), first_unit = blockIdx.z * kWaves + wave;
@@ -769,23 +905,27 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
     u.end = __builtin_amdgcn_readfirstlane(s.first[u.n + 1]);
   };
   auto advance = [&](Unit& u) {
-    u.at += 16 * kTiles;
+    u.at += kPlaces * kTiles;
     if (u.at < u.end) return;
     u.unit += waves;
     begin(u);
   };
   auto length = [&](const Unit& u) { return min(part_chunks, chunks - u.part * part_chunks); };
-  using Where = Place<kTiles, 1>;
+  using Where = Place<kTiles, kParts>;
   auto set = [&](Where& p, const Unit& u) {
     const int expert = __builtin_amdgcn_readfirstlane(s.active[u.n]);
-    const int64_t row = static_cast<int64_t>(expert) * a.H + blockIdx.x * kRows;
-    p.rows[0] = buffer_at(a.down + row * all.bytes, kRows * all.bytes);
-    p.scales[0] = a.down_scales + row * all.scale_bytes;
+    const int64_t row = static_cast<int64_t>(expert) * a.H + blockIdx.x * (kRows * kParts);
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      p.rows[i] = buffer_at(a.down + (row + i * kRows) * all.bytes, kRows * all.bytes);
+      p.scales[i] = a.down_scales + (row + i * kRows) * all.scale_bytes;
+    }
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      const int place = u.at + t * 16 + (kSort ? lane / 4 : r), g = kSort ? lane % 4 : group;
-      p.x[t] = place < u.end ? static_cast<uint32_t>(t0 * a.k + s.slot[place]) * a.I * 2 + g * 16 : kOutside;
+      const int place = u.at + t * kPlaces + r % kPlaces;
+      p.x[t] = place < u.end ? Between::of(s.between[s.slot[place]]).at(a.I, group, r / kPlaces) : kOutside;
     }
+    p.pitch = __builtin_amdgcn_readfirstlane(Between::of(s.between[s.slot[u.at]]).pitch());
     p.c = u.part * part_chunks;
     p.left = length(u);
     p.step = 1;
@@ -806,30 +946,35 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
       }
     };
     set(where, u);
-    Stream<kMx, kBf16, kTiles, kSort, 1> stream;
+    Stream<kMx, kBf16, kTiles, From::kBetween, kParts> stream;
     stream.load(0, where, all, next);
     for (; u.unit < units; advance(u)) {
-      f32x4 acc[1][kTiles];
+      f32x4 acc[kParts][kTiles];
       stream.sum(acc, length(u), where, all, next);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
-        const int place = u.at + t * 16 + r;
-        if (place < u.end) mine[s.slot[place] / a.k * 4 + group] += acc[0][t];
+        const int place = u.at + t * kPlaces + r;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          const f32x4 sum = acc[i][t] + eighth_lane(acc[i][t]);
+          if (r < kPlaces && place < u.end) mine[s.slot[place] / a.k * kGroups + i * 4 + group] += sum;
+        }
       }
     }
   }
   __syncthreads();
   auto store = [&](int i, f32x4 sum) {
-    store_row4<kBf16>(a.y + (static_cast<int64_t>(t0 + i / 4) * a.H + blockIdx.x * kRows + i % 4 * 4) * 2, sum);
+    store_row4<kBf16>(
+        a.y + (static_cast<int64_t>(t0 + i / kGroups) * a.H + (blockIdx.x * kGroups + i % kGroups) * 4) * 2, sum);
   };
-  // [workgroups of a run][runs][tokens][4]; the last run of tokens may have fewer
-  const int run = blockIdx.y * gridDim.x + blockIdx.x, pitch = min(a.T, kDownTokens) * 4;
+  // [workgroups of a run][runs][tokens][groups]; the last run of tokens may have fewer
+  const int run = blockIdx.y * gridDim.x + blockIdx.x, pitch = min(a.T, kDownTokens) * kGroups;
   f32x4* part = a.ws_part + static_cast<int64_t>(run) * pitch;
   const int64_t apart = static_cast<int64_t>(gridDim.y * gridDim.x) * pitch;
-  for (int i = tid; i < tokens * 4; i += kThreads) {
+  for (int i = tid; i < tokens * kGroups; i += kThreads) {
     f32x4 sum = sums[i];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) sum += sums[w * tokens * 4 + i];
+    for (int w = 1; w < kWaves; ++w) sum += sums[w * tokens * kGroups + i];
     if (gridDim.z == 1)
       store(i, sum);
     else
@@ -842,56 +987,83 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
   if (tid == 0) *s.wave_sum = atomicAdd(a.ws_arrived + run, 1);
   __syncthreads();
   if (*s.wave_sum != static_cast<int>(gridDim.z) - 1) return;
-  for (int i = tid; i < tokens * 4; i += kThreads) {
+  constexpr unsigned kAtOnce = 4;
+  for (int i = tid; i < tokens * kGroups; i += kThreads) {
     f32x4 sum = load_shared(part + i);
-    for (unsigned z = 1; z < gridDim.z; ++z) sum += load_shared(part + z * apart + i);
+    for (unsigned z = 1; z < gridDim.z; z += kAtOnce) {  // several on their way, added in their order
+      f32x4 v[kAtOnce];
+#pragma unroll
+      for (unsigned n = 0; n < kAtOnce; ++n) v[n] = load_shared(part + min(z + n, gridDim.z - 1) * apart + i);
+#pragma unroll
+      for (unsigned n = 0; n < kAtOnce; ++n)
+        if (z + n < gridDim.z) sum += v[n];
+    }
     store(i, sum);
   }
 }
 
 template <bool kMx, bool kBf16, int kTiles, bool kSort>
-mrr_status launch_few_tiles(const FewArgs& a, hipStream_t stream) {
+mrr_status launch_up(const FewArgs& a, hipStream_t stream) {
   const int slots = a.T * a.k;
-  if (a.logits != nullptr && a.T > kSelfRouted) {
-    hipLaunchKernelGGL(few_route_kernel, dim3(a.T), dim3(64), 0, stream, a);
-    if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
-  }
   // the workgroups that the chip holds at once (by their registers), each taking
   // its units in turn
   const int64_t units = static_cast<int64_t>(slots < a.E ? slots : a.E) * (a.I / kRows), most = 256 * (kMx ? 2 : 4);
   hipLaunchKernelGGL((few_up_kernel<kMx, kBf16, kTiles, kSort>), dim3(static_cast<unsigned>(units < most ? units : most)),
                      dim3(kUpWaves * 64), up_part_bytes(kTiles) + plan_bytes(slots, a.E), stream, a);
-  if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
-  const int tokens = a.T < kDownTokens ? a.T : kDownTokens;
-  dim3 grid(a.H / kRows, (a.T + kDownTokens - 1) / kDownTokens);
+  return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
+}
+
+template <bool kMx, bool kBf16, int kTiles, int kParts>
+mrr_status launch_down(const FewArgs& a, hipStream_t stream) {
+  const int slots = a.T * a.k, tokens = a.T < kDownTokens ? a.T : kDownTokens;
+  dim3 grid(a.H / (kRows * kParts), (a.T + kDownTokens - 1) / kDownTokens);
   const size_t plan = plan_bytes(tokens * a.k, a.E);
+  const int runs = static_cast<int>(grid.x * grid.y);
+  // Workgroups of a run: with few runs as many as the chip holds (two a CU, by their
+  // registers), with four chunks a wave at least, more tokens counting as more chunks
+  // (16 tokens, 6 of 64 fp16 experts, H 2048: 147 us with one, 134 with four; 16 tokens,
+  // 8 of 64 4-bit experts, H 1024: 38 and 29). Few: of eight waves half the CUs, of four,
+  // with two parts, two thirds of them (64 tokens, 4 of 8 4-bit experts, 160 runs: 100 us
+  // with one, 93 with three; 4 of 32, 224 runs: 216 and 221 with two).
+  const int used = slots < a.E ? slots : a.E, chunks = ((kMx ? a.I / 32 : a.I / 8) + 7) / 8;
+  const int steps = used * chunks + slots * chunks / 8;
+  if (runs <= (kParts == 1 ? 128 : 170)) grid.z = std::max(1, std::min(static_cast<int>(kFewMostRuns) / runs, steps / 32));
+  auto launch = [&](auto waves) {
+    constexpr int kWaves = decltype(waves)::value;
+    hipLaunchKernelGGL((few_down_kernel<kMx, kBf16, kTiles, kParts, kWaves>), grid, dim3(kWaves * 64),
+                       down_sum_bytes(tokens, kWaves, kParts) + plan, stream, a);
+  };
   // Up to a workgroup a CU eight waves, else four, so that the chip holds them all
   // (one token, 8 of 64 4-bit experts, H 7168: 45.6 us with eight, 42.1 with four;
   // 64 tokens, 4 of 32, H 4096: 128.8 and 133.7).
-  const int runs = static_cast<int>(grid.x * grid.y);
-  // Workgroups of a run: with fewer runs than half the CUs as many as the chip holds
-  // (two a CU, by their registers), with four chunks a wave at least, more tokens
-  // counting as more chunks (16 tokens, 6 of 64 fp16 experts, H 2048: 147 us with one,
-  // 134 with four; 16 tokens, 8 of 64 4-bit experts, H 1024: 38 and 29).
-  const int used = slots < a.E ? slots : a.E, chunks = ((kMx ? a.I / 32 : a.I / 8) + 7) / 8;
-  const int steps = used * chunks + slots * chunks / 8;
-  const int most_runs = static_cast<int>(kTiles == 1 ? kFewMostRuns : kFewMostRuns / 2);
-  if (runs <= 128) grid.z = std::max(1, std::min(most_runs / runs, steps / 32));
-  if (runs <= 256)
-    hipLaunchKernelGGL((few_down_kernel<kMx, kBf16, kTiles, kSort, 8>), grid, dim3(512),
-                       down_sum_bytes(tokens, 8) + plan, stream, a);
-  else
-    hipLaunchKernelGGL((few_down_kernel<kMx, kBf16, kTiles, kSort, 4>), grid, dim3(256),
-                       down_sum_bytes(tokens, 4) + plan, stream, a);
+  if constexpr (kParts == 1) {
+    if (runs <= 256) launch(std::integral_constant<int, 8>{});
+  }
+  if (kParts > 1 || runs > 256) launch(std::integral_constant<int, 4>{});
   return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
 }
 
 template <bool kMx, bool kBf16>
 mrr_status launch_few(const FewArgs& a, hipStream_t stream) {
+  if (a.logits != nullptr && a.T > kSelfRouted) {
+    hipLaunchKernelGGL(few_route_kernel, dim3(a.T), dim3(64), 0, stream, a);
+    if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
+  }
   // two tiles of tokens at once where an expert has more than one, on average
-  return a.T <= kSelfRouted        ? launch_few_tiles<kMx, kBf16, 1, false>(a, stream)
-         : a.T * a.k <= 16 * a.E ? launch_few_tiles<kMx, kBf16, 1, true>(a, stream)
-                                   : launch_few_tiles<kMx, kBf16, 2, true>(a, stream);
+  const int slots = a.T * a.k;
+  const mrr_status st = a.T <= kSelfRouted  ? launch_up<kMx, kBf16, 1, false>(a, stream)
+                        : slots <= 16 * a.E ? launch_up<kMx, kBf16, 1, true>(a, stream)
+                                            : launch_up<kMx, kBf16, 2, true>(a, stream);
+  if (st != MRR_SUCCESS) return st;
+  // The second kernel's tiles are of eight tokens: one where an expert has fewer than
+  // half of it, on average (48 tokens, 4 of 64 4-bit experts: 202 us, 207 with two;
+  // 64 tokens, 4 of 32: 150 and 134). Two of them are bound by the loads of h, which
+  // two runs of rows then share (64 tokens, 4 of 32 4-bit experts: 146 us with one run,
+  // 134 with two; 64 tokens, 8 of 16 bf16 experts: 264 and 233).
+  if (a.T <= kPlaces || slots <= 4 * a.E) return launch_down<kMx, kBf16, 1, 1>(a, stream);
+  if (kMx || slots <= 16 * a.E) return launch_down<kMx, kBf16, 2, 2>(a, stream);
+  if constexpr (!kMx) return launch_down<kMx, kBf16, 4, 2>(a, stream);
+  return MRR_SUCCESS;
 }
 
 }  // namespace
@@ -915,6 +1087,7 @@ extern "C" mrr_status mrr_few_tokens(const mrr_few_tokens_args* args, void* work
   a.y = static_cast<uint8_t*>(args->y);
   a.ws_ids = reinterpret_cast<int32_t*>(ws + l.ids);
   a.ws_weight = reinterpret_cast<float*>(ws + l.weight);
+  a.ws_between = reinterpret_cast<int32_t*>(ws + l.between);
   a.ws_arrived = reinterpret_cast<int32_t*>(ws + l.arrived);
   a.ws_part = reinterpret_cast<mrr::f32x4*>(ws + l.part);
   a.ws_h = ws + l.h;
