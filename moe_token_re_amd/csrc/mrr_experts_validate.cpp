@@ -95,7 +95,8 @@ mrr_status check_few_tokens(const mrr_few_tokens_args* a, const void* ws, size_t
   if (a == nullptr) return MRR_ERROR_INVALID_VALUE;
   if (a->dtype != MRR_F16 && a->dtype != MRR_BF16) return MRR_ERROR_UNSUPPORTED_DTYPE;
   const bool mx = a->weights_dtype == MRR_F4_E2M1;
-  // 4-bit values times their scale are exact in bf16, and beyond the range of fp16
+  // 4-bit values times their scale are exact in bf16 (of the two largest scales an
+  // eighth of them is), and beyond the range of fp16
   if (mx ? a->dtype != MRR_BF16 : a->weights_dtype != a->dtype) return MRR_ERROR_UNSUPPORTED_DTYPE;
   if (a->renormalize != 0 && a->renormalize != 1) return MRR_ERROR_INVALID_VALUE;
   if (a->T < 0 || a->T > MRR_FEW_TOKENS_MAX || a->H <= 0 || a->H > 65536 || a->H % 32 != 0 || a->I <= 0 ||

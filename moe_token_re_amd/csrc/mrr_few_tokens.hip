@@ -14,9 +14,10 @@
 //
 // Both feed the matrix instructions with 16 weight rows and up to 16 of the tokens
 // that chose the expert. A lane reads 32 bytes of a weight row at a time: 16 16-bit
-// values, or two blocks of 32 4-bit values, widened to bf16 with their scale, which
-// is exact. x has 16 bits as it comes. h has no such type, and 16 bits would round it
-// or, fp16, end at 65504: it is held as two bf16 values, hi + lo, off by at most 2^-15.
+// values, or two blocks of 32 4-bit values, widened to bf16 with their scale, which is
+// exact but for the two largest scales (take_blocks). x has 16 bits as it comes. h has
+// no such type, and 16 bits would round it or, fp16, end at 65504: it is held as two
+// bf16 values, hi + lo, off by at most 2^-15.
 // They take two columns of the instruction's 16, so that 8 tokens cost what 16 of one
 // column would; fp16 weights are multiplied as the two bf16 values that they are the
 // sum of. (fp32 products, 16x16x4, would need neither: 64 tokens, 8 of 16 bf16 experts,
@@ -461,6 +462,31 @@ __device__ __forceinline__ void cut_weights(Weights<kMx>& w, int lo, int hi, int
     w.scale[1] = static_cast<uint32_t>(v >> 32);
   }
 }
+// Widened to bf16, values under a scale of 2^126 or 2^127 may be infinities where their
+// products with the tokens' values are none. So where a workgroup of the first kernel,
+// or a wave of the second, has had a sum that is not finite, it makes its sums again,
+// carefully: of the other blocks, and then of an eighth of these. (To make each sum
+// again by itself kept enough scalar registers busy to cost 2 to 4% of every call; this
+// costs 0.3 to 2%.)
+__device__ __forceinline__ bool is_large(uint32_t scale) { return scale == 253 || scale == 254; }
+__device__ __forceinline__ void take_blocks(Weights<true>& w, bool large) {
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const uint32_t mine = w.scale[p] >> threadIdx.x % 4 * 8 & 0xff;
+    if (mine != 255 && is_large(mine) != large) w.v[p] = u32x4{0, 0, 0, 0};
+    if (!large) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (is_large(w.scale[p] >> 8 * i & 0xff)) w.scale[p] -= 3u << 8 * i;
+  }
+}
+
+// Whether a lane's sums are finite.
+__device__ __forceinline__ bool is_finite(f32x4 v) {
+  const f32x4 nothing = v * 0.0f;  // or a NaN
+  return (nothing[0] + nothing[1]) + (nothing[2] + nothing[3]) == 0.0f;
+}
+
 template <bool kMx, int kTiles, From kFrom>
 __device__ __forceinline__ void cut_tokens(Tokens<kMx, kTiles, kFrom>& x, int lo, int hi) {
   const int g = kFrom == From::kSorted ? threadIdx.x % 4 : threadIdx.x % 64 / 16;
@@ -596,8 +622,8 @@ __device__ __forceinline__ void store_between(uint8_t* h, const Between& to, int
 // (rows of fewer than eight pieces: those that follow). kSorted: the tokens are read
 // by neighbouring lanes too; up to four cost less as they are (one token, 8 of 64
 // 4-bit experts, H 7168: 48.7 us so and 56.2 sorted). `next` moves a place to the next
-// sum's first chunk.
-template <bool kMx, bool kBf16, int kTiles, From kFrom, int kParts>
+// sum's first chunk, `again` brings the present one's back.
+template <bool kMx, bool kBf16, int kTiles, From kFrom, int kParts, bool kCareful>
 struct Stream {
   Weights<kMx> w[2][kParts];
   Tokens<kMx, kTiles, kFrom> x[2];
@@ -615,11 +641,15 @@ struct Stream {
     if (--at.left == 0) next(at);
   }
 
-  __device__ __forceinline__ void use(int b, f32x4 (&acc)[kParts][kTiles], const Rows& all) {
+  __device__ __forceinline__ void use(int b, f32x4 (&acc)[kParts][kTiles], const Rows& all, bool large) {
     if (low[b] > 0 || all.pieces < 8) {
 #pragma unroll
       for (int i = 0; i < kParts; ++i) cut_weights<kMx>(w[b][i], low[b], all.pieces, all.scales_shift);
       cut_tokens(x[b], low[b], all.pieces);
+    }
+    if constexpr (kCareful) {
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) take_blocks(w[b][i], large);
     }
     if constexpr (kFrom == From::kSorted) {
 #pragma unroll
@@ -633,16 +663,33 @@ struct Stream {
   }
 
   // The sums of the next n > 0 chunks, whose first is in the first buffer.
-  template <typename Next>
+  template <typename Next, typename Again>
   __device__ __forceinline__ void sum(f32x4 (&acc)[kParts][kTiles], int n, Place<kTiles, kParts>& at, const Rows& all,
-                                      Next&& next) {
+                                      Next&& next, Again&& again) {
+    each(acc, [](f32x4) { return f32x4{0, 0, 0, 0}; });
+    add(acc, n, at, all, next, false);
+    if constexpr (kCareful) {
+      each(acc, [](f32x4 v) { return v * 0.125f; });
+      again();
+      add(acc, n, at, all, next, true);
+      each(acc, [](f32x4 v) { return v * 8.0f; });
+    }
+  }
+
+  template <typename F>
+  static __device__ __forceinline__ void each(f32x4 (&acc)[kParts][kTiles], F&& f) {
 #pragma unroll
     for (int i = 0; i < kParts; ++i)
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) acc[i][t] = f32x4{0, 0, 0, 0};
+      for (int t = 0; t < kTiles; ++t) acc[i][t] = f(acc[i][t]);
+  }
+
+  template <typename Next>
+  __device__ __forceinline__ void add(f32x4 (&acc)[kParts][kTiles], int n, Place<kTiles, kParts>& at, const Rows& all,
+                                      Next&& next, bool large) {
     for (;;) {
       load(1, at, all, next);
-      use(0, acc, all);
+      use(0, acc, all, large);
       if (--n == 0) {
 #pragma unroll
         for (int i = 0; i < kParts; ++i) w[0][i] = w[1][i];
@@ -651,7 +698,7 @@ struct Stream {
         return;
       }
       load(0, at, all, next);
-      use(1, acc, all);
+      use(1, acc, all, large);
       if (--n == 0) return;
     }
   }
@@ -743,9 +790,7 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void few_up_kernel(FewArgs a) {
     u.unit += gridDim.x;
     begin(u);
   };
-  Unit u{static_cast<int>(blockIdx.x), 0, 0, 0, 0};
-  if (u.unit >= units) return;
-  begin(u);
+  if (static_cast<int>(blockIdx.x) >= units) return;
 
   const Rows all = make_rows<kMx>(a.x, a.T * a.H * 2, a.H);
   const int chunks = (all.pieces + 7) / 8;
@@ -768,59 +813,80 @@ __global__ __launch_bounds__(kUpWaves * 64, 2) void few_up_kernel(FewArgs a) {
     p.left = n;
     p.step = kUpWaves;
   };
-  Unit ahead = u;
-  Where where;
-  auto next = [&](Where& p) {  // behind the last unit: its first chunk again
-    if (ahead.unit < units) advance(ahead);
-    if (ahead.unit < units) {
-      set(p, ahead);
-    } else {
-      p.c = wave;
-      p.left = 1 << 30;
-      p.step = 0;
-    }
-  };
-  set(where, u);
-  Stream<kMx, kBf16, kTiles, kSort ? From::kSorted : From::kRows, 2> stream;
-  if (n > 0) stream.load(0, where, all, next);
   f32x4* part = reinterpret_cast<f32x4*>(lds);  // two of [waves][2][tiles][64]: partial sums of a unit
   constexpr int kPart = kUpWaves * 2 * kTiles * 64;
   int finisher = 0;
-  for (; u.unit < units; advance(u)) {
-    f32x4 acc[2][kTiles];
-    if (n > 0) {
-      stream.sum(acc, n, where, all, next);
-    } else {
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) acc[0][t] = acc[1][t] = f32x4{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) part[((wave * 2 + i) * kTiles + t) * 64 + lane] = acc[i][t];
-    lds_barrier();
-    // a wave finishes a tile of tokens, each its turn: a lane has four rows of one
-    // token. Meanwhile the others go on, in the other half of `part`.
-    for (int t = 0; t < kTiles; ++t, finisher = (finisher + 1) % kUpWaves) {
-      if (wave != finisher) continue;
-      f32x4 gs = part[t * 64 + lane], us = part[(kTiles + t) * 64 + lane];
-#pragma unroll
-      for (int w = 1; w < kUpWaves; ++w) {
-        gs += part[(w * 2 * kTiles + t) * 64 + lane];
-        us += part[((w * 2 + 1) * kTiles + t) * 64 + lane];
+  // All units; whether the sums that the lane saw were finite.
+  auto compute = [&](auto careful) {
+    bool finite = true;
+    Unit u{static_cast<int>(blockIdx.x), 0, 0, 0, 0};
+    begin(u);
+    Unit ahead = u;
+    Where where;
+    auto next = [&](Where& p) {  // behind the last unit: its first chunk again
+      if (ahead.unit < units) advance(ahead);
+      if (ahead.unit < units) {
+        set(p, ahead);
+      } else {
+        p.c = wave;
+        p.left = 1 << 30;
+        p.step = 0;
       }
-      const int place = u.at + t * 16 + lane % 16, first = s.first[u.n];
-      if (place < u.end) {
-        const float p = s.weight[s.slot[place]];
-        f32x4 h;
+    };
+    Stream<kMx, kBf16, kTiles, kSort ? From::kSorted : From::kRows, 2, decltype(careful)::value> stream;
+    auto again = [&]() {
+      ahead = u;
+      set(where, u);
+      stream.load(0, where, all, next);
+    };
+    set(where, u);
+    if (n > 0) stream.load(0, where, all, next);
+    for (; u.unit < units; advance(u)) {
+      f32x4 acc[2][kTiles];
+      if (n > 0) {
+        stream.sum(acc, n, where, all, next, again);
+      } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = p * (gs[i] / (1.0f + __expf(-gs[i]))) * us[i];
-        const int col = u.tile * kRows + lane / 16 * 4;
-        const Between to{uint32_t(first), uint32_t(u.end - first), uint32_t(place - first)};
-        store_between(a.ws_h, to, a.I, col, h);
+        for (int t = 0; t < kTiles; ++t) acc[0][t] = acc[1][t] = f32x4{0, 0, 0, 0};
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) part[((wave * 2 + i) * kTiles + t) * 64 + lane] = acc[i][t];
+      lds_barrier();
+      // a wave finishes a tile of tokens, each its turn: a lane has four rows of one
+      // token. Meanwhile the others go on, in the other half of `part`.
+      for (int t = 0; t < kTiles; ++t, finisher = (finisher + 1) % kUpWaves) {
+        if (wave != finisher) continue;
+        f32x4 gs = part[t * 64 + lane], us = part[(kTiles + t) * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < kUpWaves; ++w) {
+          gs += part[(w * 2 * kTiles + t) * 64 + lane];
+          us += part[((w * 2 + 1) * kTiles + t) * 64 + lane];
+        }
+        const int place = u.at + t * 16 + lane % 16, first = s.first[u.n];
+        if (place < u.end) {
+          if constexpr (kMx) finite &= is_finite(gs), finite &= is_finite(us);
+          const float p = s.weight[s.slot[place]];
+          f32x4 h;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[i] = p * (gs[i] / (1.0f + __expf(-gs[i]))) * us[i];
+          const int col = u.tile * kRows + lane / 16 * 4;
+          const Between to{uint32_t(first), uint32_t(u.end - first), uint32_t(place - first)};
+          store_between(a.ws_h, to, a.I, col, h);
+        }
+      }
+      part = part == reinterpret_cast<f32x4*>(lds) ? part + kPart : reinterpret_cast<f32x4*>(lds);
     }
-    part = part == reinterpret_cast<f32x4*>(lds) ? part + kPart : reinterpret_cast<f32x4*>(lds);
+    return finite;
+  };
+  const bool finite = compute(std::false_type{});
+  if constexpr (kMx) {
+    s.wave_sum[wave] = !__all(finite);
+    __syncthreads();
+    int bad = 0;
+    for (int w = 0; w < kUpWaves; ++w) bad |= s.wave_sum[w];
+    if (__builtin_expect(__builtin_amdgcn_readfirstlane(bad), 0)) compute(std::true_type{});
   }
 }
 
@@ -930,8 +996,10 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
     p.left = length(u);
     p.step = 1;
   };
-  Unit u{first_unit, 0, 0, 0, 0};
-  if (u.unit < units) {
+  // All units; whether the sums that the lane saw were finite.
+  auto compute = [&](auto careful) {
+    bool finite = true;
+    Unit u{first_unit, 0, 0, 0, 0};
     begin(u);
     Unit ahead = u;
     Where where;
@@ -945,20 +1013,37 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
         p.step = 0;
       }
     };
-    set(where, u);
-    Stream<kMx, kBf16, kTiles, From::kBetween, kParts> stream;
-    stream.load(0, where, all, next);
+    Stream<kMx, kBf16, kTiles, From::kBetween, kParts, decltype(careful)::value> stream;
+    auto again = [&]() {
+      ahead = u;
+      set(where, u);
+      stream.load(0, where, all, next);
+    };
+    again();
     for (; u.unit < units; advance(u)) {
       f32x4 acc[kParts][kTiles];
-      stream.sum(acc, length(u), where, all, next);
+      stream.sum(acc, length(u), where, all, next, again);
 #pragma unroll
       for (int t = 0; t < kTiles; ++t) {
         const int place = u.at + t * kPlaces + r;
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
           const f32x4 sum = acc[i][t] + eighth_lane(acc[i][t]);
-          if (r < kPlaces && place < u.end) mine[s.slot[place] / a.k * kGroups + i * 4 + group] += sum;
+          if (r < kPlaces && place < u.end) {
+            if constexpr (kMx) finite &= is_finite(sum);
+            mine[s.slot[place] / a.k * kGroups + i * 4 + group] += sum;
+          }
         }
+      }
+    }
+    return finite;
+  };
+  if (first_unit < units) {
+    const bool finite = compute(std::false_type{});
+    if constexpr (kMx) {
+      if (__builtin_expect(!__all(finite), 0)) {
+        for (int i = lane; i < tokens * kGroups; i += 64) mine[i] = f32x4{0, 0, 0, 0};
+        compute(std::true_type{});
       }
     }
   }
