@@ -407,7 +407,7 @@ typedef struct mrr_few_tokens_args {
   int64_t H;                       /* a multiple of 32, 0 < H <= 65536 */
   int64_t E;                       /* 0 < E <= 1024 */
   int64_t I;                       /* a multiple of 32, 0 < I <= 65536 */
-  int64_t top_k;                   /* 1 <= top_k <= min(E, 16) */
+  int64_t top_k;                   /* 1 <= top_k <= 16, and with router_logits <= E */
   const float* router_logits;      /* [T, E], or NULL */
   int64_t renormalize;             /* 0 or 1, with router_logits */
   const int32_t* expert_ids;       /* [T, top_k], or NULL */

@@ -101,8 +101,10 @@ mrr_status check_few_tokens(const mrr_few_tokens_args* a, const void* ws, size_t
   if (a->renormalize != 0 && a->renormalize != 1) return MRR_ERROR_INVALID_VALUE;
   if (a->T < 0 || a->T > MRR_FEW_TOKENS_MAX || a->H <= 0 || a->H > 65536 || a->H % 32 != 0 || a->I <= 0 ||
       a->I > 65536 || a->I % 32 != 0 || a->E <= 0 || a->E > kFewMaxExperts || a->top_k < 1 ||
-      a->top_k > kFewMaxTopK || a->top_k > a->E)
+      a->top_k > kFewMaxTopK)
     return MRR_ERROR_INVALID_SHAPE;
+  // logits choose among these experts; ids may name other ranks' as well
+  if (a->router_logits != nullptr && a->top_k > a->E) return MRR_ERROR_INVALID_SHAPE;
   if ((a->router_logits == nullptr) == (a->expert_ids == nullptr) && a->T > 0) return MRR_ERROR_INVALID_VALUE;
   if ((a->expert_ids == nullptr) != (a->expert_weight == nullptr)) return MRR_ERROR_INVALID_VALUE;
   if (a->gate_up == nullptr || a->down == nullptr) return MRR_ERROR_INVALID_VALUE;

@@ -206,6 +206,7 @@ PyObject* few_tokens(PyObject*, PyObject* const* args, Py_ssize_t n) {
       PyErr_Clear();
       return none();
     }
+    if (k > E) return none();
   } else {
     if (ids->scalar_type() != at::kInt || weight->scalar_type() != at::kFloat || ids->dim() != 2 ||
         ids->size(0) != T || weight->sizes() != ids->sizes() || args[4] != Py_None)

@@ -229,7 +229,7 @@ def moe_few_tokens(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, *
     to the lowest expert, weighted by the softmax over all experts, or with
     renormalize=True over the chosen ones; an expert of logit -inf is never
     chosen), or expert_ids [T, k] int32 with expert_weight [T, k] float32 (an id
-    outside [0, E) chooses nothing). Returns y [T, H] of x's dtype; a token
+    outside [0, E) chooses nothing, and k may be more than E: experts of other ranks). Returns y [T, H] of x's dtype; a token
     without experts gives zeros."""
     if out is None and workspace is None:
         done = _lib.binding().few_tokens(x, gate_up, down, router_logits, top_k, renormalize, expert_ids,
@@ -275,6 +275,8 @@ def moe_few_tokens(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, *
             raise ValueError("expert_weight goes with expert_ids")
         if top_k is None:
             raise ValueError("router_logits need top_k")
+        if top_k > E:  # without tokens the library gets no logits to see it by
+            _raise(_lib.ERROR_INVALID_SHAPE, "mrr_few_tokens")
     else:
         _check_tensor("expert_ids", expert_ids, dev)
         if expert_weight is None:

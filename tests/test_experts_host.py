@@ -131,3 +131,15 @@ def test_python_refuses_cpu_tensors():
             call()
     with pytest.raises(TypeError):
         moe.mx_quantize([1.0])
+
+
+@pytest.mark.parametrize("change,code", [
+    ({**GIVEN, "E": 4, "top_k": 6}, OK), ({**GIVEN, "E": 1, "top_k": 16}, OK), ({**MX, **GIVEN, "E": 3, "top_k": 8}, OK),
+    ({**GIVEN, "E": 4, "top_k": 17}, SHAPE), ({**GIVEN, "E": 0, "top_k": 1}, SHAPE),
+    ({"E": 4, "top_k": 5}, SHAPE), ({"E": 4, "top_k": 4}, OK),
+    ({"T": 0, "x": None, "y": None, "router_logits": None, "E": 4, "top_k": 6}, OK),
+])
+def test_few_tokens_more_choices_than_experts(change, code):
+    """A token names experts of all ranks, and this one may have fewer; the
+    largest logits are chosen among its own."""
+    assert few(**change) == code
