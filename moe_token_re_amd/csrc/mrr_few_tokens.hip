@@ -44,6 +44,7 @@ constexpr int kUpWaves = 4;       // first kernel: they share a unit's rows, eac
 constexpr int kRows = 16;         // weight rows of a fragment
 constexpr int kDownTokens = 64;   // tokens of a workgroup of the second kernel
 constexpr int kPlaces = 8;        // tokens of a tile there: a column for hi, one for lo
+constexpr int kManyChoices = 10;  // of an expert, on average: more tiles of tokens at once
 constexpr int kSelfRouted = 4;    // so many tokens, a wave each, the first kernel routes itself
 
 struct FewArgs {
@@ -198,11 +199,11 @@ inline __host__ __device__ constexpr size_t plan_bytes(int slots, int E) {
 }
 
 // What a workgroup may have without asking for more; the first kernel takes two tiles
-// of tokens with more than 16 choices an expert alone.
+// of tokens with more than kManyChoices an expert alone.
 constexpr size_t kMostLds = 64 * 1024;
 constexpr int kMostSlots = MRR_FEW_TOKENS_MAX * static_cast<int>(kFewMaxTopK);
 static_assert(up_part_bytes(1) + plan_bytes(kMostSlots, kMaxExperts) <= kMostLds, "first kernel");
-static_assert(up_part_bytes(2) + plan_bytes(kMostSlots, kMostSlots / 16) <= kMostLds, "first kernel, two tiles");
+static_assert(up_part_bytes(2) + plan_bytes(kMostSlots, kMostSlots / kManyChoices) <= kMostLds, "first kernel, two tiles");
 static_assert(down_sum_bytes(kDownTokens, 8, 1) + plan_bytes(kDownTokens * kFewMaxTopK, kMaxExperts) <= kMostLds &&
                   down_sum_bytes(kDownTokens, 4, 2) <= down_sum_bytes(kDownTokens, 8, 1),
               "second kernel");
@@ -1090,9 +1091,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void few_down_kernel(FewArgs a) {
 template <bool kMx, bool kBf16, int kTiles, bool kSort>
 mrr_status launch_up(const FewArgs& a, hipStream_t stream) {
   const int slots = a.T * a.k;
-  // the workgroups that the chip holds at once (by their registers), each taking
-  // its units in turn
-  const int64_t units = static_cast<int64_t>(slots < a.E ? slots : a.E) * (a.I / kRows), most = 256 * (kMx ? 2 : 4);
+  // the workgroups that the chip holds at once (by their registers: two a CU with 4-bit
+  // weights, three with two tiles, else four), each taking its units in turn
+  const int64_t units = static_cast<int64_t>(slots < a.E ? slots : a.E) * (a.I / kRows), most = 256 * (kMx ? 2 : kTiles == 2 ? 3 : 4);
   hipLaunchKernelGGL((few_up_kernel<kMx, kBf16, kTiles, kSort>), dim3(static_cast<unsigned>(units < most ? units : most)),
                      dim3(kUpWaves * 64), up_part_bytes(kTiles) + plan_bytes(slots, a.E), stream, a);
   return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
@@ -1134,11 +1135,22 @@ mrr_status launch_few(const FewArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(few_route_kernel, dim3(a.T), dim3(64), 0, stream, a);
     if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
   }
-  // two tiles of tokens at once where an expert has more than one, on average
+  // Two tiles of tokens at once in the first kernel, and four of eight in the second,
+  // from ten choices an expert on, with 16-bit weights: 64 tokens, 4 of 15 bf16 experts,
+  // H 4096: 165 us, 199 with one tile in the first, 181 with two in the second; 48 tokens,
+  // 4 of 16: 158 and 162; 32 tokens: 155 and 154. 4-bit weights would not leave the
+  // registers for them: 64 tokens, 8 of 16 experts, H 4096: 238 us so, 156 with one tile
+  // in the first kernel, and weights read again for 16 tokens more.
   const int slots = a.T * a.k;
-  const mrr_status st = a.T <= kSelfRouted  ? launch_up<kMx, kBf16, 1, false>(a, stream)
-                        : slots <= 16 * a.E ? launch_up<kMx, kBf16, 1, true>(a, stream)
-                                            : launch_up<kMx, kBf16, 2, true>(a, stream);
+  const bool many = !kMx && slots > kManyChoices * a.E;
+  mrr_status st;
+  if constexpr (kMx) {
+    st = a.T <= kSelfRouted ? launch_up<kMx, kBf16, 1, false>(a, stream) : launch_up<kMx, kBf16, 1, true>(a, stream);
+  } else {
+    st = a.T <= kSelfRouted ? launch_up<kMx, kBf16, 1, false>(a, stream)
+         : many           ? launch_up<kMx, kBf16, 2, true>(a, stream)
+                            : launch_up<kMx, kBf16, 1, true>(a, stream);
+  }
   if (st != MRR_SUCCESS) return st;
   // The second kernel's tiles are of eight tokens: one where an expert has fewer than
   // half of it, on average (48 tokens, 4 of 64 4-bit experts: 202 us, 207 with two;
@@ -1146,9 +1158,10 @@ mrr_status launch_few(const FewArgs& a, hipStream_t stream) {
   // two runs of rows then share (64 tokens, 4 of 32 4-bit experts: 146 us with one run,
   // 134 with two; 64 tokens, 8 of 16 bf16 experts: 264 and 233).
   if (a.T <= kPlaces || slots <= 4 * a.E) return launch_down<kMx, kBf16, 1, 1>(a, stream);
-  if (kMx || slots <= 16 * a.E) return launch_down<kMx, kBf16, 2, 2>(a, stream);
-  if constexpr (!kMx) return launch_down<kMx, kBf16, 4, 2>(a, stream);
-  return MRR_SUCCESS;
+  if constexpr (!kMx) {
+    if (many) return launch_down<kMx, kBf16, 4, 2>(a, stream);
+  }
+  return launch_down<kMx, kBf16, 2, 2>(a, stream);
 }
 
 }  // namespace
