@@ -168,7 +168,7 @@ struct Tiles {
 // such load before it lets any LDS read pass; the kernel waits by itself.
 __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
-               : "memory");
+               : "memory", "m0");
 }
 
 // The four scale bytes of blocks b .. b + 3 of a row of n; 127 (a factor of
