@@ -165,11 +165,15 @@ struct Tiles {
 
 // 16 bytes of every lane, at `base` + its offset, to LDS from byte `lds` on in
 // the order of the lanes. In assembly, as the compiler would wait for every
-// such load before it lets any LDS read pass; the kernel waits by itself.
+// such load before it lets any LDS read pass; the kernel waits by itself. (The
+// compiler warns of m0, which it gives to no variable, but sets by itself elsewhere.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(offset), "s"(base)
                : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // The four scale bytes of blocks b .. b + 3 of a row of n; 127 (a factor of
 // one) past its end. b and n are the same for all lanes.
