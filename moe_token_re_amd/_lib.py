@@ -8,6 +8,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmoe_rerouting_v2.so")
@@ -229,6 +230,31 @@ def binding():
                                "`python -m moe_token_re_amd.build`")
         _binding = _mrr_torch
     return _binding
+
+
+class _NoBinding:
+    """In the place of a binding that is not there: it makes no call."""
+
+    quantize = dequantize = grouped_mm = few_tokens = staticmethod(lambda *args: None)
+
+
+_plain_calls = None
+
+
+def plain_calls():
+    """What makes the experts' operators' plain calls: the native binding, or, where
+    it was not built or does not fit, nothing: the Python code beside it makes every
+    call then, more slowly, and a warning says so once. The library itself has to be
+    there, as for load()."""
+    global _plain_calls
+    if _plain_calls is None:
+        load()
+        try:
+            _plain_calls = binding()
+        except RuntimeError as e:
+            warnings.warn(f"{e}; until then small calls take about twice the host time", RuntimeWarning, stacklevel=3)
+            _plain_calls = _NoBinding
+    return _plain_calls
 
 
 def library_source_hash() -> str:

@@ -6,7 +6,8 @@ mrr_fused.hip, mrr_one_launch.hip; mrr_mx_quant.hip, mrr_grouped_mm.hip,
 mrr_few_tokens.hip, with their own entry points) and the re-routing's entry
 points (mrr_entry.hip) by hipcc, in parallel. Packed-fp32 instructions are
 disabled for all device code. The short way from torch tensors to the experts'
-operators (mrr_torch.cpp) becomes _mrr_torch.so beside it.
+operators (mrr_torch.cpp) becomes _mrr_torch.so beside it, where torch is
+installed; nothing else needs it.
 """
 from __future__ import annotations
 
@@ -83,11 +84,10 @@ def _binding_commands():
 
 
 def build_library(verbose: bool = False) -> str:
-    """Compile and link the library and its torch binding; returns the library's
-    path. Always recompiles."""
+    """Compile and link the library, by g++ and hipcc alone; returns its path.
+    Always recompiles."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    compile_binding, link_binding = _binding_commands()
-    cmds, objs = [compile_binding], []
+    cmds, objs = [], []
     for src in HOST_SOURCES:
         obj = os.path.join(BUILD_DIR, src.replace(".cpp", ".o"))
         cmds.append(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra", "-Werror", "-I", INCLUDE,
@@ -103,9 +103,17 @@ def build_library(verbose: bool = False) -> str:
     tmp = LIB_PATH + ".tmp"
     _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB_PATH)
-    _run(link_binding, verbose)
-    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
     return LIB_PATH
+
+
+def build_binding(verbose: bool = False) -> str:
+    """The short way from torch tensors to the experts' operators, for the torch
+    that is installed and the library that is built; returns its path."""
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    for cmd in _binding_commands():
+        _run(cmd, verbose)
+    os.replace(BINDING_PATH + ".tmp", BINDING_PATH)
+    return BINDING_PATH
 
 
 def build_bench_copy(verbose: bool = False) -> str:
@@ -121,7 +129,14 @@ def build_bench_copy(verbose: bool = False) -> str:
 
 
 def build_all(verbose: bool = False):
-    return build_library(verbose), build_bench_copy(verbose)
+    """All of it; the binding last, and only where there is a torch to bind to."""
+    built = build_library(verbose), build_bench_copy(verbose)
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        print("no torch: the library is built without its torch binding", file=sys.stderr)
+        return built
+    return built + (build_binding(verbose),)
 
 
 if __name__ == "__main__":

@@ -6,7 +6,8 @@ Argument marshalling only, as in api.py: torch provides device memory and the
 current stream; every step runs in the HIP kernels of libmoe_rerouting_v2.so,
 and there is no CPU fallback. A plain call goes by the native binding
 (csrc/mrr_torch.cpp), which launches it or returns None; the code here makes
-every other call and raises every error. The operators serve inference: their
+every other call (all of them, by ctypes, where the binding is not built) and
+raises every error. The operators serve inference: their
 results carry no gradient.
 
 The microscaled format is the one moe_re_routing moves: a row of H values is a
@@ -90,7 +91,7 @@ def mx_quantize(x: torch.Tensor, *, out: Optional[Tuple[torch.Tensor, torch.Tens
     and saturate at 6 times the scale. A block that holds a NaN or an infinity
     becomes NaN as a whole."""
     if out is None:
-        done = _lib.binding().quantize(x)
+        done = _lib.plain_calls().quantize(x)
         if done is not None:
             return done
     dev = _gpu("x", x)
@@ -117,7 +118,7 @@ def mx_dequantize(packed: torch.Tensor, scales: torch.Tensor, *, dtype: torch.dt
     """The values of microscaled 4-bit rows (as mx_quantize returns them), rounded
     once to `dtype` (float16, bfloat16 or float32): [..., H]."""
     if out is None:
-        done = _lib.binding().dequantize(packed, scales, dtype)
+        done = _lib.plain_calls().dequantize(packed, scales, dtype)
         if done is not None:
             return done
     dev = _gpu("packed", packed)
@@ -157,7 +158,7 @@ def mx_grouped_mm(tokens: torch.Tensor, scales: torch.Tensor, weight: torch.Tens
     A nothing is written, and with check=True the call waits for the stream and
     raises MrrValueError."""
     if out is None and workspace is None and not check:
-        done = _lib.binding().grouped_mm(tokens, scales, weight, weight_scales, expert_token_num, gated, row_weight,
+        done = _lib.plain_calls().grouped_mm(tokens, scales, weight, weight_scales, expert_token_num, gated, row_weight,
                                          expert_token_num_type, dtype)
         if done is not None:
             return done
@@ -232,7 +233,7 @@ def moe_few_tokens(x: torch.Tensor, gate_up: torch.Tensor, down: torch.Tensor, *
     outside [0, E) chooses nothing, and k may be more than E: experts of other ranks). Returns y [T, H] of x's dtype; a token
     without experts gives zeros."""
     if out is None and workspace is None:
-        done = _lib.binding().few_tokens(x, gate_up, down, router_logits, top_k, renormalize, expert_ids,
+        done = _lib.plain_calls().few_tokens(x, gate_up, down, router_logits, top_k, renormalize, expert_ids,
                                          expert_weight, gate_up_scales, down_scales)
         if done is not None:
             return done
