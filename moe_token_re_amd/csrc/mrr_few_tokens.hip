@@ -1103,29 +1103,20 @@ template <bool kMx, bool kBf16, int kTiles, int kParts>
 mrr_status launch_down(const FewArgs& a, hipStream_t stream) {
   const int slots = a.T * a.k, tokens = a.T < kDownTokens ? a.T : kDownTokens;
   dim3 grid(a.H / (kRows * kParts), (a.T + kDownTokens - 1) / kDownTokens);
-  const size_t plan = plan_bytes(tokens * a.k, a.E);
   const int runs = static_cast<int>(grid.x * grid.y);
   // Workgroups of a run: with few runs as many as the chip holds (two a CU, by their
   // registers), with four chunks a wave at least, more tokens counting as more chunks
-  // (16 tokens, 6 of 64 fp16 experts, H 2048: 147 us with one, 134 with four; 16 tokens,
-  // 8 of 64 4-bit experts, H 1024: 38 and 29). Few: of eight waves half the CUs, of four,
+  // (16 tokens, 6 of 64 fp16 experts, H 2048: 173 us with one, 147 with four; 16 tokens,
+  // 8 of 64 4-bit experts, H 1024: 57 and 34). Few: of eight waves half the CUs, of four,
   // with two parts, two thirds of them (64 tokens, 4 of 8 4-bit experts, 160 runs: 100 us
   // with one, 93 with three; 4 of 32, 224 runs: 216 and 221 with two).
   const int used = slots < a.E ? slots : a.E, chunks = ((kMx ? a.I / 32 : a.I / 8) + 7) / 8;
   const int steps = used * chunks + slots * chunks / 8;
   if (runs <= (kParts == 1 ? 128 : 170)) grid.z = std::max(1, std::min(static_cast<int>(kFewMostRuns) / runs, steps / 32));
-  auto launch = [&](auto waves) {
-    constexpr int kWaves = decltype(waves)::value;
-    hipLaunchKernelGGL((few_down_kernel<kMx, kBf16, kTiles, kParts, kWaves>), grid, dim3(kWaves * 64),
-                       down_sum_bytes(tokens, kWaves, kParts) + plan, stream, a);
-  };
-  // Up to a workgroup a CU eight waves, else four, so that the chip holds them all
-  // (one token, 8 of 64 4-bit experts, H 7168: 45.6 us with eight, 42.1 with four;
-  // 64 tokens, 4 of 32, H 4096: 128.8 and 133.7).
-  if constexpr (kParts == 1) {
-    if (runs <= 256) launch(std::integral_constant<int, 8>{});
-  }
-  if (kParts > 1 || runs > 256) launch(std::integral_constant<int, 4>{});
+  // Eight waves of one part, four of two: their sums take the same LDS.
+  constexpr int kWaves = kParts == 1 ? 8 : 4;
+  hipLaunchKernelGGL((few_down_kernel<kMx, kBf16, kTiles, kParts, kWaves>), grid, dim3(kWaves * 64),
+                     down_sum_bytes(tokens, kWaves, kParts) + plan_bytes(tokens * a.k, a.E), stream, a);
   return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
 }
 
@@ -1135,33 +1126,28 @@ mrr_status launch_few(const FewArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(few_route_kernel, dim3(a.T), dim3(64), 0, stream, a);
     if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
   }
-  // Two tiles of tokens at once in the first kernel, and four of eight in the second,
-  // from ten choices an expert on, with 16-bit weights: 64 tokens, 4 of 15 bf16 experts,
-  // H 4096: 165 us, 199 with one tile in the first, 181 with two in the second; 48 tokens,
-  // 4 of 16: 158 and 162; 32 tokens: 155 and 154. 4-bit weights would not leave the
-  // registers for them: 64 tokens, 8 of 16 experts, H 4096: 238 us so, 156 with one tile
-  // in the first kernel, and weights read again for 16 tokens more.
-  const int slots = a.T * a.k;
-  const bool many = !kMx && slots > kManyChoices * a.E;
-  mrr_status st;
-  if constexpr (kMx) {
-    st = a.T <= kSelfRouted ? launch_up<kMx, kBf16, 1, false>(a, stream) : launch_up<kMx, kBf16, 1, true>(a, stream);
-  } else {
-    st = a.T <= kSelfRouted ? launch_up<kMx, kBf16, 1, false>(a, stream)
-         : many           ? launch_up<kMx, kBf16, 2, true>(a, stream)
-                            : launch_up<kMx, kBf16, 1, true>(a, stream);
-  }
-  if (st != MRR_SUCCESS) return st;
   // The second kernel's tiles are of eight tokens: one where an expert has fewer than
-  // half of it, on average (48 tokens, 4 of 64 4-bit experts: 202 us, 207 with two;
-  // 64 tokens, 4 of 32: 150 and 134). Two of them are bound by the loads of h, which
-  // two runs of rows then share (64 tokens, 4 of 32 4-bit experts: 146 us with one run,
-  // 134 with two; 64 tokens, 8 of 16 bf16 experts: 264 and 233).
-  if (a.T <= kPlaces || slots <= 4 * a.E) return launch_down<kMx, kBf16, 1, 1>(a, stream);
-  if constexpr (!kMx) {
-    if (many) return launch_down<kMx, kBf16, 4, 2>(a, stream);
-  }
-  return launch_down<kMx, kBf16, 2, 2>(a, stream);
+  // half of it, on average (48 tokens, 4 of 64 4-bit experts: 194 us, 207 with two;
+  // 64 tokens, 4 of 32: 139 and 130). What takes its time beside the weights are the
+  // loads of h, which two runs of rows share: always with 4-bit weights (one token, 8 of
+  // 64 experts, H 7168: 49.1 us, 52.8 with one run; 64 tokens, 4 of 32: 134 and 146), with
+  // 16-bit ones, which are four times as many bytes, where there are two tiles (64
+  // tokens, 8 of 16 bf16 experts: 233 us and 264; with one tile, 32 tokens, 4 of 64: 245
+  // us and 241 with one run).
+  // From ten choices an expert on 16-bit weights have two tiles of sixteen tokens in the
+  // first kernel and four of eight in the second (64 tokens, 4 of 15 bf16 experts, H
+  // 4096: 165 us, 199 with one tile in the first, 181 with two in the second; 48 tokens,
+  // 4 of 16: 158 and 162; 32 tokens: 155 and 154). 4-bit ones would not leave the
+  // registers for them: 64 tokens, 8 of 16 experts, H 4096: 238 us so, 156 with one tile
+  // in the first kernel, and weights read again for each 16 tokens.
+  const int slots = a.T * a.k;
+  const bool few = a.T <= kPlaces || slots <= 4 * a.E, many = slots > kManyChoices * a.E;
+  const mrr_status st = a.T <= kSelfRouted ? launch_up<kMx, kBf16, 1, false>(a, stream)
+                        : kMx || !many     ? launch_up<kMx, kBf16, 1, true>(a, stream)
+                                           : launch_up<kMx, kBf16, kMx ? 1 : 2, true>(a, stream);
+  if (st != MRR_SUCCESS) return st;
+  if (few) return launch_down<kMx, kBf16, 1, kMx ? 2 : 1>(a, stream);
+  return kMx || !many ? launch_down<kMx, kBf16, 2, 2>(a, stream) : launch_down<kMx, kBf16, kMx ? 2 : 4, 2>(a, stream);
 }
 
 }  // namespace
