@@ -1,25 +1,26 @@
 // mrr_few_tokens.hip -- a whole mixture-of-experts layer for a few tokens:
 //     h[t, j] = p[t, j] silu(Wg[e] x[t]) * (Wu[e] x[t])   for e = ids[t, j],
 //     y[t]    = sum over j of Wd[e] h[t, j].
-// Bound by reading the chosen experts' weights, once each (6.3 TB/s is what a kernel
-// reaches that does nothing but read). Two kernels, one a product; for more than a
+// Bound by reading the chosen experts' weights, once each (a kernel that does nothing
+// else reads 6.3 TB/s by way of the caches, 7.1 past them). Two kernels, one a product; for more than a
 // few tokens a third before them finds the routing (softmax and top-k of the
 // router's logits), which every workgroup of the first would otherwise find for
 // itself. The second adds an output row's experts in a fixed order, so results do
-// not depend on timing. What it measured, weights from memory: one token, 8 of 64
-// 4-bit experts, H 7168, I 2048 (187 MB): 51 us, 3.6 TB/s; 16 tokens, 6 of 64 fp16
-// experts, H 2048, I 1408: 146 us, 5.2 TB/s; 64 tokens, 4 of 32 4-bit experts, H 4096, I 2048
-// (430 MB): 117 us, 3.7 TB/s, of which half is issuing instructions: a chunk of
-// 4 KiB of weights takes 250 of them, 64 to widen the weights, 52 to sort lanes.
+// not depend on timing. What it measured: one token, 8 of 64 4-bit experts, H 7168,
+// I 2048 (187 MB): 49 us, 3.8 TB/s; 16 tokens, 6 of 64 fp16 experts by ids, a quarter of
+// them elsewhere, H 2048, I 1408 (762 MB): 148 us, 5.1 TB/s; 64 tokens, 4 of 32 4-bit
+// experts, H 4096, I 2048 (428 MB): 128 us, 3.3 TB/s, of which half is issuing
+// instructions: in the first kernel a chunk of 4 KiB of weights takes 250 of them, 64 to
+// widen the weights, 52 to sort lanes. Here and below weights come from memory, as
+// several layers' take turns, and h and tokens from the caches.
 //
 // Both feed the matrix instructions with 16 weight rows and up to 16 of the tokens
 // that chose the expert. A lane reads 32 bytes of a weight row at a time: 16 16-bit
 // values, or two blocks of 32 4-bit values, widened to bf16 with their scale, which is
 // exact but for the two largest scales (take_blocks). x has 16 bits as it comes. h has
 // no such type, and 16 bits would round it or, fp16, end at 65504: it is held as two
-// bf16 values, hi + lo, off by at most 2^-15.
-// They take two columns of the instruction's 16, so that 8 tokens cost what 16 of one
-// column would; fp16 weights are multiplied as the two bf16 values that they are the
+// bf16 values, hi + lo, off by at most 2^-15. They take two columns of the instruction's
+// 16, so that 8 tokens cost what 16 of one column would; fp16 weights are multiplied as the two bf16 values that they are the
 // sum of. (fp32 products, 16x16x4, would need neither: 64 tokens, 8 of 16 bf16 experts,
 // H 4096, took 289 us with them and 267 so, at one run of rows a wave.)
 #include "mrr_device.h"
@@ -224,8 +225,8 @@ __device__ __forceinline__ Plan carve(uint8_t* lds, int slots, int E) {
 
 // The plan of a few slots, of which a lane has one's expert (-1: none): by every
 // wave alone, without a barrier, as all of them write the same (one token, 2 of 16
-// experts, H 1024: the layer takes 9.0 us so and 10.1 by the counting below; with 64
-// slots it is the other way, 31.7 and 25.8).
+// experts, H 1024: the layer takes 11.1 us so and 12.6 by the counting below; 4 tokens,
+// 8 of 16, 32 slots: 23.1 and 21.1; 64 slots: 30.4 and 24.4).
 constexpr int kSmallPlan = 16;
 static_assert(kSmallPlan >= kFewMaxTopK, "one token's slots");
 __device__ __forceinline__ void make_small_plan(Plan& p, int expert, int slots) {
@@ -622,7 +623,7 @@ __device__ __forceinline__ void store_between(uint8_t* h, const Between& to, int
 // in is read as its last eight pieces, and those that were counted before are cut
 // (rows of fewer than eight pieces: those that follow). kSorted: the tokens are read
 // by neighbouring lanes too; up to four cost less as they are (one token, 8 of 64
-// 4-bit experts, H 7168: 48.7 us so and 56.2 sorted). `next` moves a place to the next
+// 4-bit experts, H 7168: 49.0 us so, 50.3 sorted; four tokens, H 4096: 87 and 90). `next` moves a place to the next
 // sum's first chunk, `again` brings the present one's back.
 template <bool kMx, bool kBf16, int kTiles, From kFrom, int kParts, bool kCareful>
 struct Stream {

@@ -9,9 +9,10 @@
 // expert are not known on the host: every wave scans the counts for its own.
 // What it measured: 16384 rows of 16 experts, gate and up (K 7168, N 4096) 298 us,
 // 3.2 PFLOP/s, where the matrix instructions alone would take 163 (the counters show
-// them half the time; the rest are LDS reads, loads and barriers between them); down
-// (K 2048, N 7168) 175 us, of which some 45 wait for 235 MB of results; 64 rows of 16
-// experts (K 2048, N 4096) 13.9 us, 5.1 TB/s of weights.
+// them in 40% of the active cycles; the rest are LDS reads, loads and barriers between
+// them, and a last round of tiles that is half empty); down (K 2048, N 7168) 175 us, of
+// which some 45 wait for 235 MB of results; 64 rows of 16 experts (K 2048, N 4096)
+// 13.9 us, 5.1 TB/s of weights.
 #include "mrr_device.h"
 #include "mrr_experts.h"
 
@@ -228,8 +229,11 @@ __device__ __forceinline__ float silu(float g) {
 // and columns col0 on of `cols`. A lane has one token row of each fragment and,
 // of its 32 weight rows, four times four neighbours; by way of LDS (kLdsBytes of
 // the wave alone, rows' 16-byte chunks permuted) it stores 16 bytes of a row, and
-// its neighbours the next ones. kStream: past the caches (16384 x 7168 results of
-// bf16, 235 MB: the call takes 154 us instead of 176).
+// its neighbours the next ones. kStream: past the caches, as the large tiles store,
+// whatever the result's size: of bf16, 2048 x 7168 (29 MB) took 30.7 us so and 33.0 by
+// way of the caches, 4096 x 2048 (17 MB, gated, K 7168) 65 and 69, 16384 x 7168 (235 MB)
+// 139 and 159, and quantising them right behind does not turn it: 38.6 us for both and
+// 40.2, 75 and 77, 179 and 196.
 template <typename T, int kFM, int kFN, bool kGated, int kLdsBytes, bool kStream>
 __device__ __forceinline__ void store_tile(const f32x16 (&acc)[kFN][kFM], uint8_t* lds, T* out, const float* row_weight,
                                            int64_t row0, int m0, int rows, int col0, int cols) {
