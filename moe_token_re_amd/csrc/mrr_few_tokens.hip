@@ -2,13 +2,13 @@
 //     h[t, j] = p[t, j] silu(Wg[e] x[t]) * (Wu[e] x[t])   for e = ids[t, j],
 //     y[t]    = sum over j of Wd[e] h[t, j].
 // Bound by reading the chosen experts' weights, once each (a kernel that does nothing
-// else reads 6.3 TB/s by way of the caches, 7.1 past them). Two kernels, one a product; for more than a
-// few tokens a third before them finds the routing (softmax and top-k of the
-// router's logits), which every workgroup of the first would otherwise find for
-// itself. The second adds an output row's experts in a fixed order, so results do
-// not depend on timing. What it measured: one token, 8 of 64 4-bit experts, H 7168,
-// I 2048 (187 MB): 49 us, 3.8 TB/s; 16 tokens, 6 of 64 fp16 experts by ids, a quarter of
-// them elsewhere, H 2048, I 1408 (762 MB): 148 us, 5.1 TB/s; 64 tokens, 4 of 32 4-bit
+// else reads 6.3 TB/s by way of the caches, 7.1 past them). Two kernels, one a product;
+// for more than a few tokens a third before them finds the routing (softmax and top-k
+// of the router's logits), which every workgroup of the first would otherwise find for
+// itself. The second adds an output row's experts in a fixed order, so results do not
+// depend on timing. What it measured: one token, 8 of 64 4-bit experts, H 7168, I 2048
+// (187 MB): 49 us, 3.8 TB/s; 16 tokens, 6 of 64 fp16 experts by ids, a quarter of them
+// elsewhere, H 2048, I 1408 (762 MB): 148 us, 5.1 TB/s; 64 tokens, 4 of 32 4-bit
 // experts, H 4096, I 2048 (428 MB): 128 us, 3.3 TB/s, of which half is issuing
 // instructions: in the first kernel a chunk of 4 KiB of weights takes 250 of them, 64 to
 // widen the weights, 52 to sort lanes. Here and below weights come from memory, as
@@ -20,9 +20,10 @@
 // exact but for the two largest scales (take_blocks). x has 16 bits as it comes. h has
 // no such type, and 16 bits would round it or, fp16, end at 65504: it is held as two
 // bf16 values, hi + lo, off by at most 2^-15. They take two columns of the instruction's
-// 16, so that 8 tokens cost what 16 of one column would; fp16 weights are multiplied as the two bf16 values that they are the
-// sum of. (fp32 products, 16x16x4, would need neither: 64 tokens, 8 of 16 bf16 experts,
-// H 4096, took 289 us with them and 267 so, at one run of rows a wave.)
+// 16, so that 8 tokens cost what 16 of one column would; fp16 weights are multiplied as
+// the two bf16 values that they are the sum of. (fp32 products, 16x16x4, would need
+// neither: 64 tokens, 8 of 16 bf16 experts, H 4096, took 289 us with them and 267 so, at
+// one run of rows a wave.)
 #include "mrr_device.h"
 #include "mrr_experts.h"
 
@@ -68,7 +69,9 @@ struct FewArgs {
   int32_t renormalize;
 };
 
-inline __host__ __device__ constexpr size_t up_part_bytes(int tiles) { return 2 * sizeof(f32x4) * kUpWaves * 2 * tiles * 64; }
+inline __host__ __device__ constexpr size_t up_part_bytes(int tiles) {
+  return 2 * sizeof(f32x4) * kUpWaves * 2 * tiles * 64;
+}
 inline __host__ __device__ constexpr size_t down_sum_bytes(int tokens, int waves, int parts) {
   return sizeof(f32x4) * waves * tokens * 4 * parts;
 }
@@ -204,7 +207,8 @@ inline __host__ __device__ constexpr size_t plan_bytes(int slots, int E) {
 constexpr size_t kMostLds = 64 * 1024;
 constexpr int kMostSlots = MRR_FEW_TOKENS_MAX * static_cast<int>(kFewMaxTopK);
 static_assert(up_part_bytes(1) + plan_bytes(kMostSlots, kMaxExperts) <= kMostLds, "first kernel");
-static_assert(up_part_bytes(2) + plan_bytes(kMostSlots, kMostSlots / kManyChoices) <= kMostLds, "first kernel, two tiles");
+static_assert(up_part_bytes(2) + plan_bytes(kMostSlots, kMostSlots / kManyChoices) <= kMostLds,
+              "first kernel, two tiles");
 static_assert(down_sum_bytes(kDownTokens, 8, 1) + plan_bytes(kDownTokens * kFewMaxTopK, kMaxExperts) <= kMostLds &&
                   down_sum_bytes(kDownTokens, 4, 2) <= down_sum_bytes(kDownTokens, 8, 1),
               "second kernel");
@@ -1094,9 +1098,10 @@ mrr_status launch_up(const FewArgs& a, hipStream_t stream) {
   const int slots = a.T * a.k;
   // the workgroups that the chip holds at once (by their registers: two a CU with 4-bit
   // weights, three with two tiles, else four), each taking its units in turn
-  const int64_t units = static_cast<int64_t>(slots < a.E ? slots : a.E) * (a.I / kRows), most = 256 * (kMx ? 2 : kTiles == 2 ? 3 : 4);
-  hipLaunchKernelGGL((few_up_kernel<kMx, kBf16, kTiles, kSort>), dim3(static_cast<unsigned>(units < most ? units : most)),
-                     dim3(kUpWaves * 64), up_part_bytes(kTiles) + plan_bytes(slots, a.E), stream, a);
+  const int64_t units = static_cast<int64_t>(slots < a.E ? slots : a.E) * (a.I / kRows);
+  const int64_t most = 256 * (kMx ? 2 : kTiles == 2 ? 3 : 4), grid = units < most ? units : most;
+  hipLaunchKernelGGL((few_up_kernel<kMx, kBf16, kTiles, kSort>), dim3(static_cast<unsigned>(grid)), dim3(kUpWaves * 64),
+                     up_part_bytes(kTiles) + plan_bytes(slots, a.E), stream, a);
   return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
 }
 
@@ -1113,7 +1118,8 @@ mrr_status launch_down(const FewArgs& a, hipStream_t stream) {
   // with one, 93 with three; 4 of 32, 224 runs: 216 and 221 with two).
   const int used = slots < a.E ? slots : a.E, chunks = ((kMx ? a.I / 32 : a.I / 8) + 7) / 8;
   const int steps = used * chunks + slots * chunks / 8;
-  if (runs <= (kParts == 1 ? 128 : 170)) grid.z = std::max(1, std::min(static_cast<int>(kFewMostRuns) / runs, steps / 32));
+  if (runs <= (kParts == 1 ? 128 : 170))
+    grid.z = std::max(1, std::min(static_cast<int>(kFewMostRuns) / runs, steps / 32));
   // Eight waves of one part, four of two: their sums take the same LDS.
   constexpr int kWaves = kParts == 1 ? 8 : 4;
   hipLaunchKernelGGL((few_down_kernel<kMx, kBf16, kTiles, kParts, kWaves>), grid, dim3(kWaves * 64),
