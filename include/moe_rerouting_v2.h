@@ -434,6 +434,221 @@ mrr_status mrr_few_tokens_validate(const mrr_few_tokens_args* args, const void* 
 mrr_status mrr_few_tokens(const mrr_few_tokens_args* args, void* workspace, size_t workspace_bytes,
                           struct ihipStream_t* stream);
 
+/* ------------------------------------------------------------------------
+ * The operators around an expert layer: the norm before it, which makes the
+ * 8-bit (or microscaled) rows that are moved; the router's choice of experts;
+ * a rank's tokens sorted by expert, which is the order the all-to-all sends
+ * them in; and the experts' rows summed back by token. Each has its gradient.
+ * The conventions at the top of this file hold for them too: device pointers,
+ * dense rows (of any alignment of their elements), host-detectable errors
+ * before anything is launched, asynchronous on `stream`, no allocation. No
+ * call adds in an order that depends on timing: results are the same bits
+ * each time.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Root-mean-square norm of rows:
+ *     s = x + residual, rounded to x's type (x itself without a residual)
+ *     y = weight * s / sqrt(mean(s^2) + eps)
+ * y is rounded once, to y_dtype:
+ *   - dtype (x's own): no scales.
+ *   - I8 or F8_E4M3FN with scales F32 [rows]: scale = max |y| / 127 or / 448 of
+ *     the row, values y / scale = 127 (448) p / max |p| with p = weight * s,
+ *     rounded to nearest, ties to even. A row of zeros has scale 0. A row of
+ *     which some p is not finite has the scale NaN and zeros as values.
+ *   - F8_E4M3FN or F4_E2M1 with scales F8_E8M0 [rows, ceil(H/64), 2]:
+ *     microscaled, as mrr_mx_quantize() does for 4 bits: 32 values share
+ *     2^(e - 127) with e - 127 = floor(log2(max |y|)) - 8 (e2m1: - 2), clamped to
+ *     [0, 254] in e, values rounded to nearest even, beyond 448 (6) to it;
+ *     a block with a NaN or an infinity has e = 255 and zeros as values.
+ */
+typedef struct mrr_rms_norm_args {
+  const void* x;                   /* [rows, H] F16, BF16 or F32 */
+  int32_t dtype;
+  int64_t rows;                    /* 0 <= rows <= INT32_MAX */
+  int64_t H;                       /* 0 < H <= 16384; even with y_dtype F4_E2M1 */
+  const void* residual;            /* [rows, H], x's dtype; NULL = none */
+  const void* weight;              /* [H] */
+  int32_t weight_dtype;            /* dtype or F32 */
+  double eps;                      /* 2^-126 <= eps < 2^127 */
+  void* y;                         /* [rows, H] */
+  int32_t y_dtype;
+  void* scales;                    /* NULL exactly when y_dtype is dtype */
+  int32_t scales_dtype;            /* F32 or F8_E8M0; not read without scales */
+  void* sum;                       /* [rows, H]: s; NULL exactly when residual is */
+} mrr_rms_norm_args;
+
+/* The checks mrr_rms_norm() makes on the host; no HIP call. */
+mrr_status mrr_rms_norm_validate(const mrr_rms_norm_args* args);
+/* Runs it on `stream`: one kernel. */
+mrr_status mrr_rms_norm(const mrr_rms_norm_args* args, struct ihipStream_t* stream);
+
+/*
+ * The gradient of the norm with an output of x's type. With n = x / sqrt(mean(x^2) + eps):
+ *     grad_x = (grad * weight - n mean(grad * weight * n)) / sqrt(mean(x^2) + eps) + grad_sum
+ *     grad_weight = sum over the rows of grad * n
+ * x is what the norm was taken of: the sum, where a residual was added; grad_x
+ * is then the gradient of both x and residual. Sums are kept in 32 bits, each
+ * result is rounded once.
+ */
+typedef struct mrr_rms_norm_backward_args {
+  const void* grad;                /* [rows, H], dtype */
+  const void* x;                   /* [rows, H] */
+  int32_t dtype;                   /* F16, BF16 or F32 */
+  int64_t rows;
+  int64_t H;                       /* as in mrr_rms_norm_args */
+  const void* weight;              /* [H] */
+  int32_t weight_dtype;            /* dtype or F32 */
+  double eps;
+  const void* grad_sum;            /* [rows, H]: the gradient that reaches the sum by itself; NULL = none */
+  void* grad_x;                    /* [rows, H] */
+  void* grad_weight;               /* [H], weight_dtype */
+} mrr_rms_norm_backward_args;
+
+/* Bytes of workspace (16-byte aligned); 0 for sizes outside the contract. */
+size_t mrr_rms_norm_backward_workspace_size(int64_t rows, int64_t H);
+mrr_status mrr_rms_norm_backward_validate(const mrr_rms_norm_backward_args* args, const void* workspace,
+                                          size_t workspace_bytes);
+/* Runs it on `stream`: two kernels. */
+mrr_status mrr_rms_norm_backward(const mrr_rms_norm_backward_args* args, void* workspace, size_t workspace_bytes,
+                                 struct ihipStream_t* stream);
+
+/*
+ * The router's choice, as mrr_few_tokens() makes it from its logits: the top_k
+ * largest of each row, ties to the lowest expert, in falling order, weighted by
+ * the row's softmax, over all E logits or with renormalize over the chosen
+ * ones. An expert whose logit is -inf is never chosen: where fewer than top_k
+ * are left the id is -1 and the weight 0. NaN counts as the largest; a NaN or
+ * +inf in a row makes the weights of its chosen experts NaN.
+ */
+typedef struct mrr_router_args {
+  const void* logits;              /* [T, E] F16, BF16 or F32 */
+  int32_t dtype;
+  int64_t T;                       /* 0 <= T <= INT32_MAX */
+  int64_t E;                       /* 0 < E <= 1024 */
+  int64_t top_k;                   /* 1 <= top_k <= min(E, 16) */
+  int64_t renormalize;             /* 0 or 1 */
+  float* expert_weight;            /* [T, top_k] */
+  int32_t* expert_ids;             /* [T, top_k] */
+} mrr_router_args;
+
+mrr_status mrr_router_validate(const mrr_router_args* args);
+/* Runs it on `stream`: one kernel. */
+mrr_status mrr_router(const mrr_router_args* args, struct ihipStream_t* stream);
+
+/*
+ * The gradient of expert_weight with respect to the logits. With p the softmax
+ * (over all experts, or the chosen ones) and g the gradient of each p (0 where
+ * it is not returned): grad_logits = p (g - sum of g p). Ids outside [0, E) add
+ * nothing. expert_weight and expert_ids are what mrr_router() returned: no expert
+ * twice in a row.
+ */
+typedef struct mrr_router_backward_args {
+  const float* grad_weight;        /* [T, top_k] */
+  const void* logits;              /* [T, E]; not read with renormalize */
+  int32_t dtype;
+  int64_t T, E, top_k;             /* as in mrr_router_args */
+  int64_t renormalize;
+  const float* expert_weight;      /* [T, top_k] */
+  const int32_t* expert_ids;       /* [T, top_k] */
+  void* grad_logits;               /* [T, E], dtype */
+} mrr_router_backward_args;
+
+mrr_status mrr_router_backward_validate(const mrr_router_backward_args* args);
+mrr_status mrr_router_backward(const mrr_router_backward_args* args, struct ihipStream_t* stream);
+
+/*
+ * Tokens sorted by expert: choice (t, j), the j-th expert of token t, goes to
+ * the row that a stable sort of all choices, in the order t top_k + j, by their
+ * expert gives it:
+ *     permute_tokens[r(t, j)] = tokens[t], and the scales and weights alike.
+ * Experts numbered over all ranks (rank-major) make this the order in which the
+ * all-to-all sends rows, and expert_token_num the counts that it sends. Choices
+ * whose id is outside [0, E) come last, behind the experts' rows; their rows,
+ * scales and weights are zeros, and their index is -1 - r, below 0.
+ */
+typedef struct mrr_token_permute_args {
+  const void* tokens;              /* [T, H], moved as bytes */
+  int32_t tokens_dtype;            /* MRR_F16 .. MRR_F4_E1M2, or MRR_F32 */
+  int64_t T;                       /* 0 <= T, T top_k <= INT32_MAX - 1 */
+  int64_t H;                       /* 0 < H <= 65536; even for fp4 */
+  const int32_t* expert_ids;       /* [T, top_k] */
+  int64_t top_k;                   /* 1 <= top_k <= 16 */
+  int64_t E;                       /* 0 < E <= 4096 */
+  const void* per_token_scales;    /* as in mrr_args with T rows, or NULL */
+  int32_t scales_dtype;
+  int32_t scales_ndim;
+  int64_t scales_dims[3];
+  const float* expert_weight;      /* [T, top_k], or NULL */
+  void* permute_tokens;            /* [T top_k, H] */
+  void* permute_per_token_scales;  /* [T top_k, ...]; NULL exactly without scales */
+  int32_t* permute_token_idx;      /* [T, top_k] */
+  int32_t* expert_token_num;       /* [E] */
+  float* permute_topk_weight;      /* [T top_k, 1]; NULL exactly without expert_weight */
+  int64_t expert_token_num_type;   /* 1: rows per expert; 0: their inclusive running sum */
+} mrr_token_permute_args;
+
+/* Bytes of workspace (16-byte aligned); 0 for sizes outside the contract. */
+size_t mrr_token_permute_workspace_size(int64_t T, int64_t top_k, int64_t E);
+mrr_status mrr_token_permute_validate(const mrr_token_permute_args* args, const void* workspace,
+                                      size_t workspace_bytes);
+/* Runs it on `stream`: one kernel for few choices, three otherwise. */
+mrr_status mrr_token_permute(const mrr_token_permute_args* args, void* workspace, size_t workspace_bytes,
+                             struct ihipStream_t* stream);
+
+/*
+ * The experts' rows summed back by token:
+ *     y[t] = sum over j of expert_weight[t, j] * rows[permute_token_idx[t, j]]
+ * in the order of j, kept in 32 bits and rounded once; without expert_weight
+ * every weight is 1. Indices outside [0, R) add nothing, whatever their weight.
+ * Without weights this is the gradient of mrr_token_permute()'s tokens; with
+ * row_values it also reads one value by index, choice_values[t, j] =
+ * row_values[permute_token_idx[t, j]] (0 for an index outside), which is the
+ * gradient of its weights.
+ */
+typedef struct mrr_token_unpermute_args {
+  const void* rows;                /* [R, H] F16, BF16 or F32 */
+  int32_t dtype;
+  int64_t R;                       /* 0 <= R <= INT32_MAX */
+  int64_t H;                       /* 0 < H <= 65536 */
+  const int32_t* permute_token_idx; /* [T, top_k] */
+  int64_t T;                       /* 0 <= T, T top_k <= INT32_MAX - 1 */
+  int64_t top_k;                   /* 1 <= top_k <= 16 */
+  const float* expert_weight;      /* [T, top_k], or NULL */
+  void* y;                         /* [T, H], rows' dtype */
+  const float* row_values;         /* [R], or NULL */
+  float* choice_values;            /* [T, top_k]; NULL exactly without row_values */
+} mrr_token_unpermute_args;
+
+mrr_status mrr_token_unpermute_validate(const mrr_token_unpermute_args* args);
+/* Runs it on `stream`: one kernel. */
+mrr_status mrr_token_unpermute(const mrr_token_unpermute_args* args, struct ihipStream_t* stream);
+
+/*
+ * The gradients of mrr_token_unpermute():
+ *     grad_rows[permute_token_idx[t, j]] = expert_weight[t, j] * grad[t]
+ *     grad_weight[t, j] = sum over h of grad[t, h] * rows[permute_token_idx[t, j], h]
+ * Indices are those mrr_token_permute() writes: no row is named twice, and one
+ * below 0, -1 - r, means that row r of grad_rows gets zeros and the weight's
+ * gradient is 0. Rows that no index names are left as they were; indices outside
+ * [-R, R) are passed over. Without expert_weight (and grad_weight) rows are not read.
+ */
+typedef struct mrr_token_unpermute_backward_args {
+  const void* grad;                /* [T, H], dtype */
+  const void* rows;                /* [R, H]; not read without expert_weight */
+  int32_t dtype;                   /* F16, BF16 or F32 */
+  int64_t R, H;                    /* as in mrr_token_unpermute_args */
+  const int32_t* permute_token_idx; /* [T, top_k] */
+  int64_t T, top_k;
+  const float* expert_weight;      /* [T, top_k], or NULL */
+  void* grad_rows;                 /* [R, H] */
+  float* grad_weight;              /* [T, top_k]; NULL exactly without expert_weight */
+} mrr_token_unpermute_backward_args;
+
+mrr_status mrr_token_unpermute_backward_validate(const mrr_token_unpermute_backward_args* args);
+/* Runs it on `stream`: one kernel. */
+mrr_status mrr_token_unpermute_backward(const mrr_token_unpermute_backward_args* args, struct ihipStream_t* stream);
+
 #ifdef __cplusplus
 }
 #endif

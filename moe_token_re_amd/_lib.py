@@ -34,7 +34,12 @@ EXPORTS = ("mrr_workspace_size", "mrr_validate", "mrr_describe_plan", "moe_rerou
            "moe_rerouting_v2_offsets", "moe_rerouting_v2_gather", "mrr_get_device_status", "mrr_status_string",
            "mrr_source_hash", "moe_rerouting_v2_noalloc", "mrr_mx_quantize", "mrr_mx_dequantize",
            "mrr_grouped_mm_validate", "mrr_mx_grouped_mm", "mrr_few_tokens_workspace_size",
-           "mrr_few_tokens_validate", "mrr_few_tokens")
+           "mrr_few_tokens_validate", "mrr_few_tokens", "mrr_rms_norm_validate", "mrr_rms_norm",
+           "mrr_rms_norm_backward_workspace_size", "mrr_rms_norm_backward_validate", "mrr_rms_norm_backward",
+           "mrr_router_validate", "mrr_router", "mrr_router_backward_validate", "mrr_router_backward",
+           "mrr_token_permute_workspace_size", "mrr_token_permute_validate", "mrr_token_permute",
+           "mrr_token_unpermute_validate", "mrr_token_unpermute", "mrr_token_unpermute_backward_validate",
+           "mrr_token_unpermute_backward")
 NOALLOC_SCRATCH_BYTES = 8 << 20  # MRR_NOALLOC_SCRATCH_BYTES
 
 
@@ -145,6 +150,137 @@ class MrrFewTokensArgs(ctypes.Structure):
     ]
 
 
+class MrrRmsNormArgs(ctypes.Structure):
+    """struct mrr_rms_norm_args, field for field."""
+
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("rows", ctypes.c_int64),
+        ("H", ctypes.c_int64),
+        ("residual", ctypes.c_void_p),
+        ("weight", ctypes.c_void_p),
+        ("weight_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_double),
+        ("y", ctypes.c_void_p),
+        ("y_dtype", ctypes.c_int32),
+        ("scales", ctypes.c_void_p),
+        ("scales_dtype", ctypes.c_int32),
+        ("sum", ctypes.c_void_p),
+    ]
+
+
+class MrrRmsNormBackwardArgs(ctypes.Structure):
+    """struct mrr_rms_norm_backward_args, field for field."""
+
+    _fields_ = [
+        ("grad", ctypes.c_void_p),
+        ("x", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("rows", ctypes.c_int64),
+        ("H", ctypes.c_int64),
+        ("weight", ctypes.c_void_p),
+        ("weight_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_double),
+        ("grad_sum", ctypes.c_void_p),
+        ("grad_x", ctypes.c_void_p),
+        ("grad_weight", ctypes.c_void_p),
+    ]
+
+
+class MrrRouterArgs(ctypes.Structure):
+    """struct mrr_router_args, field for field."""
+
+    _fields_ = [
+        ("logits", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("T", ctypes.c_int64),
+        ("E", ctypes.c_int64),
+        ("top_k", ctypes.c_int64),
+        ("renormalize", ctypes.c_int64),
+        ("expert_weight", ctypes.c_void_p),
+        ("expert_ids", ctypes.c_void_p),
+    ]
+
+
+class MrrRouterBackwardArgs(ctypes.Structure):
+    """struct mrr_router_backward_args, field for field."""
+
+    _fields_ = [
+        ("grad_weight", ctypes.c_void_p),
+        ("logits", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("T", ctypes.c_int64),
+        ("E", ctypes.c_int64),
+        ("top_k", ctypes.c_int64),
+        ("renormalize", ctypes.c_int64),
+        ("expert_weight", ctypes.c_void_p),
+        ("expert_ids", ctypes.c_void_p),
+        ("grad_logits", ctypes.c_void_p),
+    ]
+
+
+class MrrTokenPermuteArgs(ctypes.Structure):
+    """struct mrr_token_permute_args, field for field."""
+
+    _fields_ = [
+        ("tokens", ctypes.c_void_p),
+        ("tokens_dtype", ctypes.c_int32),
+        ("T", ctypes.c_int64),
+        ("H", ctypes.c_int64),
+        ("expert_ids", ctypes.c_void_p),
+        ("top_k", ctypes.c_int64),
+        ("E", ctypes.c_int64),
+        ("per_token_scales", ctypes.c_void_p),
+        ("scales_dtype", ctypes.c_int32),
+        ("scales_ndim", ctypes.c_int32),
+        ("scales_dims", ctypes.c_int64 * 3),
+        ("expert_weight", ctypes.c_void_p),
+        ("permute_tokens", ctypes.c_void_p),
+        ("permute_per_token_scales", ctypes.c_void_p),
+        ("permute_token_idx", ctypes.c_void_p),
+        ("expert_token_num", ctypes.c_void_p),
+        ("permute_topk_weight", ctypes.c_void_p),
+        ("expert_token_num_type", ctypes.c_int64),
+    ]
+
+
+class MrrTokenUnpermuteArgs(ctypes.Structure):
+    """struct mrr_token_unpermute_args, field for field."""
+
+    _fields_ = [
+        ("rows", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("R", ctypes.c_int64),
+        ("H", ctypes.c_int64),
+        ("permute_token_idx", ctypes.c_void_p),
+        ("T", ctypes.c_int64),
+        ("top_k", ctypes.c_int64),
+        ("expert_weight", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("row_values", ctypes.c_void_p),
+        ("choice_values", ctypes.c_void_p),
+    ]
+
+
+class MrrTokenUnpermuteBackwardArgs(ctypes.Structure):
+    """struct mrr_token_unpermute_backward_args, field for field."""
+
+    _fields_ = [
+        ("grad", ctypes.c_void_p),
+        ("rows", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("R", ctypes.c_int64),
+        ("H", ctypes.c_int64),
+        ("permute_token_idx", ctypes.c_void_p),
+        ("T", ctypes.c_int64),
+        ("top_k", ctypes.c_int64),
+        ("expert_weight", ctypes.c_void_p),
+        ("grad_rows", ctypes.c_void_p),
+        ("grad_weight", ctypes.c_void_p),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -203,6 +339,21 @@ def load() -> ctypes.CDLL:
             lib.mrr_few_tokens.restype = ctypes.c_int
             lib.mrr_few_tokens_workspace_size.argtypes = [ctypes.c_int64] * 3
             lib.mrr_few_tokens_workspace_size.restype = sz
+            for name, struct in (("rms_norm", MrrRmsNormArgs), ("router", MrrRouterArgs),
+                                 ("router_backward", MrrRouterBackwardArgs),
+                                 ("token_unpermute", MrrTokenUnpermuteArgs),
+                                 ("token_unpermute_backward", MrrTokenUnpermuteBackwardArgs)):
+                for fn, more in ((f"mrr_{name}_validate", []), (f"mrr_{name}", [vp])):
+                    getattr(lib, fn).argtypes = [ctypes.POINTER(struct)] + more
+                    getattr(lib, fn).restype = ctypes.c_int
+            for name, struct, sizes in (("rms_norm_backward", MrrRmsNormBackwardArgs, 2),
+                                        ("token_permute", MrrTokenPermuteArgs, 3)):
+                for fn, more in ((f"mrr_{name}_validate", []), (f"mrr_{name}", [vp])):
+                    getattr(lib, fn).argtypes = [ctypes.POINTER(struct), vp, sz] + more
+                    getattr(lib, fn).restype = ctypes.c_int
+                size = getattr(lib, f"mrr_{name}_workspace_size")
+                size.argtypes = [ctypes.c_int64] * sizes
+                size.restype = sz
             lib.mrr_status_string.argtypes = [ctypes.c_int]
             lib.mrr_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -213,7 +364,7 @@ _binding = None
 
 
 def binding():
-    """The native binding of the experts' operators (_mrr_torch.so), built with
+    """The native binding of the experts' and the layer's operators (_mrr_torch.so), built with
     the library; raises RuntimeError like load()."""
     global _binding
     if _binding is None:
@@ -236,13 +387,15 @@ class _NoBinding:
     """In the place of a binding that is not there: it makes no call."""
 
     quantize = dequantize = grouped_mm = few_tokens = staticmethod(lambda *args: None)
+    rms_norm = rms_norm_backward = router = router_backward = staticmethod(lambda *args: None)
+    permute = unpermute = unpermute_backward = staticmethod(lambda *args: None)
 
 
 _plain_calls = None
 
 
 def plain_calls():
-    """What makes the experts' operators' plain calls: the native binding, or, where
+    """What makes the experts' and the layer's operators' plain calls: the native binding, or, where
     it was not built or does not fit, nothing: the Python code beside it makes every
     call then, more slowly, and a warning says so once. The library itself has to be
     there, as for load()."""

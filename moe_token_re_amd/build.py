@@ -1,11 +1,11 @@
 """Builds the HIP library libmoe_rerouting_v2.so in-tree, for gfx950.
 
-The host checks (mrr_validate.cpp, mrr_experts_validate.cpp) are compiled by
-g++ with no HIP header; the kernel files (mrr_offsets.hip, mrr_gather.hip,
-mrr_fused.hip, mrr_one_launch.hip; mrr_mx_quant.hip, mrr_grouped_mm.hip,
-mrr_few_tokens.hip, with their own entry points) and the re-routing's entry
-points (mrr_entry.hip) by hipcc, in parallel. Packed-fp32 instructions are
-disabled for all device code. The short way from torch tensors to the experts'
+The host checks (mrr_validate.cpp, mrr_experts_validate.cpp,
+mrr_layer_validate.cpp) are compiled by g++ with no HIP header; the kernel files
+(mrr_offsets.hip, mrr_gather.hip, mrr_fused.hip, mrr_one_launch.hip; and those of
+the experts' operators and the ones around a layer, with their own entry points)
+and the re-routing's entry points (mrr_entry.hip) by hipcc, in parallel. Packed-fp32 instructions are
+disabled for all device code. The short way from torch tensors to those
 operators (mrr_torch.cpp) becomes _mrr_torch.so beside it, where torch is
 installed; nothing else needs it.
 """
@@ -62,8 +62,9 @@ def _run(cmd, verbose):
 
 
 HIP_SOURCES = ("mrr_offsets.hip", "mrr_gather.hip", "mrr_fused.hip", "mrr_one_launch.hip", "mrr_entry.hip",
-               "mrr_mx_quant.hip", "mrr_grouped_mm.hip", "mrr_few_tokens.hip")
-HOST_SOURCES = ("mrr_validate.cpp", "mrr_experts_validate.cpp")
+               "mrr_mx_quant.hip", "mrr_grouped_mm.hip", "mrr_few_tokens.hip", "mrr_rms_norm.hip",
+               "mrr_rms_norm_backward.hip", "mrr_router.hip", "mrr_token_permute.hip", "mrr_token_unpermute.hip")
+HOST_SOURCES = ("mrr_validate.cpp", "mrr_experts_validate.cpp", "mrr_layer_validate.cpp")
 
 
 def _binding_commands():

@@ -1,0 +1,79 @@
+// mrr_layer.h -- shared between the host checks of the operators around an
+// expert layer (mrr_layer_validate.cpp, which includes no HIP header) and their
+// kernels (mrr_rms_norm.hip, mrr_rms_norm_backward.hip, mrr_router.hip,
+// mrr_token_permute.hip, mrr_token_unpermute.hip). Not part of the public ABI.
+#pragma once
+
+#include "mrr_internal.h"
+
+namespace mrr {
+
+constexpr int64_t kNormMaxH = 16384;
+constexpr int64_t kLayerMaxTopK = 16;
+constexpr int64_t kRouterMaxExperts = 1024;
+constexpr int64_t kPermuteMaxExperts = 4096;
+constexpr int64_t kPermuteMaxH = 65536;
+
+// How rows of H values lie on the lanes of the norm's kernels: 8 neighbouring
+// values a lane and unit, `lanes` lanes and `units` units a lane a row.
+struct NormShape {
+  int lanes, units;
+};
+// Rows up to this many take more lanes a row: they leave most of the chip empty.
+constexpr int64_t kNormFewRows = 256;
+inline NormShape norm_shape(int64_t rows, int64_t H) {
+  if (H <= 512) return {64, 1};
+  if (rows <= kNormFewRows) return H <= 2048 ? NormShape{256, 1} : H <= 8192 ? NormShape{1024, 1} : NormShape{1024, 2};
+  if (H <= 1024) return {64, 2};
+  if (H <= 2048) return {256, 1};
+  if (H <= 4096) return {256, 2};
+  if (H <= 8192) return {256, 4};
+  return {1024, 2};
+}
+
+// The same for the gradient, which keeps three times as much of a row in registers.
+inline NormShape norm_backward_shape(int64_t rows, int64_t H) {
+  const NormShape s = norm_shape(rows, H);
+  return s.lanes < 1024 ? s : NormShape{512, 2 * s.units};
+}
+// Workgroups that each take every so-manieth row and keep a partial sum of the weight's
+// gradient for each of their rows that run at once.
+constexpr int64_t kNormBackwardGroups = 512;
+inline int64_t norm_backward_groups(int64_t rows, int64_t H) {
+  const NormShape s = norm_backward_shape(rows, H);
+  const int64_t at_once = s.lanes == 64 ? 4 : 1, most = s.lanes == 512 ? kNormBackwardGroups / 2 : kNormBackwardGroups;
+  const int64_t groups = (rows + at_once - 1) / at_once;
+  return at_once * (groups < most ? groups : most);
+}
+
+// Few choices are sorted by every workgroup of one kernel by itself; more in blocks,
+// whose counts by expert [blocks, E + 1] lie in the workspace: so many blocks that the
+// counts, which every block reads, stay few, and none smaller than a workgroup.
+constexpr int64_t kPermuteFewChoices = 4096;
+constexpr int64_t kPermuteBlockChoices = 1024;
+constexpr int64_t kPermuteMostCounts = 32768;
+inline int64_t permute_block(int64_t choices, int64_t E) {
+  int64_t blocks = kPermuteMostCounts / (E + 1);
+  blocks = blocks < 1 ? 1 : blocks > 256 ? 256 : blocks;
+  const int64_t each = (choices + blocks - 1) / blocks;
+  return each <= kPermuteBlockChoices ? kPermuteBlockChoices
+                                      : static_cast<int64_t>(round_up(static_cast<size_t>(each), kPermuteBlockChoices));
+}
+inline int64_t permute_blocks(int64_t choices, int64_t E) {
+  const int64_t block = permute_block(choices, E);
+  return (choices + block - 1) / block;
+}
+
+mrr_status check_rms_norm(const mrr_rms_norm_args* a);
+mrr_status check_rms_norm_backward(const mrr_rms_norm_backward_args* a, const void* ws, size_t ws_bytes);
+mrr_status check_router(const mrr_router_args* a);
+mrr_status check_router_backward(const mrr_router_backward_args* a);
+mrr_status check_token_permute(const mrr_token_permute_args* a, const void* ws, size_t ws_bytes);
+mrr_status check_token_unpermute(const mrr_token_unpermute_args* a);
+mrr_status check_token_unpermute_backward(const mrr_token_unpermute_backward_args* a);
+
+// Bytes of a token's row and of its scales' (0: none), of checked arguments.
+int64_t permute_row_bytes(const mrr_token_permute_args* a);
+int64_t permute_scale_bytes(const mrr_token_permute_args* a);
+
+}  // namespace mrr

@@ -1,0 +1,168 @@
+// mrr_rows.h -- rows of fp16, bf16 or fp32 values in a wave's registers, some
+// neighbouring ones a lane, and sums over a wave or a workgroup. Device code
+// of the norm and the row sums.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "mrr_layer.h"
+
+namespace mrr {
+
+using f32x2 = float __attribute__((ext_vector_type(2)));
+using rows_u32x4 = uint32_t __attribute__((ext_vector_type(4)));
+
+// 16 bytes at any alignment, past the caches where kStream.
+template <bool kStream>
+__device__ __forceinline__ rows_u32x4 load16(const uint8_t* p) {
+  using loose = rows_u32x4 __attribute__((aligned(1)));
+  if constexpr (kStream) return __builtin_nontemporal_load(reinterpret_cast<const loose*>(p));
+  return *reinterpret_cast<const loose*>(p);
+}
+template <bool kStream>
+__device__ __forceinline__ void store16(uint8_t* p, rows_u32x4 v) {
+  using loose = rows_u32x4 __attribute__((aligned(1)));
+  if constexpr (kStream)
+    __builtin_nontemporal_store(v, reinterpret_cast<loose*>(p));
+  else
+    *reinterpret_cast<loose*>(p) = v;
+}
+
+// kN neighbouring values of a row as they lie in memory, a multiple of 16 bytes; fewer
+// at the row's end, zeros behind.
+template <int kDtype, int kN>
+struct Pack {
+  static constexpr int kBytes = kDtype == MRR_F32 ? 4 : 2;
+  static constexpr int kWords = kBytes * kN / 4;  // of 4 bytes
+  uint32_t w[kWords];
+
+  template <bool kStream>
+  __device__ __forceinline__ void load(const uint8_t* row, uint32_t col, uint32_t H) {
+    const uint8_t* p = row + static_cast<size_t>(col) * kBytes;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+    if (col + kN <= H) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const rows_u32x4 v = load16<kStream>(p + 4 * i);
+        w[i] = v[0], w[i + 1] = v[1], w[i + 2] = v[2], w[i + 3] = v[3];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kN - 1; ++k)
+        if (col + k < H) {
+          if constexpr (kBytes == 4) {
+            __builtin_memcpy(&w[k], p + 4 * k, 4);
+          } else {
+            uint16_t v;
+            __builtin_memcpy(&v, p + 2 * k, 2);
+            w[k / 2] |= static_cast<uint32_t>(v) << (k % 2 * 16);
+          }
+        }
+    }
+  }
+
+  template <bool kStream>
+  __device__ __forceinline__ void store(uint8_t* row, uint32_t col, uint32_t H) const {
+    uint8_t* p = row + static_cast<size_t>(col) * kBytes;
+    if (col + kN <= H) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) store16<kStream>(p + 4 * i, rows_u32x4{w[i], w[i + 1], w[i + 2], w[i + 3]});
+    } else {
+#pragma unroll
+      for (int k = 0; k < kN - 1; ++k)
+        if (col + k < H) {
+          if constexpr (kBytes == 4) {
+            __builtin_memcpy(p + 4 * k, &w[k], 4);
+          } else {
+            const uint16_t v = static_cast<uint16_t>(w[k / 2] >> (k % 2 * 16));
+            __builtin_memcpy(p + 2 * k, &v, 2);
+          }
+        }
+    }
+  }
+
+  __device__ __forceinline__ float get(int k) const {
+    if constexpr (kDtype == MRR_F32) return __uint_as_float(w[k]);
+    const uint32_t v = w[k / 2];
+    if constexpr (kDtype == MRR_BF16) return __uint_as_float(k % 2 ? v & 0xffff0000u : v << 16);
+    using f16x2 = _Float16 __attribute__((ext_vector_type(2)));
+    return static_cast<float>(__builtin_bit_cast(f16x2, v)[k % 2]);
+  }
+
+  // Values 2 i and 2 i + 1, rounded to nearest even.
+  __device__ __forceinline__ void put(int i, float a, float b) {
+    if constexpr (kDtype == MRR_F32) {
+      w[2 * i] = __float_as_uint(a), w[2 * i + 1] = __float_as_uint(b);
+    } else {
+      using T = std::conditional_t<kDtype == MRR_BF16, __bf16, _Float16>;
+      using T2 = T __attribute__((ext_vector_type(2)));
+      w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, T2));
+    }
+  }
+};
+template <int kDtype>
+using Eight = Pack<kDtype, 8>;
+// 16 bytes of them.
+template <int kDtype>
+using Unit16 = Pack<kDtype, kDtype == MRR_F32 ? 4 : 8>;
+
+// Lane i takes lane i ^ 1, i ^ 2's value of its four, 7 - i's of its eight, 15 - i's
+// of its sixteen: sums and maxima over those many lanes, without LDS.
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppMirror8 = 0x141, kDppMirror16 = 0x140;
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), kCtrl, 0xf, 0xf, true));
+}
+template <int kCtrl>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __uint_as_float(dpp_u32<kCtrl>(__float_as_uint(v)));
+}
+
+// Sums over the 16 lanes of a row of lanes, every lane getting the result.
+__device__ __forceinline__ float sum16_f32(float v) {
+  v += dpp_f32<kDppXor1>(v);
+  v += dpp_f32<kDppXor2>(v);
+  v += dpp_f32<kDppMirror8>(v);
+  return v + dpp_f32<kDppMirror16>(v);
+}
+__device__ __forceinline__ uint32_t max16_u32(uint32_t v) {
+  v = max(v, dpp_u32<kDppXor1>(v));
+  v = max(v, dpp_u32<kDppXor2>(v));
+  v = max(v, dpp_u32<kDppMirror8>(v));
+  return max(v, dpp_u32<kDppMirror16>(v));
+}
+__device__ __forceinline__ uint32_t min16_u32(uint32_t v) { return ~max16_u32(~v); }
+
+// Over all 64 lanes.
+__device__ __forceinline__ float sum64_f32(float v) {
+  v = sum16_f32(v);
+  v += __shfl_xor(v, 16);
+  return v + __shfl_xor(v, 32);
+}
+__device__ __forceinline__ uint32_t max64_u32(uint32_t v) {
+  v = max16_u32(v);
+  v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 16)));
+  return max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), 32)));
+}
+__device__ __forceinline__ double sum64_f64(double v) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d);
+  return v;
+}
+__device__ __forceinline__ double max64_f64(double v) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) v = fmax(v, __shfl_xor(v, d));
+  return v;
+}
+
+// Rows src [T] to rows dst [R] by an index [T, k], zeros for an index below 0, -1 - row
+// (mrr_token_permute.hip).
+void move_rows(const void* src, void* dst, int64_t row_bytes, const int32_t* idx, int64_t T, int64_t k, int64_t R,
+               hipStream_t stream);
+
+}  // namespace mrr

@@ -1,0 +1,635 @@
+"""The operators around an expert layer on the GPU (rms_norm, moe_router_top_k,
+moe_token_permute, moe_token_unpermute and their gradients) against their
+definitions in 64 bits (layer_reference.py).
+
+Tolerances. A result is rounded once to its type, by at most half a step:
+finfo(t).eps / 2 of its size (or half of the smallest subnormal step, finfo.tiny
+eps / 2). Before that, fp32: a row's sum is at most 64 additions a lane
+and 10 across, each off by 2^-24 of a partial sum that is at most the sum of the
+terms' sizes, with a few more roundings on the way: F32 = 2^-17 of the terms'
+sizes covers 128 of them."""
+import math
+import zlib
+
+import layer_reference as ref
+import pytest
+import torch
+
+import moe_token_re_amd as moe
+from gpu_helpers import Guarded, _dev
+
+pytestmark = pytest.mark.gpu
+
+F32 = 2.0 ** -17
+BF16, F16, FP32 = torch.bfloat16, torch.float16, torch.float32
+PAIRS = [(BF16, BF16), (BF16, FP32), (F16, F16), (F16, FP32), (FP32, FP32)]
+
+
+def near(got, want, size, dtype=None):
+    """got is want, rounded to its type, with 32-bit errors relative to `size`."""
+    info = torch.finfo(dtype or got.dtype)
+    got = got.double().cpu()
+    want, size = want.double().cpu(), size.double().cpu()
+    most = want.abs() * info.eps / 2 + size * F32 + info.tiny * info.eps
+    off = (got - want).abs() - most
+    assert got.shape == want.shape and not torch.isnan(got).any()
+    assert (off <= 0).all(), f"off by {float(off.max())} more than {float(most.flatten()[off.argmax()])}"
+
+
+def same(a, b):
+    a, b = (None if t is None else t.detach().contiguous().view(-1).view(torch.uint8).cpu() for t in (a, b))
+    return (a is None and b is None) or torch.equal(a, b)
+
+
+def odd(t, guard=None, name=""):
+    """The same values one element past an aligned address."""
+    buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    buf[1:] = t.reshape(-1)
+    return buf[1:].view(t.shape)
+
+
+def rows_like(g, T, H, dtype, dev):
+    x = torch.randn(T, H, generator=g) * torch.exp(0.5 * torch.randn(T, 1, generator=g))
+    x[:, ::97] *= 8
+    return x.to(dtype).to(dev)
+
+
+def gen(*parts):
+    return torch.Generator().manual_seed(zlib.crc32(repr(parts).encode()))
+
+
+# ------------------------------------------------------------------------ norm
+
+# a wave a row, four waves, sixteen; rows that end inside a unit; few and many rows
+SHAPES = [(1, 1), (3, 5), (2, 33), (7, 512), (9, 513), (1, 7168), (5, 1059), (257, 777), (300, 1024), (261, 1999),
+          (260, 2049), (258, 4097), (259, 7168), (300, 8191), (3, 8200), (270, 9001), (2, 16384), (260, 16384)]
+
+
+def check_values(q, unrounded, rounder, d):
+    """Every value is the rounding of a number within d of the exact one."""
+    q = q.double().cpu()
+    lo, hi = rounder(unrounded * (1 - d)), rounder(unrounded * (1 + d))
+    lo, hi = torch.minimum(lo, hi), torch.maximum(lo, hi)
+    assert ((q >= lo) & (q <= hi)).all()
+
+
+def check_norm(out, s, weight, eps, quantize):
+    y, scales, _ = out
+    want, p = ref.norm(s.cpu(), weight.cpu(), eps)
+    if quantize is None:
+        near(y, want, want.abs())
+        return
+    H = want.shape[1]
+    if quantize in ("int8", "fp8"):
+        most = 127 if quantize == "int8" else 448
+        near(scales, want.abs().amax(1) / most, want.abs().amax(1) / most)
+        top = p.abs().amax(1, keepdim=True).clamp(min=1e-300)
+        exact_products = s.dtype != FP32 and weight.dtype == s.dtype and s.dtype == BF16
+        # bf16 products (and 127 of them) are exact in 32 bits, and so is the quotient's rounding
+        check_values(y, most * p / top, torch.round if most == 127 else ref.e4m3, 0.0 if exact_products else F32)
+        return
+    blocks = 2 * math.ceil(H / 64)
+    least = 8 if quantize == "mxfp8" else 2
+    code = scales.view(torch.uint8).cpu().view(-1, blocks).long()
+    padded = torch.nn.functional.pad(want, (0, 32 * blocks - H)).view(-1, blocks, 32)
+    top = padded.abs().amax(-1)
+    for d in (-F32, F32):  # floor(log2) of a largest value within F32 of the exact one
+        e = torch.floor(torch.log2((top * (1 + d)).clamp(min=2.0 ** -200))).long() - least + 127
+        e = torch.where(top > 0, e.clamp(0, 254), 0)
+        assert ((code - e) * (1 if d < 0 else -1) >= 0).all()
+    unit = torch.exp2(code.double() - 127)[..., None]
+    if quantize == "mxfp8":
+        values = torch.nn.functional.pad(y.double().cpu(), (0, 32 * blocks - H)).view(-1, blocks, 32)
+        check_values(values, padded / unit, ref.e4m3, F32)
+    else:
+        b = y.view(torch.uint8).cpu()
+        c = torch.stack((b & 15, b >> 4), -1).flatten(-2).long()
+        v = torch.tensor([0.0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64)[c]
+        check_values(torch.nn.functional.pad(v, (0, 32 * blocks - H)).view(-1, blocks, 32), padded / unit, ref.e2m1, F32)
+
+
+@pytest.mark.parametrize("quantize", [None, "int8", "fp8", "mxfp8", "mxfp4"])
+@pytest.mark.parametrize("T,H", SHAPES)
+def test_norm(T, H, quantize):
+    dev = _dev()
+    if quantize == "mxfp4" and H % 2:
+        with pytest.raises(ValueError):
+            moe.rms_norm(torch.ones(T, H, device=dev), torch.ones(H, device=dev), quantize=quantize)
+        return
+    for n, (xt, wt) in enumerate(PAIRS):
+        g = gen("norm", T, H, n)
+        x, w = rows_like(g, T, H, xt, dev), (1 + 0.3 * torch.randn(H, generator=g)).to(wt).to(dev)
+        r = rows_like(g, T, H, xt, dev) if (T + n) % 2 else None
+        out = moe.rms_norm(x, w, residual=r, quantize=quantize, eps=1e-5)
+        s = ref.norm_sum(x, r)
+        assert (out[2] is None) == (r is None) and (r is None or same(out[2], s))
+        check_norm(out, s, w, 1e-5, quantize)
+        # the same bits from any address, with the outputs between guards
+        guard = Guarded()
+        outs = tuple(None if t is None else guard.like(str(i), t) for i, t in enumerate(out))
+        moe.rms_norm(odd(x), odd(w), residual=None if r is None else odd(r), quantize=quantize, eps=1e-5, out=outs)
+        torch.cuda.synchronize()
+        guard.check()
+        assert all(same(a, b) for a, b in zip(out, outs))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, FP32])
+@pytest.mark.parametrize("H", [96, 5000])
+def test_norm_of_rows_that_are_not_finite_or_all_zero(H, dtype):
+    dev = _dev()
+    x = torch.randn(6, H, generator=gen(H, str(dtype))).to(dtype).to(dev)
+    x[1] = 0
+    x[2, 3], x[3, 40], x[4, 7] = float("nan"), float("inf"), float("-inf")
+    w = torch.ones(H, dtype=dtype, device=dev)
+    y, _, _ = moe.rms_norm(x, w)
+    assert (y[1] == 0).all() and torch.isnan(y[2]).all()
+    for r, c in ((3, 40), (4, 7)):
+        assert torch.isnan(y[r, c]) and (y[r, :c] == 0).all() and (y[r, c + 1:] == 0).all()
+    for q in ("int8", "fp8"):
+        y, scales, _ = moe.rms_norm(x, w, quantize=q)
+        assert scales[1] == 0 and torch.isnan(scales[2:5]).all() and torch.isfinite(scales[[0, 5]]).all()
+        assert (y[1:5].float() == 0).all()
+    for q in ("mxfp8", "mxfp4"):
+        y, scales, _ = moe.rms_norm(x, w, quantize=q)
+        codes = scales.view(torch.uint8).view(6, -1)
+        assert (codes[1] == 0).all() and (codes[2][:H // 32] == 255).all()
+        assert codes[3, 1] == 255 and codes[4, 0] == 255 and codes[3, 0] == 0 and codes[4, 1] == 0
+        assert (y[1:5].view(torch.uint8) & 0x77 == 0).all() if q == "mxfp4" else (y[1:5].float() == 0).all()
+
+
+@pytest.mark.parametrize("size,eps", [(1e30, 1e-6), (1e37, 1e-6), (1e-25, 1e-30), (1e-36, 1.2e-38), (1e-25, 1e-6)])
+@pytest.mark.parametrize("H", [64, 3000])
+def test_norm_at_the_ends_of_the_range(H, size, eps):
+    """Squares beyond 32 bits on either side; weights that take products there."""
+    dev = _dev()
+    g = gen(H, size)
+    for dtype in (BF16, FP32):
+        x = (torch.randn(3, H, generator=g).double() * size).to(dtype).to(dev)
+        for by in (1.0, 1e-30, 1e8):
+            w = ((1 + 0.3 * torch.randn(H, generator=g)) * by).to(dtype).to(dev)
+            want, p = ref.norm(x.cpu(), w.cpu(), eps)
+            y, _, _ = moe.rms_norm(x, w, eps=eps)
+            near(y, want, want.abs())
+            top = want.abs().amax(1)
+            if float(top.min()) < 1e-36:
+                continue  # the scale itself is subnormal
+            for q, most, rounder in (("int8", 127, torch.round), ("fp8", 448, ref.e4m3)):
+                y, scales, _ = moe.rms_norm(x, w, eps=eps, quantize=q)
+                near(scales, top / most, top / most)
+                check_values(y, most * p / p.abs().amax(1, keepdim=True), rounder, F32)
+
+
+def test_norm_ties_go_to_even():
+    """127 p / max |p| halfway between whole numbers, exactly: products k + 0.5 under a largest of 127."""
+    dev = _dev()
+    k = torch.arange(-63, 63).float() + 0.5
+    x = torch.cat([torch.tensor([127.0]), k]).to(BF16).to(dev)[None]
+    y, scales, _ = moe.rms_norm(x, torch.ones(x.shape[1], dtype=BF16, device=dev), quantize="int8")
+    assert torch.equal(y[0, 1:].cpu().float(), torch.round(k))  # torch.round is to even
+    y, _, _ = moe.rms_norm(x * 2, torch.full((x.shape[1],), 0.125, dtype=BF16, device=dev), quantize="int8")
+    assert torch.equal(y[0, 1:].cpu().float(), torch.round(k))
+
+
+def test_norm_of_any_rank_and_of_no_rows():
+    dev = _dev()
+    x = torch.randn(2, 3, 40, generator=gen("rank")).to(BF16).to(dev)
+    w = torch.ones(40, dtype=BF16, device=dev)
+    for q, shape in ((None, None), ("int8", (2, 3)), ("mxfp4", (2, 3, 1, 2))):
+        y, scales, _ = moe.rms_norm(x, w, quantize=q)
+        flat = moe.rms_norm(x.view(6, 40), w, quantize=q)
+        assert same(y, flat[0]) and same(scales, flat[1]) and (scales is None or tuple(scales.shape) == shape)
+        assert same(moe.rms_norm(x[0, 0], w, quantize=q)[0], y[0, 0])
+        none = moe.rms_norm(x[:0], w, quantize=q, residual=x[:0])
+        assert none[0].shape[0] == 0 and none[2].shape == (0, 3, 40)
+    d, dw = moe.rms_norm_backward(x[:0], x[:0], w)
+    assert d.shape == (0, 3, 40) and (dw == 0).all()
+
+
+@pytest.mark.parametrize("T,H", SHAPES + [(2100, 100), (1100, 4000)])
+def test_norm_backward(T, H):
+    dev = _dev()
+    for n, (xt, wt) in enumerate(PAIRS):
+        g = gen("back", T, H, n)
+        x, w = rows_like(g, T, H, xt, dev), (1 + 0.3 * torch.randn(H, generator=g)).to(wt).to(dev)
+        up = torch.randn(T, H, generator=g).to(xt).to(dev)
+        more = torch.randn(T, H, generator=g).to(xt).to(dev) if (T + n) % 2 else None
+        dx, dw = moe.rms_norm_backward(up, x, w, grad_residual=more, eps=1e-5)
+        c = [t.cpu() if t is not None else None for t in (up, x, w, more)]
+        want, want_w = ref.norm_backward(c[0], c[1], c[2], 1e-5, c[3])
+        r = 1 / torch.sqrt(c[1].double().square().mean(1, keepdim=True) + 1e-5)
+        gw, norm = c[0].double() * c[2].double(), c[1].double() * r
+        size = r * (gw.abs() + norm.abs() * (gw * norm).abs().mean(1, keepdim=True)) + (
+            c[3].double().abs() if more is not None else 0)
+        near(dx, want, size)
+        # at most (rows a group) + (groups a wave) + 16 additions: 2100 / 4 of 64 lanes are the most here, 528
+        near(dw, want_w, (c[0].double() * norm).abs().sum(0) * 5)
+        guard = Guarded()
+        outs = guard.like("dx", dx), guard.like("dw", dw)
+        ws = guard.bytes("workspace", moe.rms_norm_backward_workspace_size(T, H), dev)
+        moe.rms_norm_backward(odd(up), odd(x), odd(w), grad_residual=None if more is None else odd(more), eps=1e-5,
+                              out=outs, workspace=ws)
+        torch.cuda.synchronize()
+        guard.check()
+        assert same(dx, outs[0]) and same(dw, outs[1])
+
+
+@pytest.mark.parametrize("size,eps", [(1e30, 1e-6), (1e37, 1e-6), (1e-25, 1e-30), (1e-36, 1.2e-38)])
+@pytest.mark.parametrize("H", [64, 3000])
+def test_norm_backward_at_the_ends_of_the_range(H, size, eps):
+    dev = _dev()
+    g = gen("ends", H, size)
+    for dtype in (BF16, FP32):
+        x = (torch.randn(3, H, generator=g).double() * size).to(dtype)
+        up, w = torch.randn(3, H, generator=g).to(dtype), (1 + 0.3 * torch.randn(H, generator=g)).to(dtype)
+        dx, dw = moe.rms_norm_backward(up.to(dev), x.to(dev), w.to(dev), eps=eps)
+        want, want_w = ref.norm_backward(up, x, w, eps)
+        r = 1 / torch.sqrt(x.double().square().mean(1, keepdim=True) + eps)
+        gw, n = up.double() * w.double(), x.double() * r
+        near(dx, want, r * (gw.abs() + n.abs() * (gw * n).abs().mean(1, keepdim=True)))
+        near(dw, want_w, (up.double() * n).abs().sum(0))
+
+
+# ---------------------------------------------------------------------- router
+
+ROUTER = [(1, 1, 1), (1, 4, 4), (5, 7, 3), (16, 64, 6), (33, 65, 8), (40, 128, 16), (17, 130, 2), (64, 256, 8),
+          (9, 257, 16), (21, 512, 8), (6, 515, 5), (10, 1023, 16), (3, 1024, 1)]
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("dtype", [FP32, BF16, F16])
+@pytest.mark.parametrize("T,E,k", ROUTER)
+def test_router(T, E, k, dtype, renormalize):
+    """16-bit logits have many ties; some experts are closed, and a row of nothing else."""
+    dev = _dev()
+    g = gen("router", T, E, k, str(dtype))
+    logits = (2 * torch.randn(T, E, generator=g)).to(dtype)
+    logits[torch.rand(T, E, generator=g) < 0.2] = float("-inf")
+    logits[T // 2, :] = float("-inf")
+    logits[0] = 0.25
+    logits[0, ::2] *= -0.0 if T == 1 else 1.0
+    up = torch.randn(T, k, generator=g)
+    weight, ids = moe.moe_router_top_k(logits.to(dev), k, renormalize=renormalize)
+    want, want_ids = ref.router(logits, k, renormalize)
+    assert torch.equal(ids.cpu(), want_ids)
+    near(weight, want, want)
+    d = moe.moe_router_top_k_backward(up.to(dev), logits.to(dev), weight, ids, renormalize=renormalize)
+    want_d = ref.router_backward(up, logits, want_ids, renormalize)
+    p = torch.softmax(logits.double(), 1).nan_to_num(0.0)
+    if renormalize:
+        p = torch.zeros(T, E, dtype=torch.float64).scatter_add_(1, want_ids.clamp(min=0).long(), want)
+    near(d, want_d, p * (up.abs().amax(1, keepdim=True) * 2))
+    guard = Guarded()
+    outs = guard.like("weight", weight), guard.like("ids", ids)
+    grad = guard.like("grad", d)
+    moe.moe_router_top_k(odd(logits.to(dev)), k, renormalize=renormalize, out=outs)
+    moe.moe_router_top_k_backward(odd(up.to(dev)), odd(logits.to(dev)), *map(odd, outs), renormalize=renormalize, out=grad)
+    torch.cuda.synchronize()
+    guard.check()
+    assert same(weight, outs[0]) and same(ids, outs[1]) and same(d, grad)
+
+
+def test_router_chooses_as_the_few_token_layer():
+    """Its ids and weights given to moe_few_tokens make what the logits make."""
+    dev = _dev()
+    g = gen("few")
+    x = torch.randn(7, 64, generator=g).to(BF16).to(dev)
+    up, down = torch.randn(20, 64, 64, generator=g).to(BF16).to(dev), torch.randn(20, 64, 32, generator=g).to(BF16).to(dev)
+    logits = torch.randn(7, 20, generator=g).to(dev)
+    logits[3, 5:] = float("-inf")
+    for renormalize in (True, False):
+        weight, ids = moe.moe_router_top_k(logits, 6, renormalize=renormalize)
+        a = moe.moe_few_tokens(x, up, down, router_logits=logits, top_k=6, renormalize=renormalize)
+        b = moe.moe_few_tokens(x, up, down, expert_ids=ids, expert_weight=weight)
+        near(a, b.double(), b.double().abs() * 2 ** 10)  # two roundings to bf16 of weights a few ulps apart
+
+
+@pytest.mark.parametrize("E", [5, 100, 600])
+def test_router_of_logits_that_are_not_finite(E):
+    dev = _dev()
+    logits = torch.zeros(3, E)
+    logits[0, 4], logits[1, 2], logits[2, 1] = float("nan"), float("inf"), 3.0
+    weight, ids = moe.moe_router_top_k(logits.to(dev), 3)
+    assert ids.tolist() == [[4, 0, 1], [2, 0, 1], [1, 0, 2]]
+    assert torch.isnan(weight[0]).all() and torch.isnan(weight[1]).all() and torch.isfinite(weight[2]).all()
+    for renormalize in (True, False):
+        weight, ids = moe.moe_router_top_k(logits.to(dev), 3, renormalize=renormalize)
+        d = moe.moe_router_top_k_backward(torch.ones_like(weight), logits.to(dev), weight, ids, renormalize=renormalize)
+        assert torch.isnan(d[0, 4]) and torch.isnan(d[1, 2]) and torch.isfinite(d[2]).all()
+
+
+def test_router_of_no_tokens():
+    dev = _dev()
+    weight, ids = moe.moe_router_top_k(torch.zeros(0, 8, device=dev), 2)
+    assert weight.shape == ids.shape == (0, 2)
+    assert moe.moe_router_top_k_backward(weight, torch.zeros(0, 8, device=dev), weight, ids).shape == (0, 8)
+
+
+# ------------------------------------------------------- rows by expert and back
+
+# T, k, E, H, tokens, scales, away: few choices (one kernel) and many, blocks and waves that end
+# anywhere, one expert and the most, rows of one byte to several units
+PERMUTE = [(1, 1, 1, 1, "int8", None, 0.0), (1, 8, 64, 7168, "int8", "row", 0.0), (3, 16, 16, 33, "fp8", "mx", 0.5),
+           (37, 6, 60, 1409, "f16", "rows3", 0.25), (512, 8, 100, 256, "bf16", "row", 0.1),
+           (256, 16, 4096, 40, "fp4", "mx", 0.0), (513, 8, 7, 17, "e5m2", "rows5", 0.3),
+           (5000, 1, 3, 16, "int8", "row", 0.0), (1237, 6, 60, 1409, "f16", None, 0.25), (3000, 8, 256, 700, "fp8", "mx", 0.0),
+           (4100, 16, 4096, 6, "f32", "rows300", 0.2), (2000, 5, 1300, 2050, "int8", "row", 0.9),
+           (9000, 2, 2500, 3, "int8", None, 0.0), (700, 7, 1, 1032, "bf16", "rows260", 0.0)]
+TOKENS = {"int8": torch.int8, "fp8": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2, "bf16": BF16, "f16": F16, "f32": FP32,
+          "fp4": torch.float4_e2m1fn_x2}
+
+
+def make_tokens(g, T, H, kind):
+    dtype = TOKENS[kind]
+    width = H // 2 if kind == "fp4" else H
+    return torch.randint(0, 256, (T, width * dtype.itemsize), generator=g, dtype=torch.uint8).view(dtype)
+
+
+def make_scales(g, T, H, kind):
+    if kind is None:
+        return None
+    if kind == "mx":
+        return torch.randint(0, 255, (T, math.ceil(H / 64), 2), generator=g, dtype=torch.uint8).view(torch.float8_e8m0fnu)
+    return torch.rand((T,) if kind == "row" else (T, int(kind[4:])), generator=g)
+
+
+def make_ids(g, T, k, E, away):
+    ids = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
+    gone = torch.rand(T, k, generator=g) < away
+    other = torch.tensor([-1, E, -(1 << 31), (1 << 31) - 1], dtype=torch.int64)[torch.randint(0, 4, (T, k), generator=g)]
+    return torch.where(gone, other.to(torch.int32), ids)
+
+
+@pytest.mark.parametrize("T,k,E,H,kind,scales,away", PERMUTE)
+def test_permute(T, k, E, H, kind, scales, away):
+    dev = _dev()
+    g = gen("permute", T, k, E, H)
+    tokens, s, ids = make_tokens(g, T, H, kind), make_scales(g, T, H, scales), make_ids(g, T, k, E, away)
+    w = torch.rand(T, k, generator=g)
+    up = lambda t: None if t is None else t.to(dev)  # noqa: E731
+    out = moe.moe_token_permute(up(tokens), up(ids), E, per_token_scales=up(s), expert_weight=up(w))
+    index, num = ref.plan(ids, E)
+    want = (ref.place(tokens.view(torch.uint8), index).view(tokens.dtype),
+            None if s is None else ref.place(s if s.dtype == FP32 else s.view(torch.uint8), index).view(s.dtype), index,
+            num)
+    for a, b in zip(out[:4], want):
+        assert (a is None) == (b is None) and (a is None or (a.shape == b.shape and a.dtype == b.dtype and same(a, b)))
+    weights = torch.zeros(T * k)
+    here = index.flatten() >= 0
+    weights[index.flatten()[here].long()] = w.flatten()[here]
+    assert torch.equal(out[4].cpu(), weights[:, None])
+    guard = Guarded()
+    outs = tuple(None if t is None else guard.like(str(i), t) for i, t in enumerate(out))
+    ws = guard.bytes("workspace", moe.token_permute_workspace_size(T, k, E), dev)
+    # fp4 tensors cannot be copied element by element: their bytes are
+    there = odd(up(tokens.view(torch.uint8))).view(tokens.dtype) if tokens.dtype.itemsize == 1 else odd(up(tokens))
+    there_s = None if s is None else odd(up(s.view(torch.uint8))).view(s.dtype) if s.dtype.itemsize == 1 else odd(up(s))
+    moe.moe_token_permute(there, odd(up(ids)), E, per_token_scales=there_s, expert_weight=odd(up(w)), out=outs, workspace=ws,
+                          expert_token_num_type=0)
+    torch.cuda.synchronize()
+    guard.check()
+    assert all(same(a, b) for i, (a, b) in enumerate(zip(out, outs)) if i != 3)
+    assert torch.equal(outs[3].cpu(), num.cumsum(0).to(torch.int32))
+
+
+def test_permute_takes_tagged_bytes_and_no_tokens():
+    dev = _dev()
+    ids = torch.tensor([[1, 0], [1, 7]], dtype=torch.int32, device=dev)
+    t = torch.arange(2 * 32, dtype=torch.uint8, device=dev).view(2, 32)
+    rows, scales, index, num, weight = moe.moe_token_permute(t, ids, 3, tokens_dtype="float4_e1m2fn_x2")
+    assert scales is None and weight is None and index.tolist() == [[1, 0], [2, -4]] and num.tolist() == [1, 2, 0]
+    assert rows.tolist() == [t[0].tolist(), t[0].tolist(), t[1].tolist(), [0] * 32]
+    for kind in (1, 0):
+        out = moe.moe_token_permute(t[:0].view(torch.int8), ids[:0], 5, per_token_scales=torch.rand(0, device=dev),
+                                    expert_weight=torch.rand(0, 2, device=dev), expert_token_num_type=kind)
+        assert out[0].shape == (0, 32) and out[3].tolist() == [0] * 5 and out[4].shape == (0, 1)
+
+
+def test_permute_of_more_tokens_than_a_grid_has_rows():
+    """Over 65535 tokens, of rows of several units and of short ones."""
+    dev = _dev()
+    g = gen("many")
+    T, E = 70001, 9
+    ids = torch.randint(-1, E, (T, 2), generator=g, dtype=torch.int32)
+    order = torch.sort(torch.where(ids < 0, E, ids).flatten(), stable=True)[1]
+    here = torch.where(ids < 0, E, ids).flatten()[order] < E
+    for H in (1041, 12):
+        t = torch.randint(-128, 128, (T, H), generator=g, dtype=torch.int8)
+        rows, _, index, num, _ = moe.moe_token_permute(t.to(dev), ids.to(dev), E)
+        want = torch.where(here[:, None], t[order // 2], 0)
+        assert torch.equal(rows.cpu(), want) and num.tolist() == torch.bincount(ids[ids >= 0], minlength=E).tolist()
+        back = moe.moe_token_unpermute(rows.float(), index).cpu()
+        assert torch.equal(back, t.float() * (ids >= 0).sum(1, keepdim=True))
+        d, _ = moe.moe_token_unpermute_backward(back.to(dev), rows.float(), index)
+        assert torch.equal(d.cpu(), torch.where(here[:, None], back[order // 2], 0))
+        weight = torch.rand(T, 2, generator=g).to(dev)
+        d, dw = moe.moe_token_unpermute_backward(back.to(dev), rows.float(), index, expert_weight=weight)
+        assert torch.equal(d.cpu(), torch.where(here[:, None], back[order // 2] * weight.cpu().flatten()[order, None], 0))
+        assert ((dw.cpu() == 0) | (ids >= 0)).all()
+
+
+# T, k, E, H, away
+COMBINE = [(1, 1, 1, 1, 0.0), (1, 8, 64, 7168, 0.0), (16, 8, 64, 7168, 0.1), (5, 16, 16, 33, 0.5), (37, 6, 60, 1409, 0.25),
+           (300, 3, 9, 512, 0.2), (129, 2, 4, 513, 0.0), (70, 9, 11, 255, 0.3), (41, 4, 5, 2049, 0.1), (33, 5, 8, 100, 0.9),
+           (20, 7, 9, 4100, 0.0), (50, 12, 40, 1030, 0.1), (3, 16, 64, 16000, 0.0), (600, 8, 64, 264, 0.0)]
+
+
+@pytest.mark.parametrize("weighted", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F16, FP32])
+@pytest.mark.parametrize("T,k,E,H,away", COMBINE)
+def test_unpermute_and_its_gradient(T, k, E, H, away, dtype, weighted):
+    dev = _dev()
+    g = gen("combine", T, k, E, H, str(dtype))
+    index, _ = ref.plan(make_ids(g, T, k, E, away), E)
+    rows = rows_like(g, T * k, H, dtype, "cpu")
+    gone = (-1 - index[index < 0]).long()
+    rows[gone] = float("nan")  # nothing reads them
+    w = torch.randn(T, k, generator=g) if weighted else None
+    if weighted:
+        w[index < 0] = float("inf")
+    up = torch.randn(T, H, generator=g).to(dtype)
+    there = lambda t: None if t is None else t.to(dev)  # noqa: E731
+    y = moe.moe_token_unpermute(there(rows), there(index), expert_weight=there(w))
+    want, size = ref.combine(rows, index, w)
+    near(y, want, size)
+    d, dw = moe.moe_token_unpermute_backward(there(up), there(rows), there(index), expert_weight=there(w))
+    want_d, want_dw, size_w = ref.combine_backward(up, rows, index, w)
+    near(d, want_d, want_d.abs())
+    assert (d[gone.to(dev)] == 0).all()
+    assert (dw is None) == (w is None)
+    if weighted:
+        near(dw, want_dw, size_w)
+    guard = Guarded()
+    outs = guard.like("y", y), guard.like("d", d), None if dw is None else guard.like("dw", dw)
+    moe.moe_token_unpermute(odd(there(rows)), odd(there(index)), expert_weight=None if w is None else odd(there(w)),
+                            out=outs[0])
+    moe.moe_token_unpermute_backward(odd(there(up)), odd(there(rows)), odd(there(index)),
+                                     expert_weight=None if w is None else odd(there(w)), out=outs[1:])
+    torch.cuda.synchronize()
+    guard.check()
+    assert same(y, outs[0]) and same(d, outs[1]) and same(dw, outs[2])
+
+
+@pytest.mark.parametrize("H", [24, 1300])
+def test_unpermute_passes_over_other_indices(H):
+    """Indices past the rows, and none at all; rows that no index names stay as they were."""
+    dev = _dev()
+    g = gen("other", H)
+    rows = torch.randn(4, H, generator=g)
+    index = torch.tensor([[2, 4, -1], [1 << 30, 3, -(1 << 31)], [-6, -5, (1 << 31) - 1]], dtype=torch.int32)
+    w = torch.rand(3, 3, generator=g)
+    want, size = ref.combine(rows, index, w)
+    near(moe.moe_token_unpermute(rows.to(dev), index.to(dev), expert_weight=w.to(dev)), want, size)
+    up = torch.randn(3, H, generator=g)
+    for weight in (w.to(dev), None):
+        d = torch.full((4, H), 7.0, device=dev)
+        dw = None if weight is None else torch.full((3, 3), 7.0, device=dev)
+        moe.moe_token_unpermute_backward(up.to(dev), rows.to(dev), index.to(dev), expert_weight=weight, out=(d, dw))
+        want = torch.full((4, H), 7.0)
+        want[0] = 0  # the place of a choice that was not here
+        want[2], want[3] = (up[0], up[1]) if weight is None else (up[0] * w[0, 0], up[1] * w[1, 1])
+        assert torch.equal(d.cpu(), want)
+        if dw is not None:
+            named = (index >= 0) & (index < 4)
+            assert (dw.cpu()[~named] == 0).all() and (dw.cpu()[named] != 7).all()
+    none = torch.empty(0, H, device=dev)
+    away = torch.full((2, 3), -1, dtype=torch.int32, device=dev)
+    assert (moe.moe_token_unpermute(none, away) == 0).all()
+    assert moe.moe_token_unpermute(none, away[:0]).shape == (0, H)
+    d, dw = moe.moe_token_unpermute_backward(torch.ones(2, H, device=dev), none, away, expert_weight=torch.ones(2, 3, device=dev))
+    assert d.shape == (0, H) and (dw == 0).all()
+    assert moe.moe_token_unpermute_backward(torch.ones(2, H, device=dev), none, away)[0].shape == (0, H)
+
+
+@pytest.mark.parametrize("T,k,E,H,away", COMBINE[:8])
+def test_permute_backward(T, k, E, H, away):
+    dev = _dev()
+    g = gen("pback", T, k, E, H)
+    index, _ = ref.plan(make_ids(g, T, k, E, away), E)
+    rows, w = torch.randn(T * k, H, generator=g), torch.randn(T * k, 1, generator=g)
+    grad, grad_w = moe.moe_token_permute_backward(rows.to(dev), index.to(dev), grad_topk_weight=w.to(dev))
+    want, size = ref.combine(rows, index)
+    near(grad, want, size)
+    flat = index.flatten().long()
+    assert torch.equal(grad_w.cpu().flatten(), torch.where(flat >= 0, w.flatten()[flat.clamp(min=0)], 0.0))
+    grad2, none = moe.moe_token_permute_backward(rows.to(dev), index.to(dev))
+    assert none is None and same(grad, grad2)
+    assert same(moe.moe_token_permute_backward(rows.to(dev), index.to(dev), grad_topk_weight=w.to(dev).view(-1))[1], grad_w)
+
+
+def test_rows_past_32_bit_offsets():
+    """Rows of 64 KiB, 5 GB of them: each is found again where it was put."""
+    dev = _dev()
+    T, k, H = 5000, 16, 16384
+    g = gen("large")
+    ids = torch.randint(0, 40, (T, k), generator=g, dtype=torch.int32).to(dev)
+    tokens = torch.randn(T, 1, generator=g).to(dev) + torch.arange(H, device=dev) / 64.0
+    rows, _, index, num, _ = moe.moe_token_permute(tokens, ids, 40)
+    assert rows.numel() * 4 > 1 << 32 and int(num.sum()) == T * k
+    for t in (0, 1, 2499, T - 1):
+        for j in (0, 7, 15):
+            assert torch.equal(rows[index[t, j]], tokens[t])
+    for part in range(0, T * k, 20000):  # the row of every choice
+        flat = index.flatten()[part:part + 20000].long()
+        assert torch.equal(rows[flat, 17], tokens[torch.arange(part, part + flat.numel(), device=dev) // k, 17])
+    w = torch.full((T, k), 0.0625, device=dev)
+    y = moe.moe_token_unpermute(rows, index, expert_weight=w)
+    assert torch.allclose(y, tokens, rtol=1e-5, atol=1e-5)
+    d, dw = moe.moe_token_unpermute_backward(tokens, rows, index, expert_weight=w)
+    assert torch.equal(d, rows * 0.0625)
+    want = (tokens.double().square()).sum(1, keepdim=True).expand(T, k)
+    assert ((dw.double() - want).abs() <= want * F32).all()
+
+
+# ------------------------------------------------------------- how they are called
+
+def calls(dev, T=40):
+    """Every operator once, as functions without arguments that return their outputs."""
+    g = gen("calls", T)
+    x, r, up = (torch.randn(T, 200, generator=g).to(BF16).to(dev) for _ in range(3))
+    w = torch.randn(200, generator=g).to(dev)
+    logits = torch.randn(T, 12, generator=g).to(dev)
+    weight, ids = moe.moe_router_top_k(logits, 4)
+    rows, _, index, _, _ = moe.moe_token_permute(x, ids, 12)
+    inputs = dict(x=x, r=r, up=up, w=w, logits=logits, weight=weight, rows=rows)
+    out = {"norm": lambda: moe.rms_norm(x, w, residual=r, quantize="mxfp8"),
+           "norm_i8": lambda: moe.rms_norm(x, w, quantize="int8"),
+           "norm_backward": lambda: moe.rms_norm_backward(up, x, w, grad_residual=r),
+           "router": lambda: moe.moe_router_top_k(logits, 4),
+           "router_backward": lambda: (moe.moe_router_top_k_backward(weight, logits, weight, ids, renormalize=False),),
+           "permute": lambda: moe.moe_token_permute(x, ids, 12, expert_weight=weight),
+           "unpermute": lambda: (moe.moe_token_unpermute(rows, index, expert_weight=weight),),
+           "unpermute_backward": lambda: moe.moe_token_unpermute_backward(up, rows, index, expert_weight=weight),
+           "permute_backward": lambda: moe.moe_token_permute_backward(rows, index)}
+    return out, inputs
+
+
+@pytest.mark.parametrize("T", [40, 2000])
+def test_the_same_bits_each_time_and_from_both_bindings(T, monkeypatch):
+    from moe_token_re_amd import _lib
+
+    dev = _dev()
+    todo, _ = calls(dev, T)
+    first = {n: f() for n, f in todo.items()}
+    for _ in range(2):
+        for n, f in todo.items():
+            assert all(same(a, b) for a, b in zip(f(), first[n])), n
+    monkeypatch.setattr(_lib, "_plain_calls", _lib._NoBinding)
+    for n, f in todo.items():
+        again = f()
+        assert all(same(a, b) and (a is None or (a.shape == b.shape and a.dtype == b.dtype))
+                   for a, b in zip(again, first[n])), n
+
+
+@pytest.mark.parametrize("T", [40, 2000])
+@pytest.mark.parametrize("name", ["norm", "norm_i8", "norm_backward", "router", "router_backward", "permute", "unpermute",
+                                  "unpermute_backward", "permute_backward"])
+def test_captured_and_replayed(name, T):
+    """Replays after eager work and new inputs give what an eager call gives."""
+    dev = _dev()
+    todo, inputs = calls(dev, T)
+    f = todo[name]
+    side = torch.cuda.Stream(dev)
+    with torch.cuda.stream(side):
+        f()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = f()
+    for replay in range(3):
+        for key in ("x", "r", "up", "w", "logits", "rows"):
+            inputs[key].copy_(torch.randn(inputs[key].shape, generator=gen(name, replay, key)).to(inputs[key].dtype))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(same(a, b) for a, b in zip(out, f())), replay
+
+
+def test_two_streams_at_once():
+    dev = _dev()
+    todo, _ = calls(dev, 2000)
+    want = {n: f() for n, f in todo.items()}
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(dev) for _ in range(2)]
+    got = []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append({n: f() for n, f in todo.items()})
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(same(a, b) for n in want for a, b in zip(g[n], want[n]))
+
+
+def test_a_stream_in_a_thread_with_another_current_stream():
+    """Work is ordered on the current stream: a producer on it needs no wait."""
+    dev = _dev()
+    s = torch.cuda.Stream(dev)
+    x = torch.zeros(512, 4096, dtype=BF16, device=dev)
+    w = torch.ones(4096, dtype=BF16, device=dev)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        for i in range(20):
+            x.fill_(float(i + 1))
+            y, scales, _ = moe.rms_norm(x, w, quantize="int8")
+    s.synchronize()
+    assert (y == 127).all()
