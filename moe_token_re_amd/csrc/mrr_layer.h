@@ -47,14 +47,14 @@ inline int64_t norm_backward_groups(int64_t rows, int64_t H) {
 }
 
 // Few choices are sorted by every workgroup of one kernel by itself; more in blocks,
-// whose counts by expert [blocks, E + 1] lie in the workspace: so many blocks that the
-// counts, which every block reads, stay few, and none smaller than a workgroup.
+// whose counts by expert [blocks, E + 1] lie in the workspace. Every block reads all
+// counts, so they stay few.
 constexpr int64_t kPermuteFewChoices = 4096;
-constexpr int64_t kPermuteBlockChoices = 1024;
-constexpr int64_t kPermuteMostCounts = 32768;
+constexpr int64_t kPermuteBlockChoices = 4096;
+constexpr int64_t kPermuteMostBlocks = 64, kPermuteMostCounts = 32768;
 inline int64_t permute_block(int64_t choices, int64_t E) {
   int64_t blocks = kPermuteMostCounts / (E + 1);
-  blocks = blocks < 1 ? 1 : blocks > 256 ? 256 : blocks;
+  blocks = blocks < 1 ? 1 : blocks > kPermuteMostBlocks ? kPermuteMostBlocks : blocks;
   const int64_t each = (choices + blocks - 1) / blocks;
   return each <= kPermuteBlockChoices ? kPermuteBlockChoices
                                       : static_cast<int64_t>(round_up(static_cast<size_t>(each), kPermuteBlockChoices));

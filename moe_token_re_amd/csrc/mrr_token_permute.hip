@@ -122,15 +122,35 @@ __device__ __forceinline__ void write_num(const uint32_t* count, const SortArgs&
 // ------------------------------------------------------------- few choices
 
 constexpr int kFewThreads = 256;
-// A workgroup moves so much of a token's row.
+constexpr int kFewWaves = kFewThreads / 64;
+// A workgroup moves so many units of a token's row.
 constexpr uint32_t kFewUnits = kFewThreads;
+// Up to so many choices every wave compares all of them with its own, without a barrier.
+constexpr uint32_t kFewAlone = 256;
+// Up to so many of them, and so many experts, are counted without LDS.
+constexpr uint32_t kFewest = 64, kFewestExperts = 1024;
 
+// kK: at least top_k.
+template <int kK>
 __global__ __launch_bounds__(kFewThreads) void permute_few_kernel(SortArgs a, Rows tokens, Rows scales) {
-  __shared__ uint32_t sh[kPermuteMaxExperts + 1];
-  __shared__ uint32_t sh_wave[kFewThreads / 64][kLayerMaxTopK], sh_own[kLayerMaxTopK];
-  const uint32_t tid = threadIdx.x, token = blockIdx.y;
+  __shared__ uint32_t sh[kPermuteMaxExperts];
+  __shared__ uint32_t sh_before[kFewWaves][kK];  // and, of the last workgroup, sums of its waves
+  const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64, token = blockIdx.y;
   if (token == a.T) {  // the last workgroup counts
     if (blockIdx.x != 0) return;
+    if (a.n <= kFewest && a.E <= kFewestExperts) {
+      // every thread its own experts' choices, or those up to them, one choice at a time
+      const uint32_t mine = lane < a.n ? static_cast<uint32_t>(a.ids[lane]) : a.E;
+      for (uint32_t e = tid; e < a.E; e += kFewThreads) {
+        uint32_t c = 0;
+        for (uint32_t i = 0; i < a.n; ++i) {
+          const uint32_t id = __builtin_amdgcn_readlane(mine, i);
+          c += a.cumsum ? id <= e : id == e;
+        }
+        a.num[e] = static_cast<int32_t>(c);
+      }
+      return;
+    }
     for (uint32_t e = tid; e < a.E; e += kFewThreads) sh[e] = 0;
     __syncthreads();
     for (uint32_t i = tid; i < a.n; i += kFewThreads) {
@@ -138,52 +158,67 @@ __global__ __launch_bounds__(kFewThreads) void permute_few_kernel(SortArgs a, Ro
       if (e < a.E) atomicAdd(&sh[e], 1u);
     }
     __syncthreads();
-    write_num<kFewThreads>(sh, a, sh_wave[0]);
+    write_num<kFewThreads>(sh, a, &sh_before[0][0]);
     return;
   }
-  const uint32_t unit = blockIdx.x * kFewUnits + tid;
+  const uint32_t unit = blockIdx.x * kFewUnits + tid, first = token * a.k;
+  const bool moves = unit < tokens.units, moves_scales = blockIdx.x == 0 && tid < scales.units;
+  const bool writes = blockIdx.x == 0 && tid < a.k;  // the index and the weight of choice tid
   Unit u, s;
-  if (unit < tokens.units) u.load(tokens, token, unit);
-  const bool moves_scales = blockIdx.x == 0 && tid < scales.units;  // the first of them; more below
+  if (moves) u.load(tokens, token, unit);
   if (moves_scales) s.load(scales, token, tid);
-  // (expert, place) as one number
-  const uint32_t first = token * a.k;
-  uint32_t own[kLayerMaxTopK], before[kLayerMaxTopK] = {};
+  const float weight = writes && a.weight != nullptr ? a.weight[first + tid] : 0.0f;
+  // (expert, place) as one number; a token's own are read by the lanes with all the rest
+  const auto number = [&](int32_t id, uint32_t i) { return expert_of(id, a.E) * a.n + i; };
+  const bool alone = a.n <= kFewAlone;
+  uint32_t i = (alone ? 0 : 64 * wave) + lane;
+  const int32_t own_id = lane < a.k ? a.ids[first + lane] : 0;
+  int32_t id = i < a.n ? a.ids[i] : 0;
+  const uint32_t own_number = lane < a.k ? number(own_id, first + lane) : 0;
+  uint32_t own[kK], row[kK];
 #pragma unroll
-  for (uint32_t j = 0; j < kLayerMaxTopK; ++j)
-    own[j] = j < a.k ? expert_of(a.ids[first + j], a.E) * a.n + first + j : 0;
-  for (uint32_t i0 = tid / 64 * 64; i0 < a.n; i0 += kFewThreads) {
-    const uint32_t i = i0 + tid % 64;
-    const uint32_t c = i < a.n ? expert_of(a.ids[i], a.E) * a.n + i : 0xffffffffu;
-#pragma unroll
-    for (uint32_t j = 0; j < kLayerMaxTopK; ++j)
-      if (j < a.k) before[j] += static_cast<uint32_t>(__popcll(__ballot(c < own[j])));
+  for (uint32_t j = 0; j < kK; ++j) {
+    own[j] = __builtin_amdgcn_readlane(own_number, j);
+    row[j] = 0;
   }
+  while (i - lane < a.n) {
+    const uint32_t c = i < a.n ? number(id, i) : 0xffffffffu;
+    i += alone ? 64 : kFewThreads;
+    id = i < a.n ? a.ids[i] : 0;
 #pragma unroll
-  for (uint32_t j = 0; j < kLayerMaxTopK; ++j) {
-    if (tid % 64 == 0) sh_wave[tid / 64][j] = before[j];
-    if (tid == 0) sh_own[j] = own[j];
+    for (uint32_t j = 0; j < kK; ++j) row[j] += static_cast<uint32_t>(__popcll(__ballot(c < own[j])));
   }
-  __syncthreads();
+  if (!alone) {
+#pragma unroll
+    for (uint32_t j = 0; j < kK; ++j)
+      if (lane == 0) sh_before[wave][j] = row[j];
+    __syncthreads();
+#pragma unroll
+    for (uint32_t j = 0; j < kK; ++j) {
+      row[j] = 0;
+#pragma unroll
+      for (int w = 0; w < kFewWaves; ++w) row[j] += sh_before[w][j];
+    }
+  }
   const uint32_t away = a.E * a.n;
-  for (uint32_t j = 0; j < a.k; ++j) {
-    uint32_t row = 0;
 #pragma unroll
-    for (int w = 0; w < kFewThreads / 64; ++w) row += sh_wave[w][j];
-    const bool zero = sh_own[j] >= away;
-    if (unit < tokens.units) u.store<false>(tokens, row, zero);
-    if (moves_scales) s.store<false>(scales, row, zero);
-    if (blockIdx.x == 0) {
-      for (uint32_t more = tid + kFewThreads; more < scales.units; more += kFewThreads) {
-        Unit m;
-        m.load(scales, token, more);
-        m.store<false>(scales, row, zero);
-      }
-      if (tid == j) {
-        a.idx[first + j] = static_cast<int32_t>(zero ? ~row : row);
-        if (a.weight != nullptr) a.out_weight[row] = zero ? 0.0f : a.weight[first + j];
+  for (uint32_t j = 0; j < kK; ++j) {
+    if (j < a.k) {
+      const bool zero = own[j] >= away;
+      if (moves) u.store<false>(tokens, row[j], zero);
+      if (moves_scales) s.store<false>(scales, row[j], zero);
+      if (writes && tid == j) {
+        a.idx[first + j] = static_cast<int32_t>(zero ? ~row[j] : row[j]);
+        if (a.weight != nullptr) a.out_weight[row[j]] = zero ? 0.0f : weight;
       }
     }
+  }
+  if (blockIdx.x != 0) return;
+  for (uint32_t more = tid + kFewThreads; more < scales.units; more += kFewThreads) {
+    s.load(scales, token, more);
+#pragma unroll
+    for (uint32_t j = 0; j < kK; ++j)
+      if (j < a.k) s.store<false>(scales, row[j], own[j] >= away);
   }
 }
 
@@ -208,36 +243,57 @@ __global__ __launch_bounds__(kCountThreads) void permute_count_kernel(SortArgs a
 template <int kWaves>
 __global__ __launch_bounds__(64 * kWaves) void permute_place_kernel(SortArgs a) {
   constexpr int kThreads = 64 * kWaves;
-  extern __shared__ uint32_t at[];  // [kWaves, E + 1]
+  extern __shared__ uint32_t at[];  // [kWaves + 2, E + 1]
   __shared__ uint32_t sh[kWaves];
   const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64, width = a.E + 1;
-  for (uint32_t i = tid; i < width * kWaves; i += kThreads) at[i] = 0;
+  uint32_t* total = at + kWaves * width;
+  uint32_t* start = total + width;
+  for (uint32_t i = tid; i < width * (kWaves + 2); i += kThreads) at[i] = 0;
   __syncthreads();
   const uint32_t run = a.block / kWaves;  // a multiple of 64
   const uint32_t first = blockIdx.x * a.block + wave * run, end = min(a.n, first + run);
   uint32_t* mine = at + wave * width;
   for (uint32_t i = first + lane; i < end; i += 64) atomicAdd(&mine[expert_of(a.ids[i], a.E)], 1u);
   __syncthreads();
-  // where an expert's rows begin, then where this block's of them do, then each wave's
+  // Of an expert: all its choices, and those of the blocks before this one. Threads
+  // share its column among them where there are enough.
+  const uint32_t slices = width >= kThreads ? 1 : kThreads / width;
+  for (uint32_t i = tid; i < width * slices; i += kThreads) {
+    const uint32_t e = i % width, slice = i / width;
+    uint32_t all = 0, before = 0;
+    const int32_t* c = a.counts + e;
+    uint32_t b = slice;
+    for (; b + 7 * slices < a.blocks; b += 8 * slices) {
+      uint32_t v[8];
+#pragma unroll
+      for (uint32_t x = 0; x < 8; ++x) v[x] = static_cast<uint32_t>(c[static_cast<size_t>(b + x * slices) * width]);
+#pragma unroll
+      for (uint32_t x = 0; x < 8; ++x) {
+        all += v[x];
+        before += b + x * slices < blockIdx.x ? v[x] : 0;
+      }
+    }
+    for (; b < a.blocks; b += slices) {
+      const uint32_t v = static_cast<uint32_t>(c[static_cast<size_t>(b) * width]);
+      all += v;
+      before += b < blockIdx.x ? v : 0;
+    }
+    atomicAdd(&total[e], all);
+    atomicAdd(&start[e], before);
+  }
+  __syncthreads();
+  // where its rows begin, where this block's of them do, then each wave's
   const uint32_t per = (width + kThreads - 1) / kThreads, e0 = tid * per;
   uint32_t sum = 0;
-  for (uint32_t i = 0; i < per; ++i) {
-    const uint32_t e = e0 + i;
-    if (e >= width) break;
-    for (uint32_t b = 0; b < a.blocks; ++b) sum += static_cast<uint32_t>(a.counts[static_cast<size_t>(b) * width + e]);
-  }
+  for (uint32_t i = 0; i < per; ++i)
+    if (e0 + i < width) sum += total[e0 + i];
   uint32_t begin = scan_threads<kThreads>(sum, sh) - sum;
   for (uint32_t i = 0; i < per; ++i) {
     const uint32_t e = e0 + i;
     if (e >= width) break;
-    uint32_t all = 0, place = begin;
-    for (uint32_t b = 0; b < a.blocks; ++b) {
-      const uint32_t c = static_cast<uint32_t>(a.counts[static_cast<size_t>(b) * width + e]);
-      if (b < blockIdx.x) place += c;
-      all += c;
-    }
-    begin += all;
-    if (blockIdx.x == 0 && e < a.E) a.num[e] = static_cast<int32_t>(a.cumsum ? begin : all);
+    uint32_t place = begin + start[e];
+    begin += total[e];
+    if (blockIdx.x == 0 && e < a.E) a.num[e] = static_cast<int32_t>(a.cumsum ? begin : total[e]);
     for (int w = 0; w < kWaves; ++w) {
       const uint32_t c = at[w * width + e];
       at[w * width + e] = place;
@@ -246,23 +302,36 @@ __global__ __launch_bounds__(64 * kWaves) void permute_place_kernel(SortArgs a) 
   }
   __syncthreads();
   const int bits = 32 - __builtin_clz(a.E);
-  for (uint32_t i0 = first; i0 < end; i0 += 64) {
-    const uint32_t i = i0 + lane;
-    const bool here = i < end;
-    const uint32_t e = here ? expert_of(a.ids[i], a.E) : 0;
-    uint64_t same = __ballot(here);
-    for (int bit = 0; bit < bits; ++bit) {
-      const bool set = e >> bit & 1;
-      const uint64_t with = __ballot(set);
-      same &= set ? with : ~with;
+  // four times 64 choices are read before the first is written: a load behind a store
+  // would wait for it
+  constexpr int kAhead = 4;
+  for (uint32_t i0 = first; i0 < end; i0 += 64 * kAhead) {
+    uint32_t expert[kAhead];
+    float weight[kAhead];
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const uint32_t i = min(i0 + 64 * x + lane, end - 1);
+      expert[x] = expert_of(a.ids[i], a.E);
+      weight[x] = a.weight != nullptr ? a.weight[i] : 0.0f;
     }
-    if (here) {
-      const uint32_t rank = static_cast<uint32_t>(__popcll(same & ((uint64_t(1) << lane) - 1)));
-      const uint32_t row = mine[e] + rank;
-      // the last of them, after all have read
-      if ((same >> lane) == 1) mine[e] = row + 1;
-      a.idx[i] = static_cast<int32_t>(e < a.E ? row : ~row);
-      if (a.weight != nullptr) a.out_weight[row] = e < a.E ? a.weight[i] : 0.0f;
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const uint32_t i = i0 + 64 * x + lane, e = expert[x];
+      const bool here = i < end;
+      uint64_t same = __ballot(here);
+      for (int bit = 0; bit < bits; ++bit) {
+        const bool set = e >> bit & 1;
+        const uint64_t with = __ballot(set);
+        same &= set ? with : ~with;
+      }
+      if (here) {
+        const uint32_t rank = static_cast<uint32_t>(__popcll(same & ((uint64_t(1) << lane) - 1)));
+        const uint32_t row = mine[e] + rank;
+        // the last of them, after all have read
+        if ((same >> lane) == 1) mine[e] = row + 1;
+        a.idx[i] = static_cast<int32_t>(e < a.E ? row : ~row);
+        if (a.weight != nullptr) a.out_weight[row] = e < a.E ? weight[x] : 0.0f;
+      }
     }
   }
 }
@@ -273,90 +342,133 @@ struct MoveArgs {
   uint32_t R;  // rows of the output
 };
 
-// Rows of more than 64 units: a wave moves 1 KiB of a token's row.
+// Moves one unit of a token's row to its choices' rows. The index is read before the
+// stores, eight choices at a time: a load behind a store would wait for it.
 template <bool kStream>
-__global__ __launch_bounds__(64) void move_rows_kernel(MoveArgs a, Rows r) {
-  const uint32_t token = blockIdx.y, unit = blockIdx.x * 64 + threadIdx.x;
-  if (unit >= r.units) return;
+__device__ __forceinline__ void move_unit(const MoveArgs& a, const Rows& r, size_t token, uint32_t unit) {
   Unit u;
   u.load(r, token, unit);
-  const int32_t* idx = a.idx + static_cast<size_t>(token) * a.k;
-  for (uint32_t j = 0; j < a.k; ++j) {
-    const int32_t i = idx[j];
-    const uint32_t row = static_cast<uint32_t>(i < 0 ? ~i : i);
-    if (row < a.R) u.store<kStream>(r, row, i < 0);
+  const int32_t* idx = a.idx + token * a.k;
+  for (uint32_t j0 = 0; j0 < a.k; j0 += 8) {
+    int32_t i[8];
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) i[j] = idx[min(j0 + j, a.k - 1)];
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) {
+      const uint32_t row = static_cast<uint32_t>(i[j] < 0 ? ~i[j] : i[j]);
+      if (j0 + j < a.k && row < a.R) u.store<kStream>(r, row, i[j] < 0);
+    }
   }
 }
 
-// Shorter ones: as many tokens a wave as fit.
+// Rows of more than 64 units: a wave moves 64 units of a token's row. Scales that are
+// shorter go by the waves of the first workgroups, as many tokens each as fit.
+// The token's index lies on the lanes, read once before the stores, and a row's address
+// in scalar registers.
 template <bool kStream>
-__global__ __launch_bounds__(256) void move_short_rows_kernel(MoveArgs a, Rows r) {
-  const uint32_t lane = threadIdx.x % 64, tokens = 64 / r.units, in_wave = lane / r.units;
+__global__ __launch_bounds__(64) void move_rows_kernel(MoveArgs a, Rows r, Rows scales, uint32_t first) {
+  if (blockIdx.y < first) {
+    const uint32_t tokens = 64 / scales.units, in_wave = threadIdx.x / scales.units;
+    const uint32_t t = (blockIdx.y * gridDim.x + blockIdx.x) * tokens + in_wave;
+    if (in_wave < tokens && t < a.T) move_unit<false>(a, scales, t, threadIdx.x - in_wave * scales.units);
+    return;
+  }
+  const uint32_t token = blockIdx.y - first;
+  const int32_t mine = a.idx[static_cast<size_t>(token) * a.k + min(threadIdx.x, a.k - 1)];
+  // lanes behind the row's end move its last unit as well
+  const uint32_t at = min((blockIdx.x * 64 + threadIdx.x) * 16, r.bytes - 16);
+  const rows_u32x4 v = load16<false>(r.src + static_cast<size_t>(token) * r.bytes + at);
+  for (uint32_t j = 0; j < a.k; ++j) {
+    const int32_t i = __builtin_amdgcn_readlane(mine, j);
+    const uint32_t row = static_cast<uint32_t>(i < 0 ? ~i : i);
+    if (row >= a.R) continue;
+    uint8_t* to = r.dst + static_cast<size_t>(row) * r.bytes;
+    if (i >= 0)
+      store16<kStream>(to + at, v);
+    else
+      store16<kStream>(to + at, rows_u32x4{0, 0, 0, 0});
+  }
+}
+
+// Shorter ones, scales included: as many tokens a wave as fit.
+template <bool kStream>
+__global__ __launch_bounds__(256) void move_short_rows_kernel(MoveArgs a, Rows r, Rows scales) {
+  const uint32_t units = r.units + scales.units;
+  const uint32_t lane = threadIdx.x % 64, tokens = 64 / units, in_wave = lane / units;
   const size_t token = (static_cast<size_t>(blockIdx.x) * 4 + threadIdx.x / 64) * tokens + in_wave;
   if (in_wave >= tokens || token >= a.T) return;
-  Unit u;
-  u.load(r, token, lane - in_wave * r.units);
-  const int32_t* idx = a.idx + token * a.k;
-  for (uint32_t j = 0; j < a.k; ++j) {
-    const int32_t i = idx[j];
-    const uint32_t row = static_cast<uint32_t>(i < 0 ? ~i : i);
-    if (row < a.R) u.store<kStream>(r, row, i < 0);
-  }
+  const uint32_t unit = lane - in_wave * units;
+  if (unit < r.units)
+    move_unit<kStream>(a, r, token, unit);
+  else
+    move_unit<false>(a, scales, token, unit - r.units);
 }
 
-constexpr uint32_t kMostGridY = 65535;
+// Tokens of a launch whose grid's second dimension they are, with the scales' rows of workgroups.
+constexpr uint32_t kMostGridY = 32767;
 // Outputs of so many bytes are written past the caches, which would not hold them.
 constexpr int64_t kStreamBytes = int64_t(64) << 20;
 
 template <bool kStream>
-void move_all(const MoveArgs& all, const Rows& rows, hipStream_t stream) {
-  if (rows.units > 64) {
-    for (uint32_t t = 0; t < all.T; t += kMostGridY) {
-      MoveArgs a = all;
-      Rows r = rows;
-      a.idx += static_cast<size_t>(t) * a.k;
-      r.src += static_cast<size_t>(t) * r.bytes;
-      a.T = all.T - t < kMostGridY ? all.T - t : kMostGridY;
-      move_rows_kernel<kStream><<<dim3((r.units + 63) / 64, a.T), 64, 0, stream>>>(a, r);
-    }
-    return;
+void move_all(const MoveArgs& all, Rows r, Rows scales, hipStream_t stream) {
+  if (scales.units > 64 || (r.units <= 64 && r.units + scales.units > 64)) {  // each by itself
+    move_all<false>(all, scales, Rows{}, stream);
+    scales = Rows{};
   }
+  const bool wide = r.units > 64;
   constexpr uint32_t kMostTokens = 1u << 24;  // of a launch, which holds less than 2^32 threads
+  MoveArgs a = all;
   for (uint32_t t = 0; t < all.T;) {
-    MoveArgs a = all;
-    Rows r = rows;
-    a.idx += static_cast<size_t>(t) * a.k;
-    r.src += static_cast<size_t>(t) * r.bytes;
-    a.T = all.T - t < kMostTokens ? all.T - t : kMostTokens;
-    const uint32_t each = 4 * (64 / r.units);
-    move_short_rows_kernel<kStream><<<(a.T + each - 1) / each, 256, 0, stream>>>(a, r);
+    const uint32_t most = wide ? kMostGridY : kMostTokens;
+    a.T = all.T - t < most ? all.T - t : most;
+    if (wide) {
+      const uint32_t pieces = (r.units + 63) / 64;
+      const uint32_t more = scales.units == 0 ? 0 : (a.T + pieces * (64 / scales.units) - 1) / (pieces * (64 / scales.units));
+      move_rows_kernel<kStream><<<dim3(pieces, a.T + more), 64, 0, stream>>>(a, r, scales, more);
+    } else {
+      const uint32_t each = 4 * (64 / (r.units + scales.units));
+      move_short_rows_kernel<kStream><<<(a.T + each - 1) / each, 256, 0, stream>>>(a, r, scales);
+    }
     t += a.T;
+    a.idx += static_cast<size_t>(a.T) * a.k;
+    r.src += static_cast<size_t>(a.T) * r.bytes;
+    if (scales.units > 0) scales.src += static_cast<size_t>(a.T) * scales.bytes;
   }
 }
 
-void place_all(const SortArgs& a, hipStream_t stream) {
-  const uint32_t width = a.E + 1;
-  constexpr uint32_t kMostLds = 60 * 1024;
-  if (16 * width * 4 <= kMostLds)
-    permute_place_kernel<16><<<a.blocks, 1024, 16 * width * 4, stream>>>(a);
-  else if (8 * width * 4 <= kMostLds)
-    permute_place_kernel<8><<<a.blocks, 512, 8 * width * 4, stream>>>(a);
+// scales: of no units where there are none.
+void move_both(const Rows& r, const Rows& scales, const int32_t* idx, int64_t T, int64_t k, int64_t R, hipStream_t stream) {
+  const MoveArgs a{idx, static_cast<uint32_t>(T), static_cast<uint32_t>(k), static_cast<uint32_t>(R)};
+  if (R * r.bytes >= kStreamBytes)
+    move_all<true>(a, r, scales, stream);
   else
-    permute_place_kernel<2><<<a.blocks, 128, 2 * width * 4, stream>>>(a);
+    move_all<false>(a, r, scales, stream);
 }
-static_assert(2 * (kPermuteMaxExperts + 1) * 4 <= 60 * 1024, "experts' places in LDS");
+
+template <int kWaves>
+constexpr uint32_t place_lds(uint32_t E) {
+  return (kWaves + 2) * (E + 1) * 4;
+}
+constexpr uint32_t kMostLds = 60 * 1024;
+static_assert(place_lds<1>(kPermuteMaxExperts) <= kMostLds, "experts' places in LDS");
 static_assert(kPermuteBlockChoices % (16 * 64) == 0, "a wave's run of choices");
+
+void place_all(const SortArgs& a, hipStream_t stream) {
+  if (place_lds<16>(a.E) <= kMostLds)
+    permute_place_kernel<16><<<a.blocks, 1024, place_lds<16>(a.E), stream>>>(a);
+  else if (place_lds<8>(a.E) <= kMostLds)
+    permute_place_kernel<8><<<a.blocks, 512, place_lds<8>(a.E), stream>>>(a);
+  else if (place_lds<4>(a.E) <= kMostLds)
+    permute_place_kernel<4><<<a.blocks, 256, place_lds<4>(a.E), stream>>>(a);
+  else
+    permute_place_kernel<1><<<a.blocks, 64, place_lds<1>(a.E), stream>>>(a);
+}
 
 }  // namespace
 
 void move_rows(const void* src, void* dst, int64_t row_bytes, const int32_t* idx, int64_t T, int64_t k, int64_t R,
                hipStream_t stream) {
-  const MoveArgs a{idx, static_cast<uint32_t>(T), static_cast<uint32_t>(k), static_cast<uint32_t>(R)};
-  const Rows r = rows_of(src, dst, row_bytes);
-  if (R * row_bytes >= kStreamBytes)
-    move_all<true>(a, r, stream);
-  else
-    move_all<false>(a, r, stream);
+  move_both(rows_of(src, dst, row_bytes), Rows{}, idx, T, k, R, stream);
 }
 
 }  // namespace mrr
@@ -386,14 +498,19 @@ extern "C" mrr_status mrr_token_permute(const mrr_token_permute_args* args, void
   Rows scales{};
   if (scale_row > 0) scales = rows_of(args->per_token_scales, args->permute_per_token_scales, scale_row);
   if (n <= kPermuteFewChoices) {
-    permute_few_kernel<<<dim3((tokens.units + kFewUnits - 1) / kFewUnits, a.T + 1), kFewThreads, 0, stream>>>(a, tokens,
-                                                                                                         scales);
+    const dim3 grid((tokens.units + kFewUnits - 1) / kFewUnits, a.T + 1);
+    if (a.k <= 2)
+      permute_few_kernel<2><<<grid, kFewThreads, 0, stream>>>(a, tokens, scales);
+    else if (a.k <= 4)
+      permute_few_kernel<4><<<grid, kFewThreads, 0, stream>>>(a, tokens, scales);
+    else if (a.k <= 8)
+      permute_few_kernel<8><<<grid, kFewThreads, 0, stream>>>(a, tokens, scales);
+    else
+      permute_few_kernel<16><<<grid, kFewThreads, 0, stream>>>(a, tokens, scales);
     return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
   }
   permute_count_kernel<<<a.blocks, kCountThreads, 0, stream>>>(a);
   place_all(a, stream);
-  move_rows(args->tokens, args->permute_tokens, row, a.idx, args->T, args->top_k, n, stream);
-  if (scale_row > 0)
-    move_rows(args->per_token_scales, args->permute_per_token_scales, scale_row, a.idx, args->T, args->top_k, n, stream);
+  move_both(tokens, scales, a.idx, args->T, args->top_k, n, stream);
   return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
 }

@@ -113,35 +113,39 @@ __device__ __forceinline__ void grad_choices(const GradArgs& a, size_t token, ui
   const uint32_t tid = threadIdx.x;
   const uint8_t* grad = a.grad + token * a.H * U::kBytes;
   const size_t at = token * a.k + first;
-  float dot[kK];
+  float dot[kK], w[kK];
+  int32_t idx[kK];  // read before any store: a load behind one would wait for it
 #pragma unroll
-  for (int j = 0; j < kK; ++j) dot[j] = 0.0f;
+  for (int j = 0; j < kK; ++j) {
+    const bool exists = first + j < a.k;
+    dot[j] = 0.0f;
+    idx[j] = exists ? a.idx[at + j] : static_cast<int32_t>(0x80000000u);
+    w[j] = exists ? a.weight[at + j] : 0.0f;
+  }
   for (uint32_t col = tid * kN; col < a.H; col += 64 * kWaves * kN) {
     U g, v[kK];
     g.template load<kStream>(grad, col, a.H);
 #pragma unroll
     for (int j = 0; j < kK; ++j) {
-      const uint32_t row = first + j < a.k ? static_cast<uint32_t>(a.idx[at + j]) : 0xffffffffu;
+      const uint32_t row = static_cast<uint32_t>(idx[j]);
 #pragma unroll
       for (int i = 0; i < U::kWords; ++i) v[j].w[i] = 0;
       if (row < a.R) v[j].template load<kStream>(a.rows + static_cast<size_t>(row) * a.H * U::kBytes, col, a.H);
     }
 #pragma unroll
-    for (int j = 0; j < kK; ++j)
-      if (first + j < a.k) {
-        const int32_t i = a.idx[at + j];
-        const uint32_t row = static_cast<uint32_t>(i < 0 ? ~i : i);
-        const float w = a.weight[at + j];
-        U out;
+    for (int j = 0; j < kK; ++j) {
+      const bool gone = idx[j] < 0;
+      const uint32_t row = static_cast<uint32_t>(gone ? ~idx[j] : idx[j]);
+      U out;
 #pragma unroll
-        for (uint32_t e = 0; e < kN; e += 2) {
-          const float g0 = g.get(e), g1 = g.get(e + 1);
-          dot[j] = __builtin_fmaf(g0, v[j].get(e), dot[j]);
-          dot[j] = __builtin_fmaf(g1, v[j].get(e + 1), dot[j]);
-          out.put(e / 2, i < 0 ? 0.0f : w * g0, i < 0 ? 0.0f : w * g1);
-        }
-        if (row < a.R) out.template store<kStream>(a.grad_rows + static_cast<size_t>(row) * a.H * U::kBytes, col, a.H);
+      for (uint32_t e = 0; e < kN; e += 2) {
+        const float g0 = g.get(e), g1 = g.get(e + 1);
+        dot[j] = __builtin_fmaf(g0, v[j].get(e), dot[j]);
+        dot[j] = __builtin_fmaf(g1, v[j].get(e + 1), dot[j]);
+        out.put(e / 2, gone ? 0.0f : w[j] * g0, gone ? 0.0f : w[j] * g1);
       }
+      if (row < a.R) out.template store<kStream>(a.grad_rows + static_cast<size_t>(row) * a.H * U::kBytes, col, a.H);
+    }
   }
   if (first > 0) __syncthreads();  // the choices before have been read from sh
 #pragma unroll
@@ -154,7 +158,7 @@ __device__ __forceinline__ void grad_choices(const GradArgs& a, size_t token, ui
     float d = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) d += sh[w][tid];
-    a.grad_weight[at + tid] = static_cast<uint32_t>(a.idx[at + tid]) < a.R ? d : 0.0f;
+    a.grad_weight[at + tid] = d;  // 0 where there is no row: none was added
   }
 }
 
