@@ -33,6 +33,7 @@ struct NormArgs {
   float eps;
   double eps64;
   float inv_h;
+  int32_t stream;  // rows go past the caches
   int32_t narrow;  // y's type: I8 or F8_E4M3FN with kRow, F8_E4M3FN or F4_E2M1 with kMx
 };
 
@@ -81,28 +82,33 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
 
   Eight<kX> s[kUnits];
   Eight<kW> w[kUnits];
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const uint32_t col = 8 * (i * kLanes + lane);
-    s[i].template load<false>(a.x + first * Eight<kX>::kBytes, col, a.H);
-  }
-  if (a.residual != nullptr) {
-    Eight<kX> r[kUnits];
+  const auto load = [&](auto stream, Eight<kX>(&v)[kUnits], const uint8_t* from) {
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
-      r[i].template load<false>(a.residual + first * Eight<kX>::kBytes, 8 * (i * kLanes + lane), a.H);
+      v[i].template load<decltype(stream)::value>(from + first * Eight<kX>::kBytes, 8 * (i * kLanes + lane), a.H);
+  };
+  Eight<kX> add[kUnits];
+  if (a.stream) {
+    load(std::true_type{}, s, a.x);
+    if (a.residual != nullptr) load(std::true_type{}, add, a.residual);
+  } else {
+    load(std::false_type{}, s, a.x);
+    if (a.residual != nullptr) load(std::false_type{}, add, a.residual);
+  }
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) w[i].template load<false>(a.weight, 8 * (i * kLanes + lane), a.H);
+  for (int i = 0; i < kUnits; ++i) w[i].template load<false>(a.weight, 8 * (i * kLanes + lane), a.H);
+  if (a.residual != nullptr) {
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
+      const uint32_t col = 8 * (i * kLanes + lane);
 #pragma unroll
       for (int k = 0; k < 8; k += 2)
-        s[i].put(k / 2, s[i].get(k) + r[i].get(k), s[i].get(k + 1) + r[i].get(k + 1));
-      s[i].template store<false>(a.sum + first * Eight<kX>::kBytes, 8 * (i * kLanes + lane), a.H);
+        s[i].put(k / 2, s[i].get(k) + add[i].get(k), s[i].get(k + 1) + add[i].get(k + 1));
+      if (a.stream)
+        s[i].template store<true>(a.sum + first * Eight<kX>::kBytes, col, a.H);
+      else
+        s[i].template store<false>(a.sum + first * Eight<kX>::kBytes, col, a.H);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) w[i].template load<false>(a.weight, 8 * (i * kLanes + lane), a.H);
   }
 
   float sum = 0.0f;
@@ -115,6 +121,8 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
       sum = __builtin_fmaf(v, v, sum);
       if constexpr (kOut == kRow) top = max(top, __float_as_uint(v * w[i].get(k)) & 0x7fffffffu);
     }
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i) s[i].keep_packed(), w[i].keep_packed();
   sum = sum64_f32(sum);
   if constexpr (kOut == kRow) top = max64_u32(top);
   __shared__ Shared<kLanes> sh;
@@ -220,7 +228,10 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
       Eight<kX> out;
 #pragma unroll
       for (int k = 0; k < 8; k += 2) out.put(k / 2, y[k], y[k + 1]);
-      if (col < a.H) out.template store<false>(a.y + first * Eight<kX>::kBytes, col, a.H);
+      if (a.stream)
+        out.template store<true>(a.y + first * Eight<kX>::kBytes, col, a.H);
+      else
+        out.template store<false>(a.y + first * Eight<kX>::kBytes, col, a.H);
     } else {
       uint32_t m = 0;
 #pragma unroll
@@ -296,6 +307,8 @@ void launch_types(const NormArgs& a, int out, NormShape s, hipStream_t stream) {
 
 // A launch holds less than 2^32 threads.
 constexpr int64_t kRowsPerLaunch = int64_t(1) << 21;
+// From so many bytes of rows on they are read, and written, past the caches.
+constexpr int64_t kStreamBytes = int64_t(64) << 20;
 
 }  // namespace
 }  // namespace mrr
@@ -324,6 +337,7 @@ extern "C" mrr_status mrr_rms_norm(const mrr_rms_norm_args* args, struct ihipStr
     a.eps = static_cast<float>(args->eps);
     a.eps64 = args->eps;
     a.inv_h = 1.0f / static_cast<float>(args->H);
+    a.stream = args->rows * args->H * b >= kStreamBytes;
     a.narrow = args->y_dtype;
     switch (args->dtype) {
       case MRR_F16:

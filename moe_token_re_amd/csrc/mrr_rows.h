@@ -94,6 +94,14 @@ struct Pack {
     return static_cast<float>(__builtin_bit_cast(f16x2, v)[k % 2]);
   }
 
+  // Has the values widened anew from here on, instead of kept wide in twice the registers.
+  __device__ __forceinline__ void keep_packed() {
+    if constexpr (kDtype != MRR_F32) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) asm volatile("" : "+v"(w[i]));
+    }
+  }
+
   // Values 2 i and 2 i + 1, rounded to nearest even.
   __device__ __forceinline__ void put(int i, float a, float b) {
     if constexpr (kDtype == MRR_F32) {
