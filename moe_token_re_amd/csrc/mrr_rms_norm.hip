@@ -82,32 +82,36 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
 
   Eight<kX> s[kUnits];
   Eight<kW> w[kUnits];
-  const auto load = [&](auto stream, Eight<kX>(&v)[kUnits], const uint8_t* from) {
+  constexpr uint32_t kBytes = Eight<kX>::kBytes;
+  const auto col_of = [&](int i) { return 8 * (i * kLanes + lane); };
+  const auto load = [&](Eight<kX>(&v)[kUnits], const uint8_t* from) {
+    if (a.stream) {
+      const WholeRow<> r(from + first * kBytes, a.H * kBytes);
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i)
-      v[i].template load<decltype(stream)::value>(from + first * Eight<kX>::kBytes, 8 * (i * kLanes + lane), a.H);
+      for (int i = 0; i < kUnits; ++i) v[i].load_whole(r, col_of(i));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) v[i].load(from + first * kBytes, col_of(i), a.H);
+    }
+  };
+  const auto store = [&](uint8_t* to, int i, const Eight<kX>& v) {
+    if (a.stream)
+      v.store_whole(WholeRow<>(to + first * kBytes, a.H * kBytes), col_of(i));
+    else
+      v.store(to + first * kBytes, col_of(i), a.H);
   };
   Eight<kX> add[kUnits];
-  if (a.stream) {
-    load(std::true_type{}, s, a.x);
-    if (a.residual != nullptr) load(std::true_type{}, add, a.residual);
-  } else {
-    load(std::false_type{}, s, a.x);
-    if (a.residual != nullptr) load(std::false_type{}, add, a.residual);
-  }
+  load(s, a.x);
+  if (a.residual != nullptr) load(add, a.residual);
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) w[i].template load<false>(a.weight, 8 * (i * kLanes + lane), a.H);
+  for (int i = 0; i < kUnits; ++i) w[i].load(a.weight, col_of(i), a.H);
   if (a.residual != nullptr) {
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const uint32_t col = 8 * (i * kLanes + lane);
 #pragma unroll
       for (int k = 0; k < 8; k += 2)
         s[i].put(k / 2, s[i].get(k) + add[i].get(k), s[i].get(k + 1) + add[i].get(k + 1));
-      if (a.stream)
-        s[i].template store<true>(a.sum + first * Eight<kX>::kBytes, col, a.H);
-      else
-        s[i].template store<false>(a.sum + first * Eight<kX>::kBytes, col, a.H);
+      store(a.sum, i, s[i]);
     }
   }
 
@@ -190,7 +194,7 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
     const float over = top == 0 ? 0.0f : 1.0f / most;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
-      const uint32_t col = 8 * (i * kLanes + lane);
+      const uint32_t col = col_of(i);
       if (col >= a.H) break;
       float q[8];
 #pragma unroll
@@ -215,7 +219,7 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
 
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) {
-    const uint32_t col = 8 * (i * kLanes + lane);
+    const uint32_t col = col_of(i);
     float y[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) y[k] = s[i].get(k) * r * w[i].get(k);
@@ -228,10 +232,7 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
       Eight<kX> out;
 #pragma unroll
       for (int k = 0; k < 8; k += 2) out.put(k / 2, y[k], y[k + 1]);
-      if (a.stream)
-        out.template store<true>(a.y + first * Eight<kX>::kBytes, col, a.H);
-      else
-        out.template store<false>(a.y + first * Eight<kX>::kBytes, col, a.H);
+      store(a.y, i, out);
     } else {
       uint32_t m = 0;
 #pragma unroll
@@ -337,7 +338,8 @@ extern "C" mrr_status mrr_rms_norm(const mrr_rms_norm_args* args, struct ihipStr
     a.eps = static_cast<float>(args->eps);
     a.eps64 = args->eps;
     a.inv_h = 1.0f / static_cast<float>(args->H);
-    a.stream = args->rows * args->H * b >= kStreamBytes;
+    a.stream = args->rows * args->H * b >= kStreamBytes &&
+               whole_units(args->H * b, a.x, a.residual, a.sum, out == kWide ? a.y : nullptr);
     a.narrow = args->y_dtype;
     switch (args->dtype) {
       case MRR_F16:

@@ -39,7 +39,7 @@ struct Unit {
     at = unit * r.unit;
     if (r.unit == 16) {
       at = min(at, r.bytes - 16);
-      v = load16<false>(p + at);
+      v = load16(p + at);
     } else if (r.unit == 4) {
       uint32_t x;
       __builtin_memcpy(&x, p + at, 4);
@@ -52,11 +52,10 @@ struct Unit {
       v[0] = p[at];
     }
   }
-  template <bool kStream>
   __device__ __forceinline__ void store(const Rows& r, size_t row, bool zero) const {
     uint8_t* p = r.dst + row * r.bytes + at;
     if (r.unit == 16) {
-      store16<kStream>(p, zero ? rows_u32x4{0, 0, 0, 0} : v);
+      store16(p, zero ? rows_u32x4{0, 0, 0, 0} : v);
     } else {
       const uint32_t x = zero ? 0 : v[0];
       if (r.unit == 4) {
@@ -205,8 +204,8 @@ __global__ __launch_bounds__(kFewThreads) void permute_few_kernel(SortArgs a, Ro
   for (uint32_t j = 0; j < kK; ++j) {
     if (j < a.k) {
       const bool zero = own[j] >= away;
-      if (moves) u.store<false>(tokens, row[j], zero);
-      if (moves_scales) s.store<false>(scales, row[j], zero);
+      if (moves) u.store(tokens, row[j], zero);
+      if (moves_scales) s.store(scales, row[j], zero);
       if (writes && tid == j) {
         a.idx[first + j] = static_cast<int32_t>(zero ? ~row[j] : row[j]);
         if (a.weight != nullptr) a.out_weight[row[j]] = zero ? 0.0f : weight;
@@ -218,7 +217,7 @@ __global__ __launch_bounds__(kFewThreads) void permute_few_kernel(SortArgs a, Ro
     s.load(scales, token, more);
 #pragma unroll
     for (uint32_t j = 0; j < kK; ++j)
-      if (j < a.k) s.store<false>(scales, row[j], own[j] >= away);
+      if (j < a.k) s.store(scales, row[j], own[j] >= away);
   }
 }
 
@@ -344,7 +343,6 @@ struct MoveArgs {
 
 // Moves one unit of a token's row to its choices' rows. The index is read before the
 // stores, eight choices at a time: a load behind a store would wait for it.
-template <bool kStream>
 __device__ __forceinline__ void move_unit(const MoveArgs& a, const Rows& r, size_t token, uint32_t unit) {
   Unit u;
   u.load(r, token, unit);
@@ -356,7 +354,7 @@ __device__ __forceinline__ void move_unit(const MoveArgs& a, const Rows& r, size
 #pragma unroll
     for (uint32_t j = 0; j < 8; ++j) {
       const uint32_t row = static_cast<uint32_t>(i[j] < 0 ? ~i[j] : i[j]);
-      if (j0 + j < a.k && row < a.R) u.store<kStream>(r, row, i[j] < 0);
+      if (j0 + j < a.k && row < a.R) u.store(r, row, i[j] < 0);
     }
   }
 }
@@ -370,28 +368,28 @@ __global__ __launch_bounds__(64) void move_rows_kernel(MoveArgs a, Rows r, Rows 
   if (blockIdx.y < first) {
     const uint32_t tokens = 64 / scales.units, in_wave = threadIdx.x / scales.units;
     const uint32_t t = (blockIdx.y * gridDim.x + blockIdx.x) * tokens + in_wave;
-    if (in_wave < tokens && t < a.T) move_unit<false>(a, scales, t, threadIdx.x - in_wave * scales.units);
+    if (in_wave < tokens && t < a.T) move_unit(a, scales, t, threadIdx.x - in_wave * scales.units);
     return;
   }
   const uint32_t token = blockIdx.y - first;
   const int32_t mine = a.idx[static_cast<size_t>(token) * a.k + min(threadIdx.x, a.k - 1)];
   // lanes behind the row's end move its last unit as well
   const uint32_t at = min((blockIdx.x * 64 + threadIdx.x) * 16, r.bytes - 16);
-  const rows_u32x4 v = load16<false>(r.src + static_cast<size_t>(token) * r.bytes + at);
+  const rows_u32x4 v = load16(r.src + static_cast<size_t>(token) * r.bytes + at);
   for (uint32_t j = 0; j < a.k; ++j) {
     const int32_t i = __builtin_amdgcn_readlane(mine, j);
     const uint32_t row = static_cast<uint32_t>(i < 0 ? ~i : i);
     if (row >= a.R) continue;
     uint8_t* to = r.dst + static_cast<size_t>(row) * r.bytes;
-    if (i >= 0)
-      store16<kStream>(to + at, v);
+    const rows_u32x4 out = i >= 0 ? v : rows_u32x4{0, 0, 0, 0};
+    if constexpr (kStream)
+      WholeRow<>(to, r.bytes).store(at, out);
     else
-      store16<kStream>(to + at, rows_u32x4{0, 0, 0, 0});
+      store16(to + at, out);
   }
 }
 
 // Shorter ones, scales included: as many tokens a wave as fit.
-template <bool kStream>
 __global__ __launch_bounds__(256) void move_short_rows_kernel(MoveArgs a, Rows r, Rows scales) {
   const uint32_t units = r.units + scales.units;
   const uint32_t lane = threadIdx.x % 64, tokens = 64 / units, in_wave = lane / units;
@@ -399,9 +397,9 @@ __global__ __launch_bounds__(256) void move_short_rows_kernel(MoveArgs a, Rows r
   if (in_wave >= tokens || token >= a.T) return;
   const uint32_t unit = lane - in_wave * units;
   if (unit < r.units)
-    move_unit<kStream>(a, r, token, unit);
+    move_unit(a, r, token, unit);
   else
-    move_unit<false>(a, scales, token, unit - r.units);
+    move_unit(a, scales, token, unit - r.units);
 }
 
 // Tokens of a launch whose grid's second dimension they are, with the scales' rows of workgroups.
@@ -427,7 +425,7 @@ void move_all(const MoveArgs& all, Rows r, Rows scales, hipStream_t stream) {
       move_rows_kernel<kStream><<<dim3(pieces, a.T + more), 64, 0, stream>>>(a, r, scales, more);
     } else {
       const uint32_t each = 4 * (64 / (r.units + scales.units));
-      move_short_rows_kernel<kStream><<<(a.T + each - 1) / each, 256, 0, stream>>>(a, r, scales);
+      move_short_rows_kernel<<<(a.T + each - 1) / each, 256, 0, stream>>>(a, r, scales);
     }
     t += a.T;
     a.idx += static_cast<size_t>(a.T) * a.k;
@@ -439,7 +437,7 @@ void move_all(const MoveArgs& all, Rows r, Rows scales, hipStream_t stream) {
 // scales: of no units where there are none.
 void move_both(const Rows& r, const Rows& scales, const int32_t* idx, int64_t T, int64_t k, int64_t R, hipStream_t stream) {
   const MoveArgs a{idx, static_cast<uint32_t>(T), static_cast<uint32_t>(k), static_cast<uint32_t>(R)};
-  if (R * r.bytes >= kStreamBytes)
+  if (R * r.bytes >= kStreamBytes && whole_units(r.bytes, r.dst))
     move_all<true>(a, r, scales, stream);
   else
     move_all<false>(a, r, scales, stream);

@@ -13,6 +13,10 @@
 namespace mrr {
 namespace {
 
+// How rows are read and written: of any alignment; or in whole units, written past the
+// caches; and read past them as well.
+enum { kAny = 0, kWhole = 1, kPast = 2 };
+
 struct SumArgs {
   const uint8_t* rows;
   const int32_t* idx;
@@ -24,7 +28,7 @@ struct SumArgs {
 };
 
 // One unit's sum over choices [first, first + kK) of a token, of which those below k exist.
-template <int kDtype, int kK, bool kAll, bool kStream>
+template <int kDtype, int kK, bool kAll, int kHow>
 __device__ __forceinline__ void add_choices(const SumArgs& a, size_t token, uint32_t first, uint32_t col,
                                             float (&sum)[16 / Unit16<kDtype>::kBytes]) {
   using U = Unit16<kDtype>;
@@ -38,9 +42,14 @@ __device__ __forceinline__ void add_choices(const SumArgs& a, size_t token, uint
     const uint32_t row = exists ? static_cast<uint32_t>(a.idx[at]) : 0xffffffffu;
     const bool here = row < a.R;
     w[j] = !here ? 0.0f : a.weight != nullptr ? a.weight[at] : 1.0f;
+    if constexpr (kHow != kAny) {
+      const size_t from = here ? static_cast<size_t>(row) * a.H * U::kBytes : 0;
+      v[j].load_whole(WholeRow<kHow == kPast>(a.rows + from, here ? a.H * U::kBytes : 0), col);
+    } else {
 #pragma unroll
-    for (int i = 0; i < U::kWords; ++i) v[j].w[i] = 0;
-    if (here) v[j].template load<kStream>(a.rows + static_cast<size_t>(row) * a.H * U::kBytes, col, a.H);
+      for (int i = 0; i < U::kWords; ++i) v[j].w[i] = 0;
+      if (here) v[j].load(a.rows + static_cast<size_t>(row) * a.H * U::kBytes, col, a.H);
+    }
   }
 #pragma unroll
   for (int j = 0; j < kK; ++j)
@@ -49,21 +58,24 @@ __device__ __forceinline__ void add_choices(const SumArgs& a, size_t token, uint
 }
 
 // kK: so many choices, or 0: more than 8.
-template <int kDtype, int kK, bool kStream>
+template <int kDtype, int kK, int kHow>
 __device__ __forceinline__ void sum_unit(const SumArgs& a, size_t token, uint32_t col) {
   using U = Unit16<kDtype>;
   constexpr int kN = 16 / U::kBytes;
   float sum[kN] = {};
   if constexpr (kK > 0) {
-    add_choices<kDtype, kK, true, kStream>(a, token, 0, col, sum);
+    add_choices<kDtype, kK, true, kHow>(a, token, 0, col, sum);
   } else {
-    add_choices<kDtype, 8, true, kStream>(a, token, 0, col, sum);
-    add_choices<kDtype, 8, false, kStream>(a, token, 8, col, sum);
+    add_choices<kDtype, 8, true, kHow>(a, token, 0, col, sum);
+    add_choices<kDtype, 8, false, kHow>(a, token, 8, col, sum);
   }
   U out;
 #pragma unroll
   for (int i = 0; i < kN; i += 2) out.put(i / 2, sum[i], sum[i + 1]);
-  out.template store<kStream>(a.y + token * a.H * U::kBytes, col, a.H);
+  if constexpr (kHow != kAny)
+    out.store_whole(WholeRow<kHow == kPast>(a.y + token * a.H * U::kBytes, a.H * U::kBytes), col);
+  else
+    out.store(a.y + token * a.H * U::kBytes, col, a.H);
 }
 
 __device__ __forceinline__ void choice_value(const SumArgs& a, size_t token, uint32_t j) {
@@ -73,16 +85,16 @@ __device__ __forceinline__ void choice_value(const SumArgs& a, size_t token, uin
 }
 
 // Rows of more than 64 units: a wave takes 1 KiB of a token's.
-template <int kDtype, int kK, bool kStream>
+template <int kDtype, int kK, int kHow>
 __global__ __launch_bounds__(64) void sum_rows_kernel(SumArgs a) {
   constexpr uint32_t kN = 16 / Unit16<kDtype>::kBytes;
   const uint32_t token = blockIdx.y, col = (blockIdx.x * 64 + threadIdx.x) * kN;
   if (a.choice_values != nullptr && blockIdx.x == 0 && threadIdx.x < a.k) choice_value(a, token, threadIdx.x);
-  if (col < a.H) sum_unit<kDtype, kK, kStream>(a, token, col);
+  if (col < a.H) sum_unit<kDtype, kK, kHow>(a, token, col);
 }
 
 // Shorter ones: as many tokens a wave as fit.
-template <int kDtype, int kK, bool kStream>
+template <int kDtype, int kK>
 __global__ __launch_bounds__(256) void sum_short_rows_kernel(SumArgs a) {
   constexpr uint32_t kN = 16 / Unit16<kDtype>::kBytes;
   const uint32_t units = (a.H + kN - 1) / kN;
@@ -92,7 +104,7 @@ __global__ __launch_bounds__(256) void sum_short_rows_kernel(SumArgs a) {
   const uint32_t unit = lane - in_wave * units;
   if (a.choice_values != nullptr)
     for (uint32_t j = unit; j < a.k; j += units) choice_value(a, token, j);
-  sum_unit<kDtype, kK, kStream>(a, token, unit * kN);
+  sum_unit<kDtype, kK, kAny>(a, token, unit * kN);
 }
 
 struct GradArgs {
@@ -106,7 +118,7 @@ struct GradArgs {
 };
 
 // Choices [first, first + kK) of a token, of which those below k exist.
-template <int kDtype, int kK, int kWaves, bool kStream>
+template <int kDtype, int kK, int kWaves, int kHow>
 __device__ __forceinline__ void grad_choices(const GradArgs& a, size_t token, uint32_t first, float (&sh)[kWaves][kK]) {
   using U = Unit16<kDtype>;
   constexpr uint32_t kN = 16 / U::kBytes;
@@ -124,13 +136,21 @@ __device__ __forceinline__ void grad_choices(const GradArgs& a, size_t token, ui
   }
   for (uint32_t col = tid * kN; col < a.H; col += 64 * kWaves * kN) {
     U g, v[kK];
-    g.template load<kStream>(grad, col, a.H);
+    if constexpr (kHow != kAny)
+      g.load_whole(WholeRow<kHow == kPast>(grad, a.H * U::kBytes), col);
+    else
+      g.load(grad, col, a.H);
 #pragma unroll
     for (int j = 0; j < kK; ++j) {
       const uint32_t row = static_cast<uint32_t>(idx[j]);
+      if constexpr (kHow != kAny) {
+        const size_t from = row < a.R ? static_cast<size_t>(row) * a.H * U::kBytes : 0;
+        v[j].load_whole(WholeRow<kHow == kPast>(a.rows + from, row < a.R ? a.H * U::kBytes : 0), col);
+      } else {
 #pragma unroll
-      for (int i = 0; i < U::kWords; ++i) v[j].w[i] = 0;
-      if (row < a.R) v[j].template load<kStream>(a.rows + static_cast<size_t>(row) * a.H * U::kBytes, col, a.H);
+        for (int i = 0; i < U::kWords; ++i) v[j].w[i] = 0;
+        if (row < a.R) v[j].load(a.rows + static_cast<size_t>(row) * a.H * U::kBytes, col, a.H);
+      }
     }
 #pragma unroll
     for (int j = 0; j < kK; ++j) {
@@ -144,7 +164,11 @@ __device__ __forceinline__ void grad_choices(const GradArgs& a, size_t token, ui
         dot[j] = __builtin_fmaf(g1, v[j].get(e + 1), dot[j]);
         out.put(e / 2, gone ? 0.0f : w[j] * g0, gone ? 0.0f : w[j] * g1);
       }
-      if (row < a.R) out.template store<kStream>(a.grad_rows + static_cast<size_t>(row) * a.H * U::kBytes, col, a.H);
+      uint8_t* to = a.grad_rows + static_cast<size_t>(row) * a.H * U::kBytes;
+      if constexpr (kHow != kAny)
+        out.store_whole(WholeRow<kHow == kPast>(to, row < a.R ? a.H * U::kBytes : 0), col);
+      else if (row < a.R)
+        out.store(to, col, a.H);
     }
   }
   if (first > 0) __syncthreads();  // the choices before have been read from sh
@@ -162,19 +186,23 @@ __device__ __forceinline__ void grad_choices(const GradArgs& a, size_t token, ui
   }
 }
 
-template <int kDtype, int kK, int kWaves, bool kStream>
+template <int kDtype, int kK, int kWaves, int kHow>
 __global__ __launch_bounds__(64 * kWaves) void sum_rows_backward_kernel(GradArgs a) {
   __shared__ float sh[kWaves][kK];
   for (uint32_t first = 0; first < a.k; first += kK)
-    grad_choices<kDtype, kK, kWaves, kStream>(a, blockIdx.x, first, sh);
+    grad_choices<kDtype, kK, kWaves, kHow>(a, blockIdx.x, first, sh);
 }
 
 constexpr uint32_t kMostGridY = 65535;
 constexpr uint32_t kMostTokens = 1u << 23;  // of a launch, which holds less than 2^32 threads
-// Rows of so many bytes are read past the caches.
-constexpr int64_t kStreamBytes = int64_t(64) << 20;
+// From so many bytes of rows on their sums and gradients are written past the caches, and
+// from so many on, which the last of them does not hold, the rows are read past them
+// (8192 tokens of 8 rows of 14 KiB, 940 MB: 178 us so and 193 otherwise; of 6 rows of 4 KiB,
+// 200 MB, forward and back: 120 us so and 114 otherwise).
+constexpr int64_t kWholeBytes = int64_t(64) << 20, kPastBytes = int64_t(256) << 20;
+int how(int64_t bytes, bool whole) { return !whole || bytes < kWholeBytes ? kAny : bytes < kPastBytes ? kWhole : kPast; }
 
-template <int kDtype, int kK, bool kStream>
+template <int kDtype, int kK, int kHow>
 void launch_sum(const SumArgs& all, hipStream_t stream) {
   constexpr uint32_t kN = 16 / Unit16<kDtype>::kBytes, kBytes = Unit16<kDtype>::kBytes;
   const uint32_t units = (all.H + kN - 1) / kN, most = units > 64 ? kMostGridY : kMostTokens;
@@ -186,34 +214,51 @@ void launch_sum(const SumArgs& all, hipStream_t stream) {
     if (a.choice_values != nullptr) a.choice_values += static_cast<size_t>(t) * a.k;
     a.y += static_cast<size_t>(t) * a.H * kBytes;
     if (units > 64) {
-      sum_rows_kernel<kDtype, kK, kStream><<<dim3((units + 63) / 64, a.T), 64, 0, stream>>>(a);
+      sum_rows_kernel<kDtype, kK, kHow><<<dim3((units + 63) / 64, a.T), 64, 0, stream>>>(a);
     } else {
       const uint32_t each = 4 * (64 / units);
-      sum_short_rows_kernel<kDtype, kK, kStream><<<(a.T + each - 1) / each, 256, 0, stream>>>(a);
+      sum_short_rows_kernel<kDtype, kK><<<(a.T + each - 1) / each, 256, 0, stream>>>(a);
     }
     t += a.T;
   }
 }
 
-template <int kDtype, bool kStream>
+template <int kDtype, int kHow>
 void launch_sum_k(const SumArgs& a, hipStream_t stream) {
   switch (a.k) {
-    case 1: launch_sum<kDtype, 1, kStream>(a, stream); break;
-    case 2: launch_sum<kDtype, 2, kStream>(a, stream); break;
-    case 3: launch_sum<kDtype, 3, kStream>(a, stream); break;
-    case 4: launch_sum<kDtype, 4, kStream>(a, stream); break;
-    case 5: launch_sum<kDtype, 5, kStream>(a, stream); break;
-    case 6: launch_sum<kDtype, 6, kStream>(a, stream); break;
-    case 7: launch_sum<kDtype, 7, kStream>(a, stream); break;
-    case 8: launch_sum<kDtype, 8, kStream>(a, stream); break;
-    default: launch_sum<kDtype, 0, kStream>(a, stream); break;
+    case 1: launch_sum<kDtype, 1, kHow>(a, stream); break;
+    case 2: launch_sum<kDtype, 2, kHow>(a, stream); break;
+    case 3: launch_sum<kDtype, 3, kHow>(a, stream); break;
+    case 4: launch_sum<kDtype, 4, kHow>(a, stream); break;
+    case 5: launch_sum<kDtype, 5, kHow>(a, stream); break;
+    case 6: launch_sum<kDtype, 6, kHow>(a, stream); break;
+    case 7: launch_sum<kDtype, 7, kHow>(a, stream); break;
+    case 8: launch_sum<kDtype, 8, kHow>(a, stream); break;
+    default: launch_sum<kDtype, 0, kHow>(a, stream); break;
   }
+}
+
+template <int kHow>
+void launch_sum_how(const SumArgs& a, int32_t dtype, hipStream_t stream) {
+  switch (dtype) {
+    case MRR_F16: launch_sum_k<MRR_F16, kHow>(a, stream); break;
+    case MRR_BF16: launch_sum_k<MRR_BF16, kHow>(a, stream); break;
+    default: launch_sum_k<MRR_F32, kHow>(a, stream); break;
+  }
+}
+void launch_sum_dtype(const SumArgs& a, int32_t dtype, int how, hipStream_t stream) {
+  if (how == kAny)
+    launch_sum_how<kAny>(a, dtype, stream);
+  else if (how == kWhole)
+    launch_sum_how<kWhole>(a, dtype, stream);
+  else
+    launch_sum_how<kPast>(a, dtype, stream);
 }
 
 // A token's row by a wave, or by four from so many bytes on.
 constexpr uint32_t kWideRow = 2048;
 
-template <int kDtype, int kK, bool kStream>
+template <int kDtype, int kK, int kHow>
 void launch_grad(const GradArgs& all, hipStream_t stream) {
   constexpr uint32_t kBytes = Unit16<kDtype>::kBytes;
   for (uint32_t t = 0; t < all.T;) {
@@ -224,25 +269,42 @@ void launch_grad(const GradArgs& all, hipStream_t stream) {
     a.grad_weight += static_cast<size_t>(t) * a.k;
     a.grad += static_cast<size_t>(t) * a.H * kBytes;
     if (a.H * kBytes > kWideRow)
-      sum_rows_backward_kernel<kDtype, kK, 4, kStream><<<a.T, 256, 0, stream>>>(a);
+      sum_rows_backward_kernel<kDtype, kK, 4, kHow><<<a.T, 256, 0, stream>>>(a);
     else
-      sum_rows_backward_kernel<kDtype, kK, 1, kStream><<<a.T, 64, 0, stream>>>(a);
+      sum_rows_backward_kernel<kDtype, kK, 1, kHow><<<a.T, 64, 0, stream>>>(a);
     t += a.T;
   }
 }
 
-template <int kDtype, bool kStream>
+template <int kDtype, int kHow>
 void launch_grad_k(const GradArgs& a, hipStream_t stream) {
   if (a.k == 1)
-    launch_grad<kDtype, 1, kStream>(a, stream);
+    launch_grad<kDtype, 1, kHow>(a, stream);
   else if (a.k == 2)
-    launch_grad<kDtype, 2, kStream>(a, stream);
+    launch_grad<kDtype, 2, kHow>(a, stream);
   else if (a.k <= 4)
-    launch_grad<kDtype, 4, kStream>(a, stream);
+    launch_grad<kDtype, 4, kHow>(a, stream);
   else if (a.k <= 6)
-    launch_grad<kDtype, 6, kStream>(a, stream);
+    launch_grad<kDtype, 6, kHow>(a, stream);
   else  // above 8 in two rounds
-    launch_grad<kDtype, 8, kStream>(a, stream);
+    launch_grad<kDtype, 8, kHow>(a, stream);
+}
+
+template <int kHow>
+void launch_grad_how(const GradArgs& a, int32_t dtype, hipStream_t stream) {
+  switch (dtype) {
+    case MRR_F16: launch_grad_k<MRR_F16, kHow>(a, stream); break;
+    case MRR_BF16: launch_grad_k<MRR_BF16, kHow>(a, stream); break;
+    default: launch_grad_k<MRR_F32, kHow>(a, stream); break;
+  }
+}
+void launch_grad_dtype(const GradArgs& a, int32_t dtype, int how, hipStream_t stream) {
+  if (how == kAny)
+    launch_grad_how<kAny>(a, dtype, stream);
+  else if (how == kWhole)
+    launch_grad_how<kWhole>(a, dtype, stream);
+  else
+    launch_grad_how<kPast>(a, dtype, stream);
 }
 
 }  // namespace
@@ -256,12 +318,7 @@ extern "C" mrr_status mrr_token_unpermute(const mrr_token_unpermute_args* args, 
                   static_cast<uint8_t*>(args->y), args->row_values, args->choice_values, static_cast<uint32_t>(args->T),
                   static_cast<uint32_t>(args->top_k), static_cast<uint32_t>(args->R), static_cast<uint32_t>(args->H)};
   const int64_t b = args->dtype == MRR_F32 ? 4 : 2;
-  const bool large = args->T * args->top_k * args->H * b >= kStreamBytes;
-  switch (args->dtype) {
-    case MRR_F16: large ? launch_sum_k<MRR_F16, true>(a, stream) : launch_sum_k<MRR_F16, false>(a, stream); break;
-    case MRR_BF16: large ? launch_sum_k<MRR_BF16, true>(a, stream) : launch_sum_k<MRR_BF16, false>(a, stream); break;
-    default: large ? launch_sum_k<MRR_F32, true>(a, stream) : launch_sum_k<MRR_F32, false>(a, stream); break;
-  }
+  launch_sum_dtype(a, args->dtype, how(args->T * args->top_k * args->H * b, whole_units(args->H * b, a.rows, a.y)), stream);
   return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
 }
 
@@ -280,11 +337,8 @@ extern "C" mrr_status mrr_token_unpermute_backward(const mrr_token_unpermute_bac
                    args->permute_token_idx, args->expert_weight, static_cast<uint8_t*>(args->grad_rows),
                    args->grad_weight, static_cast<uint32_t>(args->T), static_cast<uint32_t>(args->top_k),
                    static_cast<uint32_t>(args->R), static_cast<uint32_t>(args->H)};
-  const bool large = args->T * args->top_k * args->H * b >= kStreamBytes;
-  switch (args->dtype) {
-    case MRR_F16: large ? launch_grad_k<MRR_F16, true>(a, stream) : launch_grad_k<MRR_F16, false>(a, stream); break;
-    case MRR_BF16: large ? launch_grad_k<MRR_BF16, true>(a, stream) : launch_grad_k<MRR_BF16, false>(a, stream); break;
-    default: large ? launch_grad_k<MRR_F32, true>(a, stream) : launch_grad_k<MRR_F32, false>(a, stream); break;
-  }
+  launch_grad_dtype(a, args->dtype,
+                    how(args->T * args->top_k * args->H * b, whole_units(args->H * b, a.grad, a.rows, a.grad_rows)),
+                    stream);
   return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
 }
