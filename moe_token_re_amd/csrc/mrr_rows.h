@@ -185,7 +185,6 @@ __device__ __forceinline__ uint32_t max16_u32(uint32_t v) {
   v = max(v, dpp_u32<kDppMirror8>(v));
   return max(v, dpp_u32<kDppMirror16>(v));
 }
-__device__ __forceinline__ uint32_t min16_u32(uint32_t v) { return ~max16_u32(~v); }
 
 // Over all 64 lanes.
 __device__ __forceinline__ float sum64_f32(float v) {
