@@ -223,83 +223,118 @@ __global__ __launch_bounds__(kFewThreads) void permute_few_kernel(SortArgs a, Ro
 
 // ------------------------------------------------------------ many choices
 
-constexpr int kCountThreads = 1024;
+constexpr int kSortThreads = 1024;
 
-__global__ __launch_bounds__(kCountThreads) void permute_count_kernel(SortArgs a) {
+// f(i, expert) of a lane's choices, from `first` (of lane 0) on every kStride-th, up to
+// `end`, eight of them read at once. Choices that are not here are counted for the wave at
+// once, by away(i, how many): they would all meet at one place.
+template <uint32_t kStride, typename F, typename G>
+__device__ __forceinline__ void each_choice(const SortArgs& a, uint32_t first, uint32_t end, F&& f, G&& away) {
+  const uint32_t lane = threadIdx.x % 64;
+  for (uint32_t i0 = first; i0 < end; i0 += 8 * kStride) {
+    int32_t id[8];
+#pragma unroll
+    for (uint32_t x = 0; x < 8; ++x) id[x] = a.ids[min(i0 + x * kStride + lane, end - 1)];
+#pragma unroll
+    for (uint32_t x = 0; x < 8; ++x) {
+      const uint32_t i = i0 + x * kStride + lane, e = expert_of(id[x], a.E);
+      const uint64_t gone = __ballot(i < end && e == a.E);
+      if (i < end && e < a.E) f(i, e);
+      if (gone != 0 && lane == 0) away(i, static_cast<uint32_t>(__popcll(gone)));
+    }
+  }
+}
+
+__global__ __launch_bounds__(kSortThreads) void permute_count_kernel(SortArgs a) {
   __shared__ uint32_t count[kPermuteMaxExperts + 1];
-  for (uint32_t e = threadIdx.x; e <= a.E; e += kCountThreads) count[e] = 0;
+  for (uint32_t e = threadIdx.x; e <= a.E; e += kSortThreads) count[e] = 0;
   __syncthreads();
-  const uint32_t first = blockIdx.x * a.block, end = min(a.n, first + a.block);
-  for (uint32_t i = first + threadIdx.x; i < end; i += kCountThreads) atomicAdd(&count[expert_of(a.ids[i], a.E)], 1u);
+  const uint32_t first = blockIdx.x * a.block;
+  each_choice<kSortThreads>(a, first + threadIdx.x / 64 * 64, min(a.n, first + a.block), [&](uint32_t, uint32_t e) { atomicAdd(&count[e], 1u); },
+              [&](uint32_t, uint32_t n) { atomicAdd(&count[a.E], n); });
   __syncthreads();
-  for (uint32_t e = threadIdx.x; e <= a.E; e += kCountThreads)
+  for (uint32_t e = threadIdx.x; e <= a.E; e += kSortThreads)
     a.counts[static_cast<size_t>(blockIdx.x) * (a.E + 1) + e] = static_cast<int32_t>(count[e]);
 }
 
-// A block's choices take their rows. Its waves have a run of neighbouring choices each,
-// count them by expert, and place them in order, 64 at a time: the lanes of the same
-// expert are found by its bits.
-template <int kWaves>
-__global__ __launch_bounds__(64 * kWaves) void permute_place_kernel(SortArgs a) {
-  constexpr int kThreads = 64 * kWaves;
-  extern __shared__ uint32_t at[];  // [kWaves + 2, E + 1]
-  __shared__ uint32_t sh[kWaves];
+// A block's choices take their rows. kRuns of its waves have a run of neighbouring choices
+// each, counted by expert and placed in order, 64 at a time: the lanes of the same expert
+// are found by its bits.
+// kSelf: without the blocks' counts, of few blocks; each counts all choices by itself.
+template <int kRuns, bool kSelf>
+__global__ __launch_bounds__(kSortThreads) void permute_place_kernel(SortArgs a) {
+  extern __shared__ uint32_t at[];  // [kRuns + 2, E + 1]
+  __shared__ uint32_t sh[kSortThreads / 64];
   const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64, width = a.E + 1;
-  uint32_t* total = at + kWaves * width;
+  uint32_t* total = at + kRuns * width;
   uint32_t* start = total + width;
-  for (uint32_t i = tid; i < width * (kWaves + 2); i += kThreads) at[i] = 0;
+  for (uint32_t i = tid; i < width * (kRuns + 2); i += kSortThreads) at[i] = 0;
   __syncthreads();
-  const uint32_t run = a.block / kWaves;  // a multiple of 64
-  const uint32_t first = blockIdx.x * a.block + wave * run, end = min(a.n, first + run);
-  uint32_t* mine = at + wave * width;
-  for (uint32_t i = first + lane; i < end; i += 64) atomicAdd(&mine[expert_of(a.ids[i], a.E)], 1u);
-  __syncthreads();
-  // Of an expert: all its choices, and those of the blocks before this one. Threads
-  // share its column among them where there are enough.
-  const uint32_t slices = width >= kThreads ? 1 : kThreads / width;
-  for (uint32_t i = tid; i < width * slices; i += kThreads) {
-    const uint32_t e = i % width, slice = i / width;
-    uint32_t all = 0, before = 0;
-    const int32_t* c = a.counts + e;
-    uint32_t b = slice;
-    for (; b + 7 * slices < a.blocks; b += 8 * slices) {
-      uint32_t v[8];
+  const uint32_t run = (kSelf ? static_cast<uint32_t>(kPermuteSelfBlock) : a.block) / kRuns;  // a multiple of 64
+  const uint32_t from = blockIdx.x * a.block;
+  // Of an expert: all its choices, those of the blocks before this one, and each run's.
+  if constexpr (kSelf) {
+    const uint32_t to = min(a.n, from + a.block);
+    const auto count = [&](uint32_t i, uint32_t e, uint32_t n) {
+      atomicAdd(&total[e], n);
+      if (i < from)
+        atomicAdd(&start[e], n);
+      else if (i < to)
+        atomicAdd(&at[(i - from) / run * width + e], n);
+    };
+    each_choice<kSortThreads>(a, wave * 64, a.n, [&](uint32_t i, uint32_t e) { count(i, e, 1); },
+                              [&](uint32_t i, uint32_t n) { count(i, a.E, n); });  // 64 of them, in one run
+  } else {
+    constexpr uint32_t kShare = kSortThreads / 64 / kRuns;  // waves of a run
+    const uint32_t begin = from + wave / kShare * run;
+    uint32_t* counts = at + wave / kShare * width;
+    each_choice<64 * kShare>(a, begin + wave % kShare * 64, min(a.n, begin + run),
+                             [&](uint32_t, uint32_t e) { atomicAdd(&counts[e], 1u); },
+                             [&](uint32_t, uint32_t n) { atomicAdd(&counts[a.E], n); });
+    // threads share its column of the blocks' counts among them where there are enough
+    const uint32_t slices = width >= kSortThreads ? 1 : kSortThreads / width;
+    for (uint32_t i = tid; i < width * slices; i += kSortThreads) {
+      const uint32_t e = i % width, slice = i / width;
+      uint32_t all = 0, before = 0;
+      const int32_t* c = a.counts + e;
+      for (uint32_t b0 = slice; b0 < a.blocks; b0 += 16 * slices) {
+        uint32_t v[16];
 #pragma unroll
-      for (uint32_t x = 0; x < 8; ++x) v[x] = static_cast<uint32_t>(c[static_cast<size_t>(b + x * slices) * width]);
+        for (uint32_t x = 0; x < 16; ++x)
+          v[x] = static_cast<uint32_t>(c[static_cast<size_t>(min(b0 + x * slices, a.blocks - 1)) * width]);
 #pragma unroll
-      for (uint32_t x = 0; x < 8; ++x) {
-        all += v[x];
-        before += b + x * slices < blockIdx.x ? v[x] : 0;
+        for (uint32_t x = 0; x < 16; ++x) {
+          all += b0 + x * slices < a.blocks ? v[x] : 0;
+          before += b0 + x * slices < blockIdx.x ? v[x] : 0;
+        }
       }
+      atomicAdd(&total[e], all);
+      atomicAdd(&start[e], before);
     }
-    for (; b < a.blocks; b += slices) {
-      const uint32_t v = static_cast<uint32_t>(c[static_cast<size_t>(b) * width]);
-      all += v;
-      before += b < blockIdx.x ? v : 0;
-    }
-    atomicAdd(&total[e], all);
-    atomicAdd(&start[e], before);
   }
   __syncthreads();
   // where its rows begin, where this block's of them do, then each wave's
-  const uint32_t per = (width + kThreads - 1) / kThreads, e0 = tid * per;
+  const uint32_t per = (width + kSortThreads - 1) / kSortThreads, e0 = tid * per;
   uint32_t sum = 0;
   for (uint32_t i = 0; i < per; ++i)
     if (e0 + i < width) sum += total[e0 + i];
-  uint32_t begin = scan_threads<kThreads>(sum, sh) - sum;
+  uint32_t begin = scan_threads<kSortThreads>(sum, sh) - sum;
   for (uint32_t i = 0; i < per; ++i) {
     const uint32_t e = e0 + i;
     if (e >= width) break;
     uint32_t place = begin + start[e];
     begin += total[e];
     if (blockIdx.x == 0 && e < a.E) a.num[e] = static_cast<int32_t>(a.cumsum ? begin : total[e]);
-    for (int w = 0; w < kWaves; ++w) {
+    for (int w = 0; w < kRuns; ++w) {
       const uint32_t c = at[w * width + e];
       at[w * width + e] = place;
       place += c;
     }
   }
   __syncthreads();
+  if (wave >= kRuns) return;
+  const uint32_t first = from + wave * run, end = min(a.n, first + run);
+  uint32_t* mine = at + wave * width;
   const int bits = 32 - __builtin_clz(a.E);
   // four times 64 choices are read before the first is written: a load behind a store
   // would wait for it
@@ -443,23 +478,19 @@ void move_both(const Rows& r, const Rows& scales, const int32_t* idx, int64_t T,
     move_all<false>(a, r, scales, stream);
 }
 
-template <int kWaves>
-constexpr uint32_t place_lds(uint32_t E) {
-  return (kWaves + 2) * (E + 1) * 4;
-}
+constexpr uint32_t place_lds(uint32_t runs, uint32_t E) { return (runs + 2) * (E + 1) * 4; }
 constexpr uint32_t kMostLds = 60 * 1024;
-static_assert(place_lds<1>(kPermuteMaxExperts) <= kMostLds, "experts' places in LDS");
-static_assert(kPermuteBlockChoices % (16 * 64) == 0, "a wave's run of choices");
+static_assert(place_lds(1, kPermuteMaxExperts) <= kMostLds, "experts' places in LDS");
+static_assert(kPermuteBlockChoices % (16 * 64) == 0 && kPermuteSelfBlock % (16 * 64) == 0, "a wave's run of choices");
 
+template <bool kSelf>
 void place_all(const SortArgs& a, hipStream_t stream) {
-  if (place_lds<16>(a.E) <= kMostLds)
-    permute_place_kernel<16><<<a.blocks, 1024, place_lds<16>(a.E), stream>>>(a);
-  else if (place_lds<8>(a.E) <= kMostLds)
-    permute_place_kernel<8><<<a.blocks, 512, place_lds<8>(a.E), stream>>>(a);
-  else if (place_lds<4>(a.E) <= kMostLds)
-    permute_place_kernel<4><<<a.blocks, 256, place_lds<4>(a.E), stream>>>(a);
+  if (place_lds(16, a.E) <= kMostLds)
+    permute_place_kernel<16, kSelf><<<a.blocks, kSortThreads, place_lds(16, a.E), stream>>>(a);
+  else if (place_lds(4, a.E) <= kMostLds)
+    permute_place_kernel<4, kSelf><<<a.blocks, kSortThreads, place_lds(4, a.E), stream>>>(a);
   else
-    permute_place_kernel<1><<<a.blocks, 64, place_lds<1>(a.E), stream>>>(a);
+    permute_place_kernel<1, kSelf><<<a.blocks, kSortThreads, place_lds(1, a.E), stream>>>(a);
 }
 
 }  // namespace
@@ -507,8 +538,14 @@ extern "C" mrr_status mrr_token_permute(const mrr_token_permute_args* args, void
       permute_few_kernel<16><<<grid, kFewThreads, 0, stream>>>(a, tokens, scales);
     return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
   }
-  permute_count_kernel<<<a.blocks, kCountThreads, 0, stream>>>(a);
-  place_all(a, stream);
+  if (n <= kPermuteSelfChoices) {
+    a.block = kPermuteSelfBlock;
+    a.blocks = static_cast<uint32_t>((n + kPermuteSelfBlock - 1) / kPermuteSelfBlock);
+    place_all<true>(a, stream);
+  } else {
+    permute_count_kernel<<<a.blocks, kSortThreads, 0, stream>>>(a);
+    place_all<false>(a, stream);
+  }
   move_both(tokens, scales, a.idx, args->T, args->top_k, n, stream);
   return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
 }
