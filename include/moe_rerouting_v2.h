@@ -588,11 +588,14 @@ typedef struct mrr_token_permute_args {
   int64_t expert_token_num_type;   /* 1: rows per expert; 0: their inclusive running sum */
 } mrr_token_permute_args;
 
-/* Bytes of workspace (16-byte aligned); 0 for sizes outside the contract. */
+/* Bytes of workspace (16-byte aligned); 0 for sizes outside the contract. Up to
+ * MRR_TOKEN_PERMUTE_ALONE choices (T top_k) use none, and NULL and 0 do as well. */
+#define MRR_TOKEN_PERMUTE_ALONE 16384
 size_t mrr_token_permute_workspace_size(int64_t T, int64_t top_k, int64_t E);
 mrr_status mrr_token_permute_validate(const mrr_token_permute_args* args, const void* workspace,
                                       size_t workspace_bytes);
-/* Runs it on `stream`: one kernel for few choices, three otherwise. */
+/* Runs it on `stream`: one kernel for few choices, two up to MRR_TOKEN_PERMUTE_ALONE, three otherwise
+ * (and one more for scale rows over 1 KiB, or longer than token rows under it). */
 mrr_status mrr_token_permute(const mrr_token_permute_args* args, void* workspace, size_t workspace_bytes,
                              struct ihipStream_t* stream);
 

@@ -57,8 +57,9 @@ inline int64_t norm_backward_groups(int64_t rows, int64_t H) {
 // (Tokens of 4 KiB, 8 choices each: 512 by the one kernel 11.3 us and by blocks 13.2, 1024
 // 22.9 and 16.1.)
 constexpr int64_t kPermuteFewChoices = 4096;
-// Up to so many choices the blocks are small and count all choices by themselves.
-constexpr int64_t kPermuteSelfChoices = 16384, kPermuteSelfBlock = 1024;
+// Up to so many choices the blocks are small and count all choices by themselves (8192: 14.2
+// us and by the counts 17.3, 16384: 16.6 and 17.2, 32768: 24.4 and 19.0).
+constexpr int64_t kPermuteSelfChoices = MRR_TOKEN_PERMUTE_ALONE, kPermuteSelfBlock = 1024;
 constexpr int64_t kPermuteMostBlocks = 64;
 // With more experts than this fewer waves of a block place its choices: smaller blocks.
 constexpr int64_t kPermuteManyExperts = 512;

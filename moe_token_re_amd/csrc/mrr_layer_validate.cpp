@@ -168,7 +168,7 @@ mrr_status check_token_permute(const mrr_token_permute_args* a, const void* ws, 
   if (a->expert_token_num == nullptr) return MRR_ERROR_INVALID_VALUE;
   const int64_t n = a->T * a->top_k;
   if (n > 0 && (a->tokens == nullptr || a->expert_ids == nullptr || a->permute_tokens == nullptr ||
-                a->permute_token_idx == nullptr || ws == nullptr ||
+                a->permute_token_idx == nullptr || (ws == nullptr && n > kPermuteSelfChoices) ||
                 (a->per_token_scales == nullptr) != (a->permute_per_token_scales == nullptr) ||
                 (a->expert_weight == nullptr) != (a->permute_topk_weight == nullptr)))
     return MRR_ERROR_INVALID_VALUE;
@@ -179,8 +179,8 @@ mrr_status check_token_permute(const mrr_token_permute_args* a, const void* ws, 
     return MRR_ERROR_MISALIGNED;
   if (scales && a->scales_dtype == MRR_F32 && (!aligned(a->per_token_scales, 4) || !aligned(a->permute_per_token_scales, 4)))
     return MRR_ERROR_MISALIGNED;
-  const size_t need = mrr_token_permute_workspace_size(a->T, a->top_k, a->E);
-  if (n > 0 && ws_bytes < need) return MRR_ERROR_WORKSPACE_TOO_SMALL;
+  const size_t need = n > kPermuteSelfChoices ? mrr_token_permute_workspace_size(a->T, a->top_k, a->E) : 0;
+  if (ws_bytes < need) return MRR_ERROR_WORKSPACE_TOO_SMALL;
   const int64_t row = permute_row_bytes(a), srow = permute_scale_bytes(a);
   Buffers s;
   s.add(a->tokens, a->T * row, false);
@@ -192,7 +192,7 @@ mrr_status check_token_permute(const mrr_token_permute_args* a, const void* ws, 
   s.add(a->permute_token_idx, n * 4, true);
   s.add(a->expert_token_num, a->E * 4, true);
   s.add(a->permute_topk_weight, n * 4, true);
-  if (n > 0) s.add(ws, static_cast<int64_t>(need), true);
+  s.add(ws, static_cast<int64_t>(need), true);
   return s.clash() ? MRR_ERROR_INVALID_VALUE : MRR_SUCCESS;
 }
 

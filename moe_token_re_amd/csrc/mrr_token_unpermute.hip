@@ -174,7 +174,8 @@ __device__ __forceinline__ void grad_choices(const GradArgs& a, size_t token, ui
   if (first > 0) __syncthreads();  // the choices before have been read from sh
 #pragma unroll
   for (int j = 0; j < kK; ++j) {
-    const float d = sum64_f32(dot[j]);
+    // without a row it is 0, whatever the gradient holds
+    const float d = static_cast<uint32_t>(idx[j]) < a.R ? sum64_f32(dot[j]) : 0.0f;
     if (tid % 64 == 0) sh[tid / 64][j] = d;
   }
   __syncthreads();
@@ -182,7 +183,7 @@ __device__ __forceinline__ void grad_choices(const GradArgs& a, size_t token, ui
     float d = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) d += sh[w][tid];
-    a.grad_weight[at + tid] = d;  // 0 where there is no row: none was added
+    a.grad_weight[at + tid] = d;
   }
 }
 

@@ -433,7 +433,8 @@ PyObject* permute(PyObject*, PyObject* const* args, Py_ssize_t n) {
     a.permute_topk_weight = static_cast<float*>(out_weight.data_ptr());
   }
   at::Tensor rows = c.empty({T * k, tokens->size(1)}, tokens->scalar_type()), idx = c.empty({T, k}, at::kInt);
-  at::Tensor num = c.empty({E}, at::kInt), ws = c.empty({static_cast<int64_t>(bytes)}, at::kByte);
+  at::Tensor num = c.empty({E}, at::kInt), ws;
+  if (T * k > MRR_TOKEN_PERMUTE_ALONE) ws = c.empty({static_cast<int64_t>(bytes)}, at::kByte);
   a.tokens = tokens->data_ptr();
   a.tokens_dtype = code;
   a.T = T;
@@ -445,7 +446,7 @@ PyObject* permute(PyObject*, PyObject* const* args, Py_ssize_t n) {
   a.permute_token_idx = static_cast<int32_t*>(idx.data_ptr());
   a.expert_token_num = static_cast<int32_t*>(num.data_ptr());
   a.expert_token_num_type = type;
-  if (unlocked([&] { return mrr_token_permute(&a, ws.data_ptr(), bytes, c.stream()); }) != MRR_SUCCESS) return none();
+  if (unlocked([&] { return mrr_token_permute(&a, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? bytes : 0, c.stream()); }) != MRR_SUCCESS) return none();
   return result({&rows, &out_scales, &idx, &num, &out_weight});
   END_HANDLE_TH_ERRORS
 }

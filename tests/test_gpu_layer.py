@@ -500,6 +500,20 @@ def test_unpermute_passes_over_other_indices(H):
     assert moe.moe_token_unpermute_backward(torch.ones(2, H, device=dev), none, away)[0].shape == (0, H)
 
 
+@pytest.mark.parametrize("H", [24, 3000])
+def test_gradient_of_a_choice_that_is_not_here(H):
+    """It is 0, and so is its row's, whatever the gradient holds."""
+    dev = _dev()
+    up = torch.full((2, H), float("inf"), device=dev)
+    up[1] = float("nan")
+    index = torch.tensor([[0, -3, 7], [-2, -4, 1 << 30]], dtype=torch.int32, device=dev)
+    rows = torch.ones(4, H, device=dev)
+    d, dw = moe.moe_token_unpermute_backward(up, rows, index, expert_weight=torch.ones(2, 3, device=dev))
+    assert (d[1:] == 0).all() and (d[0] == float("inf")).all()
+    assert dw.tolist() == [[float("inf"), 0.0, 0.0], [0.0, 0.0, 0.0]]
+    assert (moe.moe_token_unpermute_backward(up, rows, index)[0][1:] == 0).all()
+
+
 @pytest.mark.parametrize("T,k,E,H,away", COMBINE[:8])
 def test_permute_backward(T, k, E, H, away):
     dev = _dev()

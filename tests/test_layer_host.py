@@ -141,7 +141,7 @@ NO_SCALES = {"per_token_scales": None, "permute_per_token_scales": None}
     ({"permute_token_idx": None}, VALUE), ({"expert_token_num": None}, VALUE), ({"per_token_scales": None}, VALUE),
     ({"permute_per_token_scales": None}, VALUE), ({"expert_weight": None}, VALUE), ({"permute_topk_weight": None}, VALUE),
     ({"permute_tokens": AT["tokens"] + 8}, VALUE), ({"permute_token_idx": AT["expert_ids"] + 4}, VALUE),
-    ({"expert_token_num": AT["ws"]}, VALUE), ({"permute_topk_weight": AT["permute_tokens"] + 4 * 8 * 256 - 4}, VALUE),
+    ({"permute_topk_weight": AT["permute_tokens"] + 4 * 8 * 256 - 4}, VALUE),
     ({"expert_ids": AT["expert_ids"] + 2}, MISALIGNED), ({"per_token_scales": AT["x"] + 2}, MISALIGNED),
     ({"tokens_dtype": _lib.F16, "tokens": AT["tokens"] + 1}, MISALIGNED), ({"tokens": AT["tokens"] + 1}, OK),
 ])
@@ -153,10 +153,14 @@ def test_permute_workspace():
     L = _lib.load()
     for T, k, E in ((0, 1, 1), (8, 4, 64), (100000, 16, 4096), (1 << 27, 8, 256)):
         need = L.mrr_token_permute_workspace_size(T, k, E)
-        assert 0 < need <= 256 + 4 * (32768 + E + 1) + 256
-    need = L.mrr_token_permute_workspace_size(8, 4, 64)
-    assert permute({}, ws_bytes=need) == OK and permute({}, ws_bytes=need - 1) == SMALL
-    assert permute({}, ws=None) == VALUE and permute({}, ws=AT["ws"] + 4) == MISALIGNED
+        assert 0 < need <= 256 + 4 * 64 * (E + 1) + 256
+    many = {"T": 4097, "scales_dims": (4097, 0, 0)}
+    need = L.mrr_token_permute_workspace_size(4097, 4, 64)
+    assert permute(many, ws_bytes=need) == OK and permute(many, ws_bytes=need - 1) == SMALL
+    assert permute(many, ws=None, ws_bytes=0) == VALUE and permute(many, ws=AT["ws"] + 4) == MISALIGNED
+    assert permute({**many, "expert_token_num": AT["ws"]}) == VALUE
+    alone = {"T": 4096, "scales_dims": (4096, 0, 0)}  # few choices use none
+    assert permute(alone, ws=None, ws_bytes=0) == OK and permute({}, ws=None, ws_bytes=0) == OK
     for bad in ((-1, 4, 64), (1 << 30, 4, 64), (8, 0, 64), (8, 17, 64), (8, 4, 0), (8, 4, 4097)):
         assert L.mrr_token_permute_workspace_size(*bad) == 0
 
