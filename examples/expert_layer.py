@@ -1,4 +1,8 @@
-"""A mixture-of-experts layer of 4-bit experts, the two ways a server runs it.
+"""A mixture-of-experts layer of 4-bit experts, the ways a server runs it.
+
+A layer on one device: rms_norm adds the residual and makes 4-bit rows,
+moe_router_top_k chooses experts, moe_token_permute sorts the tokens by them,
+mx_grouped_mm multiplies, and moe_token_unpermute sums the rows back by token.
 
 A batch: the rows that the all-to-all brought (ordered by source rank, then by
 expert) are microscaled 4-bit rows; moe_re_routing makes them expert-major,
@@ -32,6 +36,17 @@ def batch(rows, scales, counts, topk_weight, w):
     return moe.moe_re_routing_inverse(y, counts)[0]
 
 
+def layer(x, residual, norm_weight, router, top_k, w):
+    """One layer's output for x [T, H] bfloat16, and the residual stream behind it."""
+    rows, scales, residual = moe.rms_norm(x, norm_weight, residual=residual, quantize="mxfp4")
+    logits = moe.mx_dequantize(rows, scales) @ router
+    weight, ids = moe.moe_router_top_k(logits, top_k)
+    tokens, token_scales, index, expert_num, _ = moe.moe_token_permute(rows, ids, router.shape[1], per_token_scales=scales)
+    h = moe.mx_grouped_mm(tokens, token_scales, w["gate_up"], w["gate_up_scales"], expert_num, gated=True)
+    y = moe.mx_grouped_mm(*moe.mx_quantize(h), w["down"], w["down_scales"], expert_num)
+    return moe.moe_token_unpermute(y, index, expert_weight=weight), residual, (rows, scales, weight, ids)
+
+
 def plain(x, w, expert, weight):
     """The layer in plain operations, row by row's expert, from the 4-bit weights' values."""
     y = torch.zeros_like(x)
@@ -63,6 +78,15 @@ def main():
     w = {}
     w["gate_up"], w["gate_up_scales"] = weights(a.experts, 2 * a.inner, a.hidden)
     w["down"], w["down_scales"] = weights(a.experts, a.hidden, a.inner)
+
+    # a layer on one device
+    x, residual = (torch.empty(a.rows, a.hidden, device=dev).normal_(generator=g).to(torch.bfloat16) for _ in range(2))
+    router = torch.empty(a.hidden, a.experts, device=dev).normal_(0, a.hidden ** -0.5, generator=g).to(torch.bfloat16)
+    top_k = min(2, a.experts)
+    y, _, (rows, scales, weight, ids) = layer(x, residual, torch.ones(a.hidden, device=dev), router, top_k, w)
+    rows = moe.mx_dequantize(rows, scales, dtype=torch.float32)
+    want = sum(plain(rows, w, ids[:, j], weight[:, j]) for j in range(top_k))
+    print(f"layer of {a.rows} tokens: {relative(y, want):.3f} off the plain layer (its inner rows are 4-bit values)")
 
     # a batch: every row has come for one expert from one rank
     cell = torch.randint(a.ranks * a.experts, (a.rows,), device=dev, generator=g).sort()[0]

@@ -388,7 +388,7 @@ class _NoBinding:
 
     quantize = dequantize = grouped_mm = few_tokens = staticmethod(lambda *args: None)
     rms_norm = rms_norm_backward = router = router_backward = staticmethod(lambda *args: None)
-    permute = unpermute = unpermute_backward = staticmethod(lambda *args: None)
+    permute = permute_backward = unpermute = unpermute_backward = staticmethod(lambda *args: None)
 
 
 _plain_calls = None

@@ -475,6 +475,29 @@ PyObject* unpermute(PyObject*, PyObject* const* args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// permute_backward(grad_rows, permute_token_idx, grad_topk_weight)
+PyObject* permute_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (n != 3) return none();
+  Call c;
+  const at::Tensor* rows = c.take(args[0]);
+  const at::Tensor* idx = c.take(args[1]);
+  const at::Tensor* weight = c.take_optional(args[2]);
+  if (!c.ok || !sum_sizes(rows, idx, nullptr)) return none();
+  if (weight != nullptr && (weight->scalar_type() != at::kFloat || weight->dim() < 1 || weight->dim() > 2 ||
+                            weight->size(0) != rows->size(0) || weight->numel() != rows->size(0)))
+    return none();
+  at::Tensor grad = c.empty({idx->size(0), rows->size(1)}, rows->scalar_type()), grad_weight;
+  if (weight != nullptr) grad_weight = c.empty(idx->sizes(), at::kFloat);
+  const mrr_token_unpermute_args a{rows->data_ptr(), wide_code(rows->scalar_type()), rows->size(0), rows->size(1),
+                                   static_cast<const int32_t*>(idx->data_ptr()), idx->size(0), idx->size(1), nullptr,
+                                   grad.data_ptr(), static_cast<const float*>(ptr(weight)),
+                                   weight == nullptr ? nullptr : static_cast<float*>(grad_weight.data_ptr())};
+  if (unlocked([&] { return mrr_token_unpermute(&a, c.stream()); }) != MRR_SUCCESS) return none();
+  return result({&grad, &grad_weight});
+  END_HANDLE_TH_ERRORS
+}
+
 // unpermute_backward(grad, rows, permute_token_idx, expert_weight)
 PyObject* unpermute_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -513,6 +536,7 @@ PyMethodDef methods[] = {{"quantize", fast(quantize), METH_FASTCALL, nullptr},
                          {"router_backward", fast(router_backward), METH_FASTCALL, nullptr},
                          {"permute", fast(permute), METH_FASTCALL, nullptr},
                          {"unpermute", fast(unpermute), METH_FASTCALL, nullptr},
+                         {"permute_backward", fast(permute_backward), METH_FASTCALL, nullptr},
                          {"unpermute_backward", fast(unpermute_backward), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 

@@ -362,6 +362,10 @@ def moe_token_permute_backward(grad_rows: torch.Tensor, permute_token_idx: torch
     grad_topk_weight [A, 1] or [A] float32 permute_topk_weight's. Returns (grad_tokens
     [T, H]: the sum of a token's rows, grad_expert_weight [T, top_k] or None); choices
     that were not here have no part in either."""
+    if out is None:
+        done = _lib.plain_calls().permute_backward(grad_rows, permute_token_idx, grad_topk_weight)
+        if done is not None:
+            return done
     dev = _gpu("grad_rows", grad_rows)
     R, H = _rows("grad_rows", grad_rows, dev)
     T, k = _index(permute_token_idx, dev)

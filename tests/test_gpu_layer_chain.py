@@ -2,6 +2,8 @@
 re-routing and the experts' operators: a whole layer of 4-bit experts for a
 batch, the way over several ranks, a training step's gradients, and the calls
 that are refused."""
+import os
+import sys
 import zlib
 
 import layer_reference as ref
@@ -211,3 +213,15 @@ def test_refusals():
             call()
             pytest.fail(f"type {n}")
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("sizes", [[], ["--rows", "37", "--experts", "3", "--hidden", "64", "--inner", "32"]])
+def test_the_example_runs(sizes, monkeypatch, capsys):
+    _dev()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    monkeypatch.syspath_prepend(os.path.join(root, "examples"))
+    monkeypatch.setattr(sys, "argv", ["expert_layer.py", *sizes])
+    import expert_layer
+
+    expert_layer.main()
+    assert capsys.readouterr().out.count("off the plain layer") == 3

@@ -239,7 +239,8 @@ def test_binding_leaves_cpu_tensors_alone():
     assert b.rms_norm(x, w, None, 1e-6, None) is None and b.rms_norm_backward(x, x, w, None, 1e-6) is None
     assert b.router(x, 2, True) is None and b.router_backward(x, x, x, i, True) is None
     assert b.permute(x, i, 4, None, None, 1) is None and b.unpermute(x, i, None) is None
-    assert b.unpermute_backward(x, x, i, None) is None
-    for call in (b.rms_norm, b.rms_norm_backward, b.router, b.router_backward, b.permute, b.unpermute, b.unpermute_backward):
+    assert b.unpermute_backward(x, x, i, None) is None and b.permute_backward(x, i, None) is None
+    for call in (b.rms_norm, b.rms_norm_backward, b.router, b.router_backward, b.permute, b.permute_backward, b.unpermute,
+                 b.unpermute_backward):
         for n in range(8):
             assert call(*[None] * n) is None
