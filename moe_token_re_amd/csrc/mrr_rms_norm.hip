@@ -13,8 +13,12 @@
 // exact in one fma, so the rounding to 8 bits is that of the exact quotient, ties
 // included, for three instructions a value instead of a division.
 //
-// Rows whose sum of squares or largest product leave the range of 32 bits (or
-// are not finite) are taken again in 64 bits, which their workgroup alone pays for.
+// Other values with few bits are rounded from 32-bit numbers that are off by less than
+// kDoubt of themselves. Where a number so much smaller and one so much larger are rounded
+// otherwise, which is in about one row of 7168 values of seven, the row is taken again in
+// 64 bits, whose roundings to 32 on the way keep on which side of a border a number lay.
+// So is a row whose sum of squares or largest product leaves the range of 32 bits, or is
+// not finite.
 #include "mrr_rows.h"
 
 namespace mrr {
@@ -42,6 +46,35 @@ struct NormArgs {
 constexpr float kMostSum = 1e37f, kLeastSum = 1e-30f, kLeastTop = 1e-30f, kMostTop = 1e35f;
 // A sum of squares below kLeastSum is nothing next to an eps from here on.
 constexpr float kLeastEps = 1e-20f;
+
+// What a 32-bit y (or a product over the largest) may be off by: the sum of squares has at
+// most 4 additions a lane and column, 3 over the columns, 6 over a wave, 4 over waves, and
+// half of that counts; the mean, root, reciprocal, two products and a quotient 6 more: 15
+// roundings of 2^-24.
+constexpr float kDoubt = 0x1p-20f;
+
+// The nearer of 32 bits' neighbours towards 0, its last bit set, where d is none of them:
+// a rounding of it to fewer bits is then that of d.
+__device__ __forceinline__ float to_odd(double d) {
+  const float f = static_cast<float>(d);
+  const double back = static_cast<double>(f);
+  if (back == d || !(fabsf(f) < INFINITY)) return f;
+  const uint32_t b = __float_as_uint(f) - (fabs(back) > fabs(d) ? 1u : 0u);
+  return __uint_as_float(b | 1u);
+}
+
+// The sum, or the largest, of a row's waves.
+template <int kWaves, typename T, typename F>
+__device__ __forceinline__ T join(const T (&sh)[kWaves], F&& f) {
+  T v[kWaves];
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) v[i] = sh[i];
+#pragma unroll
+  for (int d = kWaves / 2; d > 0; d /= 2)
+#pragma unroll
+    for (int i = 0; i < d; ++i) v[i] = f(v[i], v[i + d]);
+  return v[0];
+}
 
 template <int kLanes>
 struct Shared {
@@ -115,164 +148,179 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
     }
   }
 
-  float sum = 0.0f;
+  constexpr int kWaves = kLanes / 64;
+  const auto add_f = [](auto x, auto y) { return x + y; };
+  float column[8] = {};
   uint32_t top = 0;  // |p| by its bits, so that infinities and NaN come above every number
 #pragma unroll
   for (int i = 0; i < kUnits; ++i)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float v = s[i].get(k);
-      sum = __builtin_fmaf(v, v, sum);
+      column[k] = __builtin_fmaf(v, v, column[k]);
       if constexpr (kOut == kRow) top = max(top, __float_as_uint(v * w[i].get(k)) & 0x7fffffffu);
     }
 #pragma unroll
   for (int i = 0; i < kUnits; ++i) s[i].keep_packed(), w[i].keep_packed();
-  sum = sum64_f32(sum);
+  float sum = sum64_f32(((column[0] + column[1]) + (column[2] + column[3])) +
+                        ((column[4] + column[5]) + (column[6] + column[7])));
   if constexpr (kOut == kRow) top = max64_u32(top);
   __shared__ Shared<kLanes> sh;
-  if constexpr (kLanes > 64) {
+  if constexpr (kWaves > 1) {
     if (threadIdx.x % 64 == 0) {
       sh.sum[threadIdx.x / 64] = sum;
       if constexpr (kOut == kRow) sh.top[threadIdx.x / 64] = top;
     }
     __syncthreads();
-    sum = 0.0f, top = 0;
-#pragma unroll
-    for (int v = 0; v < kLanes / 64; ++v) {
-      sum += sh.sum[v];
-      if constexpr (kOut == kRow) top = max(top, sh.top[v]);
-    }
+    sum = join(sh.sum, add_f);
+    if constexpr (kOut == kRow) top = join(sh.top, [](uint32_t x, uint32_t y) { return max(x, y); });
   }
 
-  // the same for all lanes of a row
-  float most = __uint_as_float(top);
-  const bool plain = sum <= kMostSum && (sum >= kLeastSum || a.eps >= kLeastEps) &&
-                     (kOut != kRow || top == 0 || (most >= kLeastTop && most <= kMostTop));
-  float r = 1.0f / __builtin_sqrtf(__builtin_fmaf(sum, a.inv_h, a.eps));
-  double r64 = 0.0, most64 = 0.0;
-  bool bad = false;  // a row with one scale and a product that is not finite
-  if (!plain) {
-    double sum64 = 0.0;
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const double v = s[i].get(k);
-        sum64 += v * v;
-        if constexpr (kOut == kRow) {
-          const double p = fabs(v * static_cast<double>(w[i].get(k)));
-          most64 = p <= 1e300 ? fmax(most64, p) : 1e301;  // 32-bit numbers' products are below 1e78
-        }
-      }
-    sum64 = sum64_f64(sum64);
-    if constexpr (kOut == kRow) most64 = max64_f64(most64);
-    if constexpr (kLanes > 64) {
-      if (threadIdx.x % 64 == 0) {
-        sh.sum64[threadIdx.x / 64] = sum64;
-        sh.top64[threadIdx.x / 64] = most64;
-      }
-      __syncthreads();
-      sum64 = 0.0;
-#pragma unroll
-      for (int v = 0; v < kLanes / 64; ++v) {
-        sum64 += sh.sum64[v];
-        most64 = fmax(most64, sh.top64[v]);
-      }
-    }
-    r64 = 1.0 / sqrt(sum64 / a.H + a.eps64);
-    bad = most64 > 1e300;
-  }
-
-  if constexpr (kOut == kRow) {
-    const float full = a.narrow == MRR_I8 ? 127.0f : 448.0f;
-    if (lane == 0) {
-      const float scale = bad      ? __builtin_nanf("")
-                          : !plain ? static_cast<float>(r64 * most64 / full)
-                                   : r * (most / full);
-      __builtin_memcpy(a.scales + static_cast<size_t>(row) * 4, &scale, 4);
-    }
-    const float over = top == 0 ? 0.0f : 1.0f / most;
+  // Writes a row of values that value(i, k) gives: y, or with one scale y over it. Whether
+  // one might be rounded otherwise than its exact number.
+  const float full = a.narrow == MRR_I8 ? 127.0f : 448.0f;
+  const auto write = [&](auto guarded, auto&& value) {
+    constexpr bool kGuarded = decltype(guarded)::value;
+    constexpr float kLess = kGuarded ? 1.0f - kDoubt : 1.0f, kMore = 1.0f + kDoubt;
+    bool doubt = false;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const uint32_t col = col_of(i);
-      if (col >= a.H) break;
-      float q[8];
+      float v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float p = full * (s[i].get(k) * w[i].get(k));
-        const float q0 = p * over;
-        q[k] = __builtin_fmaf(__builtin_fmaf(-q0, most, p), over, q0);
-      }
-      if (!plain) {
+      for (int k = 0; k < 8; ++k) v[k] = value(i, k);
+      if constexpr (kOut == kWide) {
+        Eight<kX> out;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const double p = static_cast<double>(s[i].get(k)) * static_cast<double>(w[i].get(k));
-          q[k] = bad || most64 == 0.0 ? 0.0f : static_cast<float>(full * p / most64);
-        }
-      }
-      const uint64_t lo = a.narrow == MRR_I8 ? pack_i8(q[0], q[1], q[2], q[3]) : pack_e4m3(q[0], q[1], q[2], q[3]);
-      const uint64_t hi = a.narrow == MRR_I8 ? pack_i8(q[4], q[5], q[6], q[7]) : pack_e4m3(q[4], q[5], q[6], q[7]);
-      store_bytes(a.y + first + col, lo | hi << 32, static_cast<int>(min(8u, a.H - col)));
-    }
-    return;
-  }
-
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const uint32_t col = col_of(i);
-    float y[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = s[i].get(k) * r * w[i].get(k);
-    if (!plain) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        y[k] = static_cast<float>(static_cast<double>(s[i].get(k)) * r64 * static_cast<double>(w[i].get(k)));
-    }
-    if constexpr (kOut == kWide) {
-      Eight<kX> out;
-#pragma unroll
-      for (int k = 0; k < 8; k += 2) out.put(k / 2, y[k], y[k + 1]);
-      store(a.y, i, out);
-    } else {
-      uint32_t m = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(y[k]) & 0x7fffffffu);
-      m = max(m, dpp_u32<kDppXor1>(m));
-      m = max(m, dpp_u32<kDppXor2>(m));  // of the block's four lanes
-      const uint32_t e = m >> 23, least = a.narrow == MRR_F4_E2M1 ? 2 : 8;
-      const uint32_t scale = e == 255 ? 255 : e > least ? e - least : 0;
-      if (scale == 255) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] = 0.0f;
-      }
-      const uint32_t scale_row = 2 * ((a.H + 63) / 64);
-      if (lane % 4 == 0 && col / 32 < scale_row)
-        a.scales[static_cast<size_t>(row) * scale_row + col / 32] = static_cast<uint8_t>(scale);
-      if (col >= a.H) continue;
-      const int n = static_cast<int>(min(8u, a.H - col));
-      if (a.narrow == MRR_F4_E2M1) {
-        const float by = two_to(scale == 255 ? 127 : scale);
-        uint32_t c = 0;
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[0], y[1], by, 0);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[2], y[3], by, 1);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[4], y[5], by, 2);
-        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, y[6], y[7], by, 3);
-        uint8_t* p = a.y + (first + col) / 2;
-        if (n == 8) {
-          __builtin_memcpy(p, &c, 4);
-        } else {
-          for (int k = 0; k < n / 2; ++k) p[k] = static_cast<uint8_t>(c >> (8 * k));
-        }
+        for (int k = 0; k < 8; k += 2) out.put(k / 2, v[k], v[k + 1]);
+        store(a.y, i, out);
       } else {
-        // a block's values over its scale are below 512
-        const float by = two_to(scale == 255 ? 127 : 254 - scale);
-        float q[8];
+        const auto bytes = [&](float by) {
+          const bool i8 = kOut == kRow && a.narrow == MRR_I8;
+          const uint64_t lo = i8 ? pack_i8(v[0] * by, v[1] * by, v[2] * by, v[3] * by)
+                                 : pack_e4m3(v[0] * by, v[1] * by, v[2] * by, v[3] * by);
+          const uint64_t hi = i8 ? pack_i8(v[4] * by, v[5] * by, v[6] * by, v[7] * by)
+                                 : pack_e4m3(v[4] * by, v[5] * by, v[6] * by, v[7] * by);
+          return lo | hi << 32;
+        };
+        if constexpr (kOut == kMx) {
+          uint32_t m = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) q[k] = __builtin_amdgcn_fmed3f(y[k] * by, -448.0f, 448.0f);
-        const uint64_t lo = pack_e4m3(q[0], q[1], q[2], q[3]), hi = pack_e4m3(q[4], q[5], q[6], q[7]);
-        store_bytes(a.y + first + col, lo | hi << 32, n);
+          for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(v[k]) & 0x7fffffffu);
+          m = max(m, dpp_u32<kDppXor1>(m));
+          m = max(m, dpp_u32<kDppXor2>(m));  // of the block's four lanes
+          const uint32_t e = __float_as_uint(__uint_as_float(m) * kLess) >> 23;
+          if constexpr (kGuarded) doubt = doubt || e != __float_as_uint(__uint_as_float(m) * kMore) >> 23;
+          const uint32_t least = a.narrow == MRR_F4_E2M1 ? 2 : 8;
+          const uint32_t scale = e == 255 ? 255 : e > least ? e - least : 0;
+          const uint32_t scale_row = 2 * ((a.H + 63) / 64);
+          if (lane % 4 == 0 && col / 32 < scale_row)
+            a.scales[static_cast<size_t>(row) * scale_row + col / 32] = static_cast<uint8_t>(scale);
+          if (a.narrow == MRR_F4_E2M1) {
+            const float unit = two_to(scale == 255 ? 127 : scale);
+            const auto codes = [&](float by) {
+              uint32_t c = 0;
+              c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[0] * by, v[1] * by, unit, 0);
+              c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[2] * by, v[3] * by, unit, 1);
+              c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[4] * by, v[5] * by, unit, 2);
+              return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, v[6] * by, v[7] * by, unit, 3);
+            };
+            if (scale == 255) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+            }
+            const uint32_t c = codes(kLess);
+            if constexpr (kGuarded) doubt = doubt || c != codes(kMore);
+            uint8_t* p = a.y + (first + col) / 2;
+            const int n = col < a.H ? static_cast<int>(min(8u, a.H - col)) : 0;
+            if (n == 8) {
+              __builtin_memcpy(p, &c, 4);
+            } else {
+              for (int k = 0; k < n / 2; ++k) p[k] = static_cast<uint8_t>(c >> (8 * k));
+            }
+            continue;
+          }
+          // a block's values over its scale are below 512, and those over 448 end there
+          const float by = two_to(scale == 255 ? 127 : 254 - scale);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = scale == 255 ? 0.0f : __builtin_amdgcn_fmed3f(v[k] * by, -448.0f, 448.0f);
+        }
+        const uint64_t out = bytes(kLess);
+        if constexpr (kGuarded) doubt = doubt || out != bytes(kMore);
+        if (col < a.H) store_bytes(a.y + first + col, out, static_cast<int>(min(8u, a.H - col)));
       }
     }
+    return doubt;
+  };
+
+  // the same for all lanes of a row
+  const float most = __uint_as_float(top);
+  const bool plain = sum <= kMostSum && (sum >= kLeastSum || a.eps >= kLeastEps) &&
+                     (kOut != kRow || top == 0 || (most >= kLeastTop && most <= kMostTop));
+  constexpr bool kExact = kOut == kWide || (kOut == kRow && kX == MRR_BF16 && kW == MRR_BF16);
+  bool doubt = false;
+  if (plain) {
+    const float r = 1.0f / __builtin_sqrtf(__builtin_fmaf(sum, a.inv_h, a.eps));
+    if constexpr (kOut == kRow) {
+      if (lane == 0) {
+        const float scale = r * (most / full);
+        __builtin_memcpy(a.scales + static_cast<size_t>(row) * 4, &scale, 4);
+      }
+      const float over = top == 0 ? 0.0f : 1.0f / most;
+      doubt = write(std::bool_constant<!kExact>{}, [&](int i, int k) {
+        const float p = full * (s[i].get(k) * w[i].get(k)), q0 = p * over;
+        return __builtin_fmaf(__builtin_fmaf(-q0, most, p), over, q0);
+      });
+    } else {
+      doubt = write(std::bool_constant<!kExact>{}, [&](int i, int k) { return s[i].get(k) * r * w[i].get(k); });
+    }
+  }
+  if constexpr (!kExact) doubt = kWaves > 1 ? __syncthreads_or(doubt) != 0 : __any(doubt) != 0;
+  if (plain && !doubt) return;
+
+  double sum64 = 0.0, most64 = 0.0;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const double v = s[i].get(k);
+      sum64 += v * v;
+      if constexpr (kOut == kRow) {
+        const double p = fabs(v * static_cast<double>(w[i].get(k)));
+        most64 = p <= 1e300 ? fmax(most64, p) : 1e301;  // 32-bit numbers' products are below 1e78
+      }
+    }
+  sum64 = sum64_f64(sum64);
+  if constexpr (kOut == kRow) most64 = max64_f64(most64);
+  if constexpr (kWaves > 1) {
+    if (threadIdx.x % 64 == 0) {
+      sh.sum64[threadIdx.x / 64] = sum64;
+      sh.top64[threadIdx.x / 64] = most64;
+    }
+    __syncthreads();
+    sum64 = join(sh.sum64, add_f);
+    if constexpr (kOut == kRow) most64 = join(sh.top64, [](double x, double y) { return fmax(x, y); });
+  }
+  const double r64 = 1.0 / sqrt(sum64 / a.H + a.eps64);
+  if constexpr (kOut == kRow) {
+    const bool bad = most64 > 1e300;  // a product that is not finite
+    if (lane == 0) {
+      const float scale = bad ? __builtin_nanf("") : static_cast<float>(r64 * most64 / full);
+      __builtin_memcpy(a.scales + static_cast<size_t>(row) * 4, &scale, 4);
+    }
+    const double inverse = 1.0 / most64, over = bad || most64 == 0.0 ? 0.0 : full * inverse;
+    write(std::false_type{}, [&](int i, int k) {
+      const double p = static_cast<double>(s[i].get(k)) * static_cast<double>(w[i].get(k));
+      if (over == 0.0) return 0.0f;
+      // the quotient by one more step of its division: what is a border is one exactly
+      const double q0 = p * over, q = fma(fma(-q0, most64, full * p), inverse, q0);
+      return to_odd(q);
+    });
+  } else {
+    write(std::false_type{}, [&](int i, int k) {
+      const double y = static_cast<double>(s[i].get(k)) * r64 * static_cast<double>(w[i].get(k));
+      return kOut == kMx ? to_odd(y) : static_cast<float>(y);
+    });
   }
 }
 
