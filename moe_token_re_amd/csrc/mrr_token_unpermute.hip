@@ -120,6 +120,9 @@ struct GradArgs {
 // Choices [first, first + kK) of a token, of which those below k exist.
 template <int kDtype, int kK, int kWaves, int kHow>
 __device__ __forceinline__ void grad_choices(const GradArgs& a, size_t token, uint32_t first, float (&sh)[kWaves][kK]) {
+  // two products of fp16 values are not to become one instruction, which has another
+  // rounding and no subnormal numbers
+#pragma clang fp contract(off)
   using U = Unit16<kDtype>;
   constexpr uint32_t kN = 16 / U::kBytes;
   const uint32_t tid = threadIdx.x;
