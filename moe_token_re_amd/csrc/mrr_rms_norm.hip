@@ -5,7 +5,9 @@
 //   s = round(x + residual);  y = w s / sqrt(mean(s^2) + eps)
 //
 // Bound by memory: a row is read once, kept in registers as it lies there, and
-// written once. Rows of 8-bit values with one scale need two numbers of a row,
+// written once (16384 x 7168 bf16 with a residual to fp8 rows: 123 us, 6.7 TB/s of 823 MB,
+// where a plain copy reaches 5.0; with the values kept wide over the sums, and half as many
+// waves, 138). Rows of 8-bit values with one scale need two numbers of a row,
 // sum(s^2) and max |p|, p = w s; both are found in one pass over the registers and
 // one barrier, since the norm cancels in the values: y / scale = 127 p / max |p|.
 // Of bf16 weights and values p is exact in 32 bits, and so is 127 p (448 p); the
@@ -356,8 +358,10 @@ void launch_types(const NormArgs& a, int out, NormShape s, hipStream_t stream) {
 
 // A launch holds less than 2^32 threads.
 constexpr int64_t kRowsPerLaunch = int64_t(1) << 21;
-// From so many bytes of rows on they are read, and written, past the caches.
-constexpr int64_t kStreamBytes = int64_t(64) << 20;
+// From so many bytes of rows on, with which the eight L2 are full, they are read, and
+// written, past the caches. Rows of 14 KiB with their sum, to fp8 rows: 22 MB take 16.8 us
+// through the caches and 17.6 past them, 34 MB 25.1 and 24.0, 50 MB 39.8 and 32.1.
+constexpr int64_t kStreamBytes = int64_t(24) << 20;
 
 }  // namespace
 }  // namespace mrr

@@ -5,10 +5,16 @@
 // whose workgroups find their own token's rows, each the number of choices before it in
 // the order of (expert, place), by comparing all choices with it (a ballot and a count
 // for 64 of them). Many: blocks of choices are counted by expert, then placed (every
-// block adds up the blocks before it), and the rows follow the index.
+// block adds up the blocks before it), and the rows follow the index. In between blocks
+// count all choices by themselves.
 //
 // Rows move in units of 16 bytes at any alignment; the last unit of a row that is no
-// whole number of them begins earlier, so that two lanes write the same bytes twice.
+// whole number of them begins earlier, so that two lanes write the same bytes twice. A
+// wave holds 1 KiB of a token and writes it top_k times: 16384 tokens of 7168 bytes and
+// their scales, 8 choices each, move in 205 us, 5.3 TB/s (a plain copy of 1 GiB: 5.0);
+// waves that write an output row's 1 KiB each and read it anew take 258 to 390, workgroups
+// of whole rows, two KiB a wave and waves that stay as long as this. With the sort 223 us;
+// one token 3.6 us of kernel.
 #include "mrr_rows.h"
 
 namespace mrr {
@@ -124,10 +130,6 @@ constexpr int kFewThreads = 256;
 constexpr int kFewWaves = kFewThreads / 64;
 // A workgroup moves so many units of a token's row.
 constexpr uint32_t kFewUnits = kFewThreads;
-// Up to so many choices every wave compares all of them with its own, without a barrier.
-constexpr uint32_t kFewAlone = 256;
-// Up to so many of them, and so many experts, are counted without LDS.
-constexpr uint32_t kFewest = 64, kFewestExperts = 1024;
 
 // kK: at least top_k.
 template <int kK>
@@ -137,19 +139,6 @@ __global__ __launch_bounds__(kFewThreads) void permute_few_kernel(SortArgs a, Ro
   const uint32_t tid = threadIdx.x, lane = tid % 64, wave = tid / 64, token = blockIdx.y;
   if (token == a.T) {  // the last workgroup counts
     if (blockIdx.x != 0) return;
-    if (a.n <= kFewest && a.E <= kFewestExperts) {
-      // every thread its own experts' choices, or those up to them, one choice at a time
-      const uint32_t mine = lane < a.n ? static_cast<uint32_t>(a.ids[lane]) : a.E;
-      for (uint32_t e = tid; e < a.E; e += kFewThreads) {
-        uint32_t c = 0;
-        for (uint32_t i = 0; i < a.n; ++i) {
-          const uint32_t id = __builtin_amdgcn_readlane(mine, i);
-          c += a.cumsum ? id <= e : id == e;
-        }
-        a.num[e] = static_cast<int32_t>(c);
-      }
-      return;
-    }
     for (uint32_t e = tid; e < a.E; e += kFewThreads) sh[e] = 0;
     __syncthreads();
     for (uint32_t i = tid; i < a.n; i += kFewThreads) {
@@ -169,8 +158,7 @@ __global__ __launch_bounds__(kFewThreads) void permute_few_kernel(SortArgs a, Ro
   const float weight = writes && a.weight != nullptr ? a.weight[first + tid] : 0.0f;
   // (expert, place) as one number; a token's own are read by the lanes with all the rest
   const auto number = [&](int32_t id, uint32_t i) { return expert_of(id, a.E) * a.n + i; };
-  const bool alone = a.n <= kFewAlone;
-  uint32_t i = (alone ? 0 : 64 * wave) + lane;
+  uint32_t i = 64 * wave + lane;  // every wave compares its part of all choices with the token's own
   const int32_t own_id = lane < a.k ? a.ids[first + lane] : 0;
   int32_t id = i < a.n ? a.ids[i] : 0;
   const uint32_t own_number = lane < a.k ? number(own_id, first + lane) : 0;
@@ -182,22 +170,20 @@ __global__ __launch_bounds__(kFewThreads) void permute_few_kernel(SortArgs a, Ro
   }
   while (i - lane < a.n) {
     const uint32_t c = i < a.n ? number(id, i) : 0xffffffffu;
-    i += alone ? 64 : kFewThreads;
+    i += kFewThreads;
     id = i < a.n ? a.ids[i] : 0;
 #pragma unroll
     for (uint32_t j = 0; j < kK; ++j) row[j] += static_cast<uint32_t>(__popcll(__ballot(c < own[j])));
   }
-  if (!alone) {
 #pragma unroll
-    for (uint32_t j = 0; j < kK; ++j)
-      if (lane == 0) sh_before[wave][j] = row[j];
-    __syncthreads();
+  for (uint32_t j = 0; j < kK; ++j)
+    if (lane == 0) sh_before[wave][j] = row[j];
+  __syncthreads();
 #pragma unroll
-    for (uint32_t j = 0; j < kK; ++j) {
-      row[j] = 0;
+  for (uint32_t j = 0; j < kK; ++j) {
+    row[j] = 0;
 #pragma unroll
-      for (int w = 0; w < kFewWaves; ++w) row[j] += sh_before[w][j];
-    }
+    for (int w = 0; w < kFewWaves; ++w) row[j] += sh_before[w][j];
   }
   const uint32_t away = a.E * a.n;
 #pragma unroll
@@ -275,15 +261,19 @@ __global__ __launch_bounds__(kSortThreads) void permute_place_kernel(SortArgs a)
   // Of an expert: all its choices, those of the blocks before this one, and each run's.
   if constexpr (kSelf) {
     const uint32_t to = min(a.n, from + a.block);
-    const auto count = [&](uint32_t i, uint32_t e, uint32_t n) {
-      atomicAdd(&total[e], n);
-      if (i < from)
-        atomicAdd(&start[e], n);
-      else if (i < to)
-        atomicAdd(&at[(i - from) / run * width + e], n);
+    const auto count = [&](uint32_t i, uint32_t e, uint32_t n) {  // in total only those behind, for now
+      uint32_t* counts = i < from ? start : i < to ? at + (i - from) / run * width : total;
+      atomicAdd(&counts[e], n);
     };
     each_choice<kSortThreads>(a, wave * 64, a.n, [&](uint32_t i, uint32_t e) { count(i, e, 1); },
                               [&](uint32_t i, uint32_t n) { count(i, a.E, n); });  // 64 of them, in one run
+    __syncthreads();
+    for (uint32_t e = tid; e < width; e += kSortThreads) {
+      uint32_t all = total[e] + start[e];
+#pragma unroll
+      for (uint32_t w = 0; w < kRuns; ++w) all += at[w * width + e];
+      total[e] = all;
+    }
   } else {
     constexpr uint32_t kShare = kSortThreads / 64 / kRuns;  // waves of a run
     const uint32_t begin = from + wave / kShare * run;
@@ -439,9 +429,6 @@ __global__ __launch_bounds__(256) void move_short_rows_kernel(MoveArgs a, Rows r
 
 // Tokens of a launch whose grid's second dimension they are, with the scales' rows of workgroups.
 constexpr uint32_t kMostGridY = 32767;
-// Outputs of so many bytes are written past the caches, which would not hold them.
-constexpr int64_t kStreamBytes = int64_t(64) << 20;
-
 template <bool kStream>
 void move_all(const MoveArgs& all, Rows r, Rows scales, hipStream_t stream) {
   if (scales.units > 64 || (r.units <= 64 && r.units + scales.units > 64)) {  // each by itself
@@ -472,7 +459,10 @@ void move_all(const MoveArgs& all, Rows r, Rows scales, hipStream_t stream) {
 // scales: of no units where there are none.
 void move_both(const Rows& r, const Rows& scales, const int32_t* idx, int64_t T, int64_t k, int64_t R, hipStream_t stream) {
   const MoveArgs a{idx, static_cast<uint32_t>(T), static_cast<uint32_t>(k), static_cast<uint32_t>(R)};
-  if (R * r.bytes >= kStreamBytes && whole_units(r.bytes, r.dst))
+  // Aligned rows are written past the caches: 16384 rows of 14 KiB, 235 MB, take 53.6 us so
+  // and 61 through them, 8192 rows of 2 KiB 11.0 and 12.6. The largest lose a little by it:
+  // 131072 rows of 7 KiB, 940 MB, 216 us so and 212 through them.
+  if (whole_units(r.bytes, r.dst))
     move_all<true>(a, r, scales, stream);
   else
     move_all<false>(a, r, scales, stream);
