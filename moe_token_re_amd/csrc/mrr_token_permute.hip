@@ -175,35 +175,32 @@ __global__ __launch_bounds__(kFewThreads) void permute_few_kernel(SortArgs a, Ro
 #pragma unroll
     for (uint32_t j = 0; j < kK; ++j) row[j] += static_cast<uint32_t>(__popcll(__ballot(c < own[j])));
   }
+  uint32_t mine = 0;  // lane j: the row of choice j
 #pragma unroll
-  for (uint32_t j = 0; j < kK; ++j)
-    if (lane == 0) sh_before[wave][j] = row[j];
+  for (uint32_t j = 0; j < kK; ++j) mine = lane == j ? row[j] : mine;
+  if (lane < kK) sh_before[wave][lane] = mine;
   __syncthreads();
+  mine = 0;
 #pragma unroll
-  for (uint32_t j = 0; j < kK; ++j) {
-    row[j] = 0;
-#pragma unroll
-    for (int w = 0; w < kFewWaves; ++w) row[j] += sh_before[w][j];
+  for (int w = 0; w < kFewWaves; ++w) mine += sh_before[w][lane % kK];
+  const uint64_t gone = __ballot(own_number >= a.E * a.n);
+  if (writes) {
+    const bool zero = gone >> tid & 1;
+    a.idx[first + tid] = static_cast<int32_t>(zero ? ~mine : mine);
+    if (a.weight != nullptr) a.out_weight[mine] = zero ? 0.0f : weight;
   }
-  const uint32_t away = a.E * a.n;
-#pragma unroll
-  for (uint32_t j = 0; j < kK; ++j) {
-    if (j < a.k) {
-      const bool zero = own[j] >= away;
-      if (moves) u.store(tokens, row[j], zero);
-      if (moves_scales) s.store(scales, row[j], zero);
-      if (writes && tid == j) {
-        a.idx[first + j] = static_cast<int32_t>(zero ? ~row[j] : row[j]);
-        if (a.weight != nullptr) a.out_weight[row[j]] = zero ? 0.0f : weight;
-      }
-    }
+#pragma unroll 1
+  for (uint32_t j = 0; j < a.k; ++j) {
+    const uint32_t to = __builtin_amdgcn_readlane(mine, j);
+    const bool zero = gone >> j & 1;
+    if (moves) u.store(tokens, to, zero);
+    if (moves_scales) s.store(scales, to, zero);
   }
   if (blockIdx.x != 0) return;
   for (uint32_t more = tid + kFewThreads; more < scales.units; more += kFewThreads) {
     s.load(scales, token, more);
-#pragma unroll
-    for (uint32_t j = 0; j < kK; ++j)
-      if (j < a.k) s.store(scales, row[j], own[j] >= away);
+#pragma unroll 1
+    for (uint32_t j = 0; j < a.k; ++j) s.store(scales, __builtin_amdgcn_readlane(mine, j), gone >> j & 1);
   }
 }
 
