@@ -57,11 +57,12 @@ inline int64_t norm_backward_groups(int64_t rows, int64_t H) {
 // Few choices are sorted by every workgroup of one kernel by itself; more in blocks,
 // whose counts by expert [blocks, E + 1] lie in the workspace. Every block reads all
 // counts, so the blocks stay few.
-// (Tokens of 4 KiB, 8 choices each: 512 by the one kernel 11.3 us and by blocks 13.2, 1024
-// 22.9 and 16.1.)
+// (8 choices a token: 512 tokens of 4 KiB by the one kernel 11.1 us and by blocks 10.7, of
+// 128 bytes 9.6 and 11.2; 1024 of 4 KiB 23.0 and 13.9.)
 constexpr int64_t kPermuteFewChoices = 4096;
-// Up to so many choices the blocks are small and count all choices by themselves (8192: 14.2
-// us and by the counts 17.3, 16384: 16.6 and 17.2, 32768: 24.4 and 19.0).
+// Up to so many choices the blocks are small and count all choices by themselves (rows of
+// 128 bytes, us so and by the counts: 8192 choices 11.7 and 15.2, 16384 13.2 and 15.6, 32768
+// 16.6 and 16.3).
 constexpr int64_t kPermuteSelfChoices = MRR_TOKEN_PERMUTE_ALONE, kPermuteSelfBlock = 1024;
 constexpr int64_t kPermuteMostBlocks = 64;
 // With more experts than this fewer waves of a block place its choices: smaller blocks

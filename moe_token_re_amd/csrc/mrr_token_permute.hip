@@ -426,6 +426,12 @@ __global__ __launch_bounds__(256) void move_short_rows_kernel(MoveArgs a, Rows r
 
 // Tokens of a launch whose grid's second dimension they are, with the scales' rows of workgroups.
 constexpr uint32_t kMostGridY = 32767;
+// Aligned rows are written past the caches: 16384 rows of 14 KiB, 235 MB, take 53.6 us so
+// and 61 through them, 8192 rows of 2 KiB 11.0 and 12.6. From so many bytes on it is the
+// other way round: 131072 rows of 7 KiB, 940 MB, 216 us past them and 212 through them,
+// 98304 rows, 704 MB, 153 and 156.
+constexpr int64_t kThroughBytes = int64_t(768) << 20;
+
 template <bool kStream>
 void move_all(const MoveArgs& all, Rows r, Rows scales, hipStream_t stream) {
   if (scales.units > 64 || (r.units <= 64 && r.units + scales.units > 64)) {  // each by itself
@@ -456,10 +462,7 @@ void move_all(const MoveArgs& all, Rows r, Rows scales, hipStream_t stream) {
 // scales: of no units where there are none.
 void move_both(const Rows& r, const Rows& scales, const int32_t* idx, int64_t T, int64_t k, int64_t R, hipStream_t stream) {
   const MoveArgs a{idx, static_cast<uint32_t>(T), static_cast<uint32_t>(k), static_cast<uint32_t>(R)};
-  // Aligned rows are written past the caches: 16384 rows of 14 KiB, 235 MB, take 53.6 us so
-  // and 61 through them, 8192 rows of 2 KiB 11.0 and 12.6. The largest lose a little by it:
-  // 131072 rows of 7 KiB, 940 MB, 216 us so and 212 through them.
-  if (whole_units(r.bytes, r.dst))
+  if (R * r.bytes < kThroughBytes && whole_units(r.bytes, r.dst))
     move_all<true>(a, r, scales, stream);
   else
     move_all<false>(a, r, scales, stream);
