@@ -11,10 +11,10 @@
 // Rows move in units of 16 bytes at any alignment; the last unit of a row that is no
 // whole number of them begins earlier, so that two lanes write the same bytes twice. A
 // wave holds 1 KiB of a token and writes it top_k times: 16384 tokens of 7168 bytes and
-// their scales, 8 choices each, move in 205 us, 5.3 TB/s (a plain copy of 1 GiB: 5.0);
+// their scales, 8 choices each, move in 205 to 211 us, 5.3 TB/s (a plain copy of 1 GiB: 5.0);
 // waves that write an output row's 1 KiB each and read it anew take 258 to 390, workgroups
-// of whole rows, two KiB a wave and waves that stay as long as this. With the sort 223 us;
-// one token 3.6 us of kernel.
+// of whole rows, two KiB a wave and waves that stay as long as this. With the sort 225 us;
+// one token 3.5 us of kernel.
 #include "mrr_rows.h"
 
 namespace mrr {
@@ -426,12 +426,6 @@ __global__ __launch_bounds__(256) void move_short_rows_kernel(MoveArgs a, Rows r
 
 // Tokens of a launch whose grid's second dimension they are, with the scales' rows of workgroups.
 constexpr uint32_t kMostGridY = 32767;
-// Aligned rows are written past the caches: 16384 rows of 14 KiB, 235 MB, take 53.6 us so
-// and 61 through them, 8192 rows of 2 KiB 11.0 and 12.6. From so many bytes on it is the
-// other way round: 131072 rows of 7 KiB, 940 MB, 216 us past them and 212 through them,
-// 98304 rows, 704 MB, 153 and 156.
-constexpr int64_t kThroughBytes = int64_t(768) << 20;
-
 template <bool kStream>
 void move_all(const MoveArgs& all, Rows r, Rows scales, hipStream_t stream) {
   if (scales.units > 64 || (r.units <= 64 && r.units + scales.units > 64)) {  // each by itself
@@ -462,7 +456,10 @@ void move_all(const MoveArgs& all, Rows r, Rows scales, hipStream_t stream) {
 // scales: of no units where there are none.
 void move_both(const Rows& r, const Rows& scales, const int32_t* idx, int64_t T, int64_t k, int64_t R, hipStream_t stream) {
   const MoveArgs a{idx, static_cast<uint32_t>(T), static_cast<uint32_t>(k), static_cast<uint32_t>(R)};
-  if (R * r.bytes < kThroughBytes && whole_units(r.bytes, r.dst))
+  // Aligned rows are written past the caches: 16384 rows of 14 KiB, 235 MB, take 53.6 us so
+  // and 61 through them, 8192 rows of 2 KiB 11.0 and 12.6; of 940 MB both take the same
+  // within 2%.
+  if (whole_units(r.bytes, r.dst))
     move_all<true>(a, r, scales, stream);
   else
     move_all<false>(a, r, scales, stream);
