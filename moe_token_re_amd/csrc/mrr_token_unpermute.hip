@@ -7,7 +7,8 @@
 // Bound by memory: every row is read once (and its gradient written once). A lane holds
 // 16 bytes of a token's row, all of its choices' loads are under way at once, and sums are
 // fp32 in the order of j. For the gradient a workgroup takes a token, and its lanes keep a
-// part of each choice's product, which are added across lanes at the end.
+// part of each choice's product, which are added across lanes at the end; of more than eight
+// choices two workgroups take a token.
 // 8192 tokens of 8 rows of 14 KiB: 177 us, 6.0 TB/s of 1.06 GB (reading as many bytes in
 // their order takes 137; two KiB a wave, workgroups of 2 to 14 KiB and a token's pieces on
 // one die change nothing). 8192 of 6 rows of 4 KiB: 42 us, and the gradient 73, 6.0 TB/s.
@@ -177,7 +178,6 @@ __device__ __forceinline__ void grad_choices(const GradArgs& a, size_t token, ui
         out.store(to, col, a.H);
     }
   }
-  if (first > 0) __syncthreads();  // the choices before have been read from sh
 #pragma unroll
   for (int j = 0; j < kK; ++j) {
     // without a row it is 0, whatever the gradient holds
@@ -196,8 +196,7 @@ __device__ __forceinline__ void grad_choices(const GradArgs& a, size_t token, ui
 template <int kDtype, int kK, int kWaves, int kHow>
 __global__ __launch_bounds__(64 * kWaves) void sum_rows_backward_kernel(GradArgs a) {
   __shared__ float sh[kWaves][kK];
-  for (uint32_t first = 0; first < a.k; first += kK)
-    grad_choices<kDtype, kK, kWaves, kHow>(a, blockIdx.x, first, sh);
+  grad_choices<kDtype, kK, kWaves, kHow>(a, blockIdx.x, blockIdx.y * kK, sh);
 }
 
 constexpr uint32_t kMostGridY = 65535;
@@ -267,6 +266,10 @@ void launch_sum_dtype(const SumArgs& a, int32_t dtype, int how, hipStream_t stre
 // back, us by a wave and by four: of 3 KiB 8.8 and 7.0, of 8 KiB 15.9 and 9.5; 4096 tokens of
 // 6 rows of 1 KiB 20.0 and 24.9, of 4 KiB 61.5 and 60.2).
 constexpr uint32_t kWideRow = 2048;
+// And by eight past so many (us by four, eight and sixteen: one token of 15 rows of 57 KiB 63,
+// 24 and 19; 64 tokens of 8 rows of 14 KiB 10.9, 9.8 and 9.7; 8192 tokens of 8 rows of 8 KiB
+// 329, 323 and 316, of 6 rows of 5 KiB 140, 138 and 174).
+constexpr uint32_t kWiderRow = 4096;
 
 template <int kDtype, int kK, int kHow>
 void launch_grad(const GradArgs& all, hipStream_t stream) {
@@ -278,10 +281,13 @@ void launch_grad(const GradArgs& all, hipStream_t stream) {
     a.weight += static_cast<size_t>(t) * a.k;
     a.grad_weight += static_cast<size_t>(t) * a.k;
     a.grad += static_cast<size_t>(t) * a.H * kBytes;
-    if (a.H * kBytes > kWideRow)
-      sum_rows_backward_kernel<kDtype, kK, 4, kHow><<<a.T, 256, 0, stream>>>(a);
+    const dim3 grid(a.T, (a.k + kK - 1) / kK);
+    if (a.H * kBytes > kWiderRow)
+      sum_rows_backward_kernel<kDtype, kK, 8, kHow><<<grid, 512, 0, stream>>>(a);
+    else if (a.H * kBytes > kWideRow)
+      sum_rows_backward_kernel<kDtype, kK, 4, kHow><<<grid, 256, 0, stream>>>(a);
     else
-      sum_rows_backward_kernel<kDtype, kK, 1, kHow><<<a.T, 64, 0, stream>>>(a);
+      sum_rows_backward_kernel<kDtype, kK, 1, kHow><<<grid, 64, 0, stream>>>(a);
     t += a.T;
   }
 }
@@ -296,7 +302,7 @@ void launch_grad_k(const GradArgs& a, hipStream_t stream) {
     launch_grad<kDtype, 4, kHow>(a, stream);
   else if (a.k <= 6)
     launch_grad<kDtype, 6, kHow>(a, stream);
-  else  // above 8 in two rounds
+  else  // above 8 by two workgroups
     launch_grad<kDtype, 8, kHow>(a, stream);
 }
 
