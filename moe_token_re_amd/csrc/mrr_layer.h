@@ -35,7 +35,9 @@ inline NormShape norm_shape(int64_t rows, int64_t H) {
 }
 
 // The same for the gradient, which keeps three rows, the next ones, and a sum of each
-// column in registers.
+// column in registers. (8192 rows with the sum's gradient: bf16 of 7168 by 1024 lanes 85.8 us
+// and by 512 of two units 84.7, of 8192 93.4 and 96.0, fp32 of 8192 195 and 214; bf16 of 16384
+// by 512 lanes of four units 243 and by 1024 of two 285.)
 inline NormShape norm_backward_shape(int64_t H) {
   if (H <= 512) return {64, 1};
   if (H <= 1024) return {128, 1};

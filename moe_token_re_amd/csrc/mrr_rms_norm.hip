@@ -120,7 +120,7 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
   constexpr uint32_t kBytes = Eight<kX>::kBytes;
   const auto col_of = [&](int i) { return 8 * (i * kLanes + lane); };
   const auto load = [&](Eight<kX>(&v)[kUnits], const uint8_t* from) {
-    if (a.stream) {
+    if (kX != MRR_F32 && a.stream) {
       const WholeRow<> r(from + first * kBytes, a.H * kBytes);
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) v[i].load_whole(r, col_of(i));
@@ -130,7 +130,7 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
     }
   };
   const auto store = [&](uint8_t* to, int i, const Eight<kX>& v) {
-    if (a.stream)
+    if (kX != MRR_F32 && a.stream)
       v.store_whole(WholeRow<>(to + first * kBytes, a.H * kBytes), col_of(i));
     else
       v.store(to + first * kBytes, col_of(i), a.H);
@@ -360,7 +360,10 @@ void launch_types(const NormArgs& a, int out, NormShape s, hipStream_t stream) {
 constexpr int64_t kRowsPerLaunch = int64_t(1) << 21;
 // From so many bytes of rows on, with which the eight L2 are full, they are read, and
 // written, past the caches. Rows of 14 KiB with their sum, to fp8 rows: 22 MB take 16.8 us
-// through the caches and 17.6 past them, 34 MB 25.1 and 24.0, 50 MB 39.8 and 32.1.
+// through the caches and 17.6 past them, 34 MB 25.1 and 24.0, 50 MB 39.8 and 32.1. Not 32-bit
+// ones: a lane's 8 values are two units there, two requests to each line, which then moves
+// twice (8192 rows of 4096 with their sum, to e4m3 rows 155 us past the caches and 81
+// through them, to 32-bit ones 272 and 95).
 constexpr int64_t kStreamBytes = int64_t(24) << 20;
 
 }  // namespace
@@ -390,7 +393,7 @@ extern "C" mrr_status mrr_rms_norm(const mrr_rms_norm_args* args, struct ihipStr
     a.eps = static_cast<float>(args->eps);
     a.eps64 = args->eps;
     a.inv_h = 1.0f / static_cast<float>(args->H);
-    a.stream = args->rows * args->H * b >= kStreamBytes &&
+    a.stream = b == 2 && args->rows * args->H * b >= kStreamBytes &&
                whole_units(args->H * b, a.x, a.residual, a.sum, out == kWide ? a.y : nullptr);
     a.narrow = args->y_dtype;
     switch (args->dtype) {

@@ -27,7 +27,9 @@ struct BackArgs {
 };
 
 // Rows of so many bytes are read and written past the caches (H 4096: 8192 rows of bf16
-// 51.6 us so and 54.1 through them, 16384 93.5 and 100, 1024 14.6 and 14.3).
+// 51.6 us so and 54.1 through them, 16384 93.5 and 100, 1024 14.6 and 14.3). Not 32-bit ones:
+// a lane's 8 values are two units there, two requests to each line, which then comes twice
+// (8192 rows 173 us past the caches and 99 through them).
 constexpr int64_t kStreamBytes = int64_t(64) << 20;
 // Between these sums of squares 32 bits do; a smaller one is nothing next to kLeastEps.
 constexpr float kMostSum = 1e37f, kLeastSum = 1e-30f, kLeastEps = 1e-20f;
@@ -308,10 +310,13 @@ void launch(const BackArgs& a, hipStream_t stream) {
   }
   if constexpr (!kOneWay) {
     const int64_t row = static_cast<int64_t>(a.H) * Eight<kX>::kBytes;
-    if (a.rows * row >= kStreamBytes && whole_units(row, a.x, a.grad, a.grad_sum, a.grad_x))
-      rms_norm_backward_kernel<kX, kW, kLanes, kUnits, kStreamed><<<grid, kThreads, 0, stream>>>(a);
-    else
-      rms_norm_backward_kernel<kX, kW, kLanes, kUnits, kAgain><<<grid, kThreads, 0, stream>>>(a);
+    if constexpr (kX != MRR_F32) {
+      if (a.rows * row >= kStreamBytes && whole_units(row, a.x, a.grad, a.grad_sum, a.grad_x)) {
+        rms_norm_backward_kernel<kX, kW, kLanes, kUnits, kStreamed><<<grid, kThreads, 0, stream>>>(a);
+        return;
+      }
+    }
+    rms_norm_backward_kernel<kX, kW, kLanes, kUnits, kAgain><<<grid, kThreads, 0, stream>>>(a);
   }
 }
 
