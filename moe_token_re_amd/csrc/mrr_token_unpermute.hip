@@ -11,7 +11,7 @@
 // choices two workgroups take a token.
 // 8192 tokens of 8 rows of 14 KiB: 177 us, 6.0 TB/s of 1.06 GB (reading as many bytes in
 // their order takes 137; two KiB a wave, workgroups of 2 to 14 KiB and a token's pieces on
-// one die change nothing). 8192 of 6 rows of 4 KiB: 42 us, and the gradient 73, 6.0 TB/s.
+// one die change nothing). 8192 of 6 rows of 4 KiB: 43 us, and the gradient 69, 6.3 TB/s.
 #include "mrr_rows.h"
 
 namespace mrr {
