@@ -1,0 +1,44 @@
+// mrr_quotient.h -- 64-bit numbers on their way to few bits by way of 32, so that the last
+// rounding is that of the exact number. No HIP header: the tests run it on the host as well.
+#pragma once
+
+#include <stdint.h>
+
+#if defined(__HIP__)
+#define MRR_ANYWHERE __host__ __device__ inline
+#else
+#define MRR_ANYWHERE inline
+#endif
+
+namespace mrr {
+
+// The nearer of 32 bits' neighbours towards 0, its last bit set, where the number is none of
+// them: a rounding of it to fewer bits is then that of the number, which is d, or off from it
+// towards the sign of `rest` by less than d's neighbours in 64 bits are.
+MRR_ANYWHERE float to_odd(double d, double rest = 0.0) {
+  const float f = static_cast<float>(d);
+  const double back = static_cast<double>(f);
+  const bool nearer = d < 0.0 ? rest > 0.0 : rest < 0.0;  // to 0 than d
+  if (!(__builtin_fabsf(f) < __builtin_inff()) || (back == d && rest == 0.0)) return f;
+  const bool over = back == d ? nearer : __builtin_fabs(back) > __builtin_fabs(d);
+  uint32_t b;
+  __builtin_memcpy(&b, &f, 4);
+  b = (b - (over ? 1u : 0u)) | 1u;
+  float odd;
+  __builtin_memcpy(&odd, &b, 4);
+  return odd;
+}
+
+// full p / most, of products p and most of two 32-bit numbers (48 bits; |p| <= most, inverse =
+// 1 / most): full p has up to 55 bits and is taken in two parts. With most's 48 bits every
+// remainder is exact, so the last one has the sign of what q lacks of the exact quotient, and
+// is 0 where q is that: a quotient on a border between two roundings, or next to one by less
+// than 64 bits hold, is on the side where it belongs.
+MRR_ANYWHERE float quotient_to_odd(double p, double most, double inverse, double full) {
+  const double hi = full * p, lo = __builtin_fma(full, p, -hi);
+  const double q0 = hi * inverse;
+  const double q = __builtin_fma(__builtin_fma(-q0, most, hi) + lo, inverse, q0);
+  return to_odd(q, __builtin_fma(-q, most, hi) + lo);
+}
+
+}  // namespace mrr

@@ -18,9 +18,11 @@
 // Other values with few bits are rounded from 32-bit numbers that are off by less than
 // kDoubt of themselves. Where a number so much smaller and one so much larger are rounded
 // otherwise, which is in about one row of 7168 values of seven, the row is taken again in
-// 64 bits, whose roundings to 32 on the way keep on which side of a border a number lay.
+// 64 bits, whose roundings to 32 on the way keep on which side of a border a number lay
+// (mrr_quotient.h; a quotient's exact number, whatever the rows' type).
 // So is a row whose sum of squares or largest product leaves the range of 32 bits, or is
 // not finite.
+#include "mrr_quotient.h"
 #include "mrr_rows.h"
 
 namespace mrr {
@@ -54,16 +56,6 @@ constexpr float kLeastEps = 1e-20f;
 // half of that counts; the mean, root, reciprocal, two products and a quotient 6 more: 15
 // roundings of 2^-24.
 constexpr float kDoubt = 0x1p-20f;
-
-// The nearer of 32 bits' neighbours towards 0, its last bit set, where d is none of them:
-// a rounding of it to fewer bits is then that of d.
-__device__ __forceinline__ float to_odd(double d) {
-  const float f = static_cast<float>(d);
-  const double back = static_cast<double>(f);
-  if (back == d || !(fabsf(f) < INFINITY)) return f;
-  const uint32_t b = __float_as_uint(f) - (fabs(back) > fabs(d) ? 1u : 0u);
-  return __uint_as_float(b | 1u);
-}
 
 // The sum, or the largest, of a row's waves.
 template <int kWaves, typename T, typename F>
@@ -310,13 +302,11 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
       const float scale = bad ? __builtin_nanf("") : static_cast<float>(r64 * most64 / full);
       __builtin_memcpy(a.scales + static_cast<size_t>(row) * 4, &scale, 4);
     }
-    const double inverse = 1.0 / most64, over = bad || most64 == 0.0 ? 0.0 : full * inverse;
+    const bool zeros = bad || most64 == 0.0;
+    const double inverse = 1.0 / most64;
     write(std::false_type{}, [&](int i, int k) {
       const double p = static_cast<double>(s[i].get(k)) * static_cast<double>(w[i].get(k));
-      if (over == 0.0) return 0.0f;
-      // the quotient by one more step of its division: what is a border is one exactly
-      const double q0 = p * over, q = fma(fma(-q0, most64, full * p), inverse, q0);
-      return to_odd(q);
+      return zeros ? 0.0f : quotient_to_odd(p, most64, inverse, full);
     });
   } else {
     write(std::false_type{}, [&](int i, int k) {
