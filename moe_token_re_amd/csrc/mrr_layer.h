@@ -83,6 +83,25 @@ inline int64_t permute_blocks(int64_t choices, int64_t E) {
   return (choices + block - 1) / block;
 }
 
+// The gradient of the rows' sums: a token's row by a wave, or by four past so many bytes (64 tokens
+// of 6 rows, forward and back, us by a wave and by four: of 3 KiB 8.8 and 7.0, of 8 KiB 15.9 and
+// 9.5; 4096 tokens of 6 rows of 1 KiB 20.0 and 24.9, of 4 KiB 61.5 and 60.2).
+constexpr int64_t kGradWideRow = 2048;
+// And by eight past so many (us by four, eight and sixteen: one token of 15 rows of 57 KiB 63,
+// 24 and 19; 64 tokens of 8 rows of 14 KiB 10.9, 9.8 and 9.7; 8192 tokens of 8 rows of 8 KiB
+// 329, 323 and 316, of 6 rows of 5 KiB 140, 138 and 174).
+constexpr int64_t kGradWiderRow = 4096;
+constexpr int grad_waves(int64_t row_bytes) { return row_bytes > kGradWiderRow ? 8 : row_bytes > kGradWideRow ? 4 : 1; }
+// Choices of a token that one workgroup takes: above 8 two do.
+constexpr int grad_choices_at_once(int64_t top_k) {
+  return top_k <= 2 ? static_cast<int>(top_k) : top_k <= 4 ? 4 : top_k <= 6 ? 6 : 8;
+}
+// Tokens of one launch, whose grid holds less than 2^32 threads.
+constexpr int64_t grad_launch_tokens(int64_t row_bytes, int64_t top_k) {
+  const int64_t groups = (top_k + grad_choices_at_once(top_k) - 1) / grad_choices_at_once(top_k);
+  return (int64_t(1) << 31) / (64 * grad_waves(row_bytes) * groups);
+}
+
 mrr_status check_rms_norm(const mrr_rms_norm_args* a);
 mrr_status check_rms_norm_backward(const mrr_rms_norm_backward_args* a, const void* ws, size_t ws_bytes);
 mrr_status check_router(const mrr_router_args* a);

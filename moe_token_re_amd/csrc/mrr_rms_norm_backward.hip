@@ -331,6 +331,7 @@ void launch_types(const BackArgs& a, NormShape s, hipStream_t stream) {
       case 1024 * 16 + 1: launch<kX, kW, 1024, 1>(a, stream); break;
       default: launch<kX, kW, 512, 4>(a, stream); break;
     }
+    if (hipPeekAtLastError() != hipSuccess) return;
   }
   rms_norm_weight_kernel<kW><<<(a.H + kSumCols - 1) / kSumCols, 64 * kSumWaves, 0, stream>>>(a);
 }

@@ -430,6 +430,7 @@ template <bool kStream>
 void move_all(const MoveArgs& all, Rows r, Rows scales, hipStream_t stream) {
   if (scales.units > 64 || (r.units <= 64 && r.units + scales.units > 64)) {  // each by itself
     move_all<false>(all, scales, Rows{}, stream);
+    if (hipPeekAtLastError() != hipSuccess) return;
     scales = Rows{};
   }
   const bool wide = r.units > 64;
@@ -446,6 +447,7 @@ void move_all(const MoveArgs& all, Rows r, Rows scales, hipStream_t stream) {
       const uint32_t each = 4 * (64 / (r.units + scales.units));
       move_short_rows_kernel<<<(a.T + each - 1) / each, 256, 0, stream>>>(a, r, scales);
     }
+    if (hipPeekAtLastError() != hipSuccess) return;
     t += a.T;
     a.idx += static_cast<size_t>(a.T) * a.k;
     r.src += static_cast<size_t>(a.T) * r.bytes;
@@ -531,8 +533,10 @@ extern "C" mrr_status mrr_token_permute(const mrr_token_permute_args* args, void
     place_all<true>(a, stream);
   } else {
     permute_count_kernel<<<a.blocks, kSortThreads, 0, stream>>>(a);
+    if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
     place_all<false>(a, stream);
   }
+  if (hipGetLastError() != hipSuccess) return MRR_ERROR_HIP;
   move_both(tokens, scales, a.idx, args->T, args->top_k, n, stream);
   return hipGetLastError() == hipSuccess ? MRR_SUCCESS : MRR_ERROR_HIP;
 }

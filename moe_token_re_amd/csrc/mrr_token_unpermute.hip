@@ -200,7 +200,7 @@ __global__ __launch_bounds__(64 * kWaves) void sum_rows_backward_kernel(GradArgs
 }
 
 constexpr uint32_t kMostGridY = 65535;
-constexpr uint32_t kMostTokens = 1u << 23;  // of a launch, which holds less than 2^32 threads
+constexpr uint32_t kMostTokens = 1u << 23;  // of a launch of short rows, at most a wave a token: less than 2^32 threads
 // Sums and gradients of aligned rows are written past the caches (512 tokens of 8 rows of
 // 14 KiB, forward and back: 32.6 us so and 38.6 through them; smaller ones take the same
 // either way). From so many bytes on, which the last of the caches does not hold, the rows
@@ -226,6 +226,7 @@ void launch_sum(const SumArgs& all, hipStream_t stream) {
       const uint32_t each = 4 * (64 / units);
       sum_short_rows_kernel<kDtype, kK><<<(a.T + each - 1) / each, 256, 0, stream>>>(a);
     }
+    if (hipPeekAtLastError() != hipSuccess) return;
     t += a.T;
   }
 }
@@ -262,48 +263,38 @@ void launch_sum_dtype(const SumArgs& a, int32_t dtype, int how, hipStream_t stre
     launch_sum_how<kPast>(a, dtype, stream);
 }
 
-// A token's row by a wave, or by four past so many bytes (64 tokens of 6 rows, forward and
-// back, us by a wave and by four: of 3 KiB 8.8 and 7.0, of 8 KiB 15.9 and 9.5; 4096 tokens of
-// 6 rows of 1 KiB 20.0 and 24.9, of 4 KiB 61.5 and 60.2).
-constexpr uint32_t kWideRow = 2048;
-// And by eight past so many (us by four, eight and sixteen: one token of 15 rows of 57 KiB 63,
-// 24 and 19; 64 tokens of 8 rows of 14 KiB 10.9, 9.8 and 9.7; 8192 tokens of 8 rows of 8 KiB
-// 329, 323 and 316, of 6 rows of 5 KiB 140, 138 and 174).
-constexpr uint32_t kWiderRow = 4096;
-
 template <int kDtype, int kK, int kHow>
 void launch_grad(const GradArgs& all, hipStream_t stream) {
   constexpr uint32_t kBytes = Unit16<kDtype>::kBytes;
+  const int64_t row = static_cast<int64_t>(all.H) * kBytes;
+  const uint32_t most = static_cast<uint32_t>(grad_launch_tokens(row, all.k));
   for (uint32_t t = 0; t < all.T;) {
     GradArgs a = all;
-    a.T = all.T - t < kMostTokens ? all.T - t : kMostTokens;
+    a.T = all.T - t < most ? all.T - t : most;
     a.idx += static_cast<size_t>(t) * a.k;
     a.weight += static_cast<size_t>(t) * a.k;
     a.grad_weight += static_cast<size_t>(t) * a.k;
     a.grad += static_cast<size_t>(t) * a.H * kBytes;
     const dim3 grid(a.T, (a.k + kK - 1) / kK);
-    if (a.H * kBytes > kWiderRow)
-      sum_rows_backward_kernel<kDtype, kK, 8, kHow><<<grid, 512, 0, stream>>>(a);
-    else if (a.H * kBytes > kWideRow)
-      sum_rows_backward_kernel<kDtype, kK, 4, kHow><<<grid, 256, 0, stream>>>(a);
-    else
-      sum_rows_backward_kernel<kDtype, kK, 1, kHow><<<grid, 64, 0, stream>>>(a);
+    switch (grad_waves(row)) {
+      case 8: sum_rows_backward_kernel<kDtype, kK, 8, kHow><<<grid, 512, 0, stream>>>(a); break;
+      case 4: sum_rows_backward_kernel<kDtype, kK, 4, kHow><<<grid, 256, 0, stream>>>(a); break;
+      default: sum_rows_backward_kernel<kDtype, kK, 1, kHow><<<grid, 64, 0, stream>>>(a); break;
+    }
+    if (hipPeekAtLastError() != hipSuccess) return;
     t += a.T;
   }
 }
 
 template <int kDtype, int kHow>
 void launch_grad_k(const GradArgs& a, hipStream_t stream) {
-  if (a.k == 1)
-    launch_grad<kDtype, 1, kHow>(a, stream);
-  else if (a.k == 2)
-    launch_grad<kDtype, 2, kHow>(a, stream);
-  else if (a.k <= 4)
-    launch_grad<kDtype, 4, kHow>(a, stream);
-  else if (a.k <= 6)
-    launch_grad<kDtype, 6, kHow>(a, stream);
-  else  // above 8 by two workgroups
-    launch_grad<kDtype, 8, kHow>(a, stream);
+  switch (grad_choices_at_once(a.k)) {
+    case 1: launch_grad<kDtype, 1, kHow>(a, stream); break;
+    case 2: launch_grad<kDtype, 2, kHow>(a, stream); break;
+    case 4: launch_grad<kDtype, 4, kHow>(a, stream); break;
+    case 6: launch_grad<kDtype, 6, kHow>(a, stream); break;
+    default: launch_grad<kDtype, 8, kHow>(a, stream); break;
+  }
 }
 
 template <int kHow>
