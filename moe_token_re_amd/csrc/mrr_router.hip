@@ -302,7 +302,14 @@ __global__ __launch_bounds__(kThreads) void router_backward_kernel(RouterBackArg
 #pragma unroll
       for (int b = 0; b < 4; ++b) top = fmaxf(top, l[i][b]);
     top = group_max<kLanes>(top);
-    none = top == -INFINITY;
+    if (top == -INFINITY) {  // the same for all lanes of a token
+      float odd = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kFours; ++i)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) odd = l[i][b] != l[i][b] ? 1.0f : odd;
+      none = group_max<kLanes>(odd) == 0.0f;
+    }
 #pragma unroll
     for (int i = 0; i < kFours; ++i)
 #pragma unroll
