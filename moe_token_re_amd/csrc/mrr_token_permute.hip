@@ -197,10 +197,15 @@ __global__ __launch_bounds__(kFewThreads) void permute_few_kernel(SortArgs a, Ro
     if (moves_scales) s.store(scales, to, zero);
   }
   if (blockIdx.x != 0) return;
-  for (uint32_t more = tid + kFewThreads; more < scales.units; more += kFewThreads) {
-    s.load(scales, token, more);
+  // every lane takes every turn: lane j holds the row of choice j
+  for (uint32_t base = kFewThreads; base < scales.units; base += kFewThreads) {
+    const bool moves_more = base + tid < scales.units;
+    if (moves_more) s.load(scales, token, base + tid);
 #pragma unroll 1
-    for (uint32_t j = 0; j < a.k; ++j) s.store(scales, __builtin_amdgcn_readlane(mine, j), gone >> j & 1);
+    for (uint32_t j = 0; j < a.k; ++j) {
+      const uint32_t to = __builtin_amdgcn_readlane(mine, j);
+      if (moves_more) s.store(scales, to, gone >> j & 1);
+    }
   }
 }
 
