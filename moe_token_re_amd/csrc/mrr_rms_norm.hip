@@ -249,8 +249,16 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
 
   // the same for all lanes of a row
   const float most = __uint_as_float(top);
-  const bool plain = sum <= kMostSum && (sum >= kLeastSum || a.eps >= kLeastEps) &&
-                     (kOut != kRow || top == 0 || (most >= kLeastTop && most <= kMostTop));
+  bool plain = sum <= kMostSum && (sum >= kLeastSum || a.eps >= kLeastEps) &&
+               (kOut != kRow || top == 0 || (most >= kLeastTop && most <= kMostTop));
+  if constexpr (kOut == kRow) {
+    if (top == 0) {  // a row of zeros, or products that are nothing in 32 bits
+      uint32_t some = 0;
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) some |= s[i].any();
+      plain = plain && !(kWaves > 1 ? __syncthreads_or(some != 0) != 0 : __any(some != 0) != 0);
+    }
+  }
   constexpr bool kExact = kOut == kWide || (kOut == kRow && kX == MRR_BF16 && kW == MRR_BF16);
   bool doubt = false;
   if (plain) {

@@ -135,6 +135,14 @@ struct Pack {
     return static_cast<float>(__builtin_bit_cast(f16x2, v)[k % 2]);
   }
 
+  // Not 0 where one of the values is not.
+  __device__ __forceinline__ uint32_t any() const {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) bits |= w[i] & (kDtype == MRR_F32 ? 0x7fffffffu : 0x7fff7fffu);
+    return bits;
+  }
+
   // Has the values widened anew from here on, instead of kept wide in twice the registers.
   __device__ __forceinline__ void keep_packed() {
     if constexpr (kDtype != MRR_F32) {
