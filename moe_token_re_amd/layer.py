@@ -9,7 +9,9 @@ binding (csrc/mrr_torch.cpp), the code here makes every other call and raises
 every error, and there is no CPU path. The results carry no autograd graph:
 each operator's gradient is a function of its own (*_backward), which can be
 called, and captured into a graph, like any other operator here, or stand in
-the backward of a torch.autograd.Function.
+the backward of a torch.autograd.Function. While autograd records, an operator
+refuses inputs that require a gradient, which would be lost: it is called under
+torch.no_grad(), or in the forward of such a Function, where nothing is recorded.
 """
 from __future__ import annotations
 
@@ -46,6 +48,13 @@ def _is(name, t, dev, dtypes, shape):
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _no_graph(where, *tensors):
+    """Refuses to lose a gradient."""
+    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in tensors):
+        raise ValueError(f"{where} records no gradient, and one of its inputs requires one: call it under torch.no_grad(), "
+                         f"or in a torch.autograd.Function with {where}_backward as its backward")
 
 
 def _outputs(out, dev, *want):
@@ -95,6 +104,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optional[torch.
         done = _lib.plain_calls().rms_norm(x, weight, residual, eps, quantize)
         if done is not None:
             return done
+    _no_graph("rms_norm", x, weight, residual)
     dev = _gpu("x", x)
     _wide("x", x, dev)
     if x.dim() < 1 or x.shape[-1] == 0:
@@ -183,6 +193,7 @@ def moe_router_top_k(router_logits: torch.Tensor, top_k: int, *, renormalize: bo
         done = _lib.plain_calls().router(router_logits, top_k, renormalize)
         if done is not None:
             return done
+    _no_graph("moe_router_top_k", router_logits)
     dev = _gpu("router_logits", router_logits)
     T, E = _logits(router_logits, dev)
     if not 1 <= top_k <= min(E, 16):  # without tokens the library gets no address to see it by
@@ -250,6 +261,7 @@ def moe_token_permute(tokens: torch.Tensor, expert_ids: torch.Tensor, num_expert
                                           expert_token_num_type)
         if done is not None:
             return done
+    _no_graph("moe_token_permute", tokens, per_token_scales, expert_weight)
     dev = _gpu("tokens", tokens)
     _check_tensor("tokens", tokens, dev)
     if tokens.dim() != 2:
@@ -346,6 +358,7 @@ def moe_token_unpermute(rows: torch.Tensor, permute_token_idx: torch.Tensor, *,
         done = _lib.plain_calls().unpermute(rows, permute_token_idx, expert_weight)
         if done is not None:
             return done
+    _no_graph("moe_token_unpermute", rows, expert_weight)
     dev = _gpu("rows", rows)
     _, H = _rows("rows", rows, dev)
     T, k = _index(permute_token_idx, dev)
