@@ -245,6 +245,14 @@ __global__ __launch_bounds__(kSortThreads) void permute_count_kernel(SortArgs a)
     a.counts[static_cast<size_t>(blockIdx.x) * (a.E + 1) + e] = static_cast<int32_t>(count[e]);
 }
 
+// What the wave's lanes read and wrote in LDS before comes before what they do after: one
+// instruction of a wave is done for all lanes before its next, and the compiler is told to keep it so.
+__device__ __forceinline__ void in_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // A block's choices take their rows. kRuns of its waves have a run of neighbouring choices
 // each, counted by expert and placed in order, 64 at a time: the lanes of the same expert
 // are found by its bits.
@@ -350,11 +358,12 @@ __global__ __launch_bounds__(kSortThreads) void permute_place_kernel(SortArgs a)
         const uint64_t with = __ballot(set);
         same &= set ? with : ~with;
       }
+      const uint32_t rank = static_cast<uint32_t>(__popcll(same & ((uint64_t(1) << lane) - 1)));
+      const uint32_t row = mine[e] + rank;
+      in_order();  // all have read before the last of them writes
+      if (here && (same >> lane) == 1) mine[e] = row + 1;
+      in_order();  // and that is what the next 64 read
       if (here) {
-        const uint32_t rank = static_cast<uint32_t>(__popcll(same & ((uint64_t(1) << lane) - 1)));
-        const uint32_t row = mine[e] + rank;
-        // the last of them, after all have read
-        if ((same >> lane) == 1) mine[e] = row + 1;
         a.idx[i] = static_cast<int32_t>(e < a.E ? row : ~row);
         if (a.weight != nullptr) a.out_weight[row] = e < a.E ? weight[x] : 0.0f;
       }
