@@ -146,13 +146,18 @@ __device__ __forceinline__ void join_lists(const typename O::T (&v)[kN], typenam
   }
 }
 
-// e^x of x <= 0 (or NaN): 2^(x log2 e), the product's rounding made good to first order.
+// e^x of x <= 0 (or NaN): 2^(x log2 e), the product's rounding made good to first order. 0 below
+// e^-87, which is nothing in a sum that e^0 is part of; with kAll down to the smallest numbers
+// of 32 bits, which the instruction would not give.
+template <bool kAll = false>
 __device__ __forceinline__ float exp_of(float x) {
   constexpr double kLog2E = 1.4426950408889634, kLn2 = 0.6931471805599453;
   constexpr float kHi = static_cast<float>(kLog2E), kLo = static_cast<float>(kLog2E - static_cast<double>(kHi));
   const float hi = x * kHi, lo = __builtin_fmaf(x, kLo, __builtin_fmaf(x, kHi, -hi));
-  const float e = __builtin_amdgcn_exp2f(hi);
-  return x < -87.0f ? 0.0f : __builtin_fmaf(e, lo * static_cast<float>(kLn2), e);
+  const bool below = kAll && hi < -125.0f;  // hi + 64 is exact there
+  const float e = __builtin_amdgcn_exp2f(below ? hi + 64.0f : hi);
+  const float r = __builtin_fmaf(e, lo * static_cast<float>(kLn2), e);
+  return x < (kAll ? -104.0f : -87.0f) ? 0.0f : below ? r * 0x1p-64f : r;
 }
 
 template <int kLanes>
@@ -237,7 +242,7 @@ __global__ __launch_bounds__(kThreads) void router_kernel(RouterArgs a) {
 #pragma unroll
   for (int r = 0; r < kKeep; ++r) mine = static_cast<int>(lane) == r ? best[r] : mine;
   const bool chosen = mine != O::kNone && lane < a.k;
-  const float p = chosen ? exp_of(O::value(mine) - top) : 0.0f;
+  const float p = chosen ? exp_of<true>(O::value(mine) - top) : 0.0f;
   float sum = p;
   if (!a.renormalize) {
     sum = 0.0f;
