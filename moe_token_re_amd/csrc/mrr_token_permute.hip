@@ -358,12 +358,12 @@ __global__ __launch_bounds__(kSortThreads) void permute_place_kernel(SortArgs a)
         const uint64_t with = __ballot(set);
         same &= set ? with : ~with;
       }
-      const uint32_t rank = static_cast<uint32_t>(__popcll(same & ((uint64_t(1) << lane) - 1)));
-      const uint32_t row = mine[e] + rank;
-      in_order();  // all have read before the last of them writes
-      if (here && (same >> lane) == 1) mine[e] = row + 1;
-      in_order();  // and that is what the next 64 read
       if (here) {
+        const uint32_t rank = static_cast<uint32_t>(__popcll(same & ((uint64_t(1) << lane) - 1)));
+        const uint32_t row = mine[e] + rank;
+        in_order();  // all have read before the last of them writes
+        if ((same >> lane) == 1) mine[e] = row + 1;
+        in_order();  // and that is what the next 64 read
         a.idx[i] = static_cast<int32_t>(e < a.E ? row : ~row);
         if (a.weight != nullptr) a.out_weight[row] = e < a.E ? weight[x] : 0.0f;
       }
