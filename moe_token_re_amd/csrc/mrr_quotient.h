@@ -29,11 +29,20 @@ MRR_ANYWHERE float to_odd(double d, double rest = 0.0) {
   return odd;
 }
 
-// full p / most, of products p and most of two 32-bit numbers (48 bits; |p| <= most, inverse =
-// 1 / most): full p has up to 55 bits and is taken in two parts. With most's 48 bits every
-// remainder is exact, so the last one has the sign of what q lacks of the exact quotient, and
-// is 0 where q is that: a quotient on a border between two roundings, or next to one by less
-// than 64 bits hold, is on the side where it belongs.
+// full p / most, of products p and most (|p| <= most, inverse = 1 / most), where full p is exact in
+// 64 bits and no quotient lies off a border between two roundings by less than 64 bits hold: of
+// products of 46 bits by 127, and of two 32-bit numbers' 48 by 448, whose e4m3 borders have 5
+// bits, so that what is off one is off by more than 2^-53 of it.
+MRR_ANYWHERE float short_quotient_to_odd(double p, double most, double inverse, double full) {
+  const double q0 = full * p * inverse;
+  return to_odd(__builtin_fma(__builtin_fma(-q0, most, full * p), inverse, q0));
+}
+
+// Of products of two 32-bit numbers 127 p has up to 55 bits and is taken in two parts. With
+// most's 48 bits every remainder is exact, so the last one has the sign of what q lacks of the
+// exact quotient, and is 0 where q is that: a quotient on a border, or next to one by less than
+// 64 bits hold, is on the side where it belongs. (8192 x 4096 fp32 rows with their sum to int8
+// 83.8 us, with one part 82.5.)
 MRR_ANYWHERE float quotient_to_odd(double p, double most, double inverse, double full) {
   const double hi = full * p, lo = __builtin_fma(full, p, -hi);
   const double q0 = hi * inverse;

@@ -249,16 +249,8 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
 
   // the same for all lanes of a row
   const float most = __uint_as_float(top);
-  bool plain = sum <= kMostSum && (sum >= kLeastSum || a.eps >= kLeastEps) &&
-               (kOut != kRow || top == 0 || (most >= kLeastTop && most <= kMostTop));
-  if constexpr (kOut == kRow) {
-    if (top == 0) {  // a row of zeros, or products that are nothing in 32 bits
-      uint32_t some = 0;
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) some |= s[i].any();
-      plain = plain && !(kWaves > 1 ? __syncthreads_or(some != 0) != 0 : __any(some != 0) != 0);
-    }
-  }
+  const bool plain = sum <= kMostSum && (sum >= kLeastSum || a.eps >= kLeastEps) &&
+                     (kOut != kRow || top == 0 || (most >= kLeastTop && most <= kMostTop));
   constexpr bool kExact = kOut == kWide || (kOut == kRow && kX == MRR_BF16 && kW == MRR_BF16);
   bool doubt = false;
   if (plain) {
@@ -277,7 +269,13 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
       doubt = write(std::bool_constant<!kExact>{}, [&](int i, int k) { return s[i].get(k) * r * w[i].get(k); });
     }
   }
-  if constexpr (!kExact) doubt = kWaves > 1 ? __syncthreads_or(doubt) != 0 : __any(doubt) != 0;
+  if constexpr (kOut == kRow) {
+    if (top == 0) {  // of zeros, or products that are nothing in 32 bits
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) doubt = doubt || s[i].any() != 0;
+    }
+  }
+  if (!kExact || (kOut == kRow && top == 0)) doubt = kWaves > 1 ? __syncthreads_or(doubt) != 0 : __any(doubt) != 0;
   if (plain && !doubt) return;
 
   double sum64 = 0.0, most64 = 0.0;
@@ -312,10 +310,16 @@ __global__ __launch_bounds__(kLanes < 256 ? 256 : kLanes) void rms_norm_kernel(N
     }
     const bool zeros = bad || most64 == 0.0;
     const double inverse = 1.0 / most64;
-    write(std::false_type{}, [&](int i, int k) {
-      const double p = static_cast<double>(s[i].get(k)) * static_cast<double>(w[i].get(k));
-      return zeros ? 0.0f : quotient_to_odd(p, most64, inverse, full);
-    });
+    const auto rounded = [&](auto&& quotient) {
+      write(std::false_type{}, [&](int i, int k) {
+        const double p = static_cast<double>(s[i].get(k)) * static_cast<double>(w[i].get(k));
+        return zeros ? 0.0f : quotient(p, most64, inverse, full);
+      });
+    };
+    if (kX == MRR_F32 && a.narrow == MRR_I8)
+      rounded(quotient_to_odd);
+    else
+      rounded(short_quotient_to_odd);
   } else {
     write(std::false_type{}, [&](int i, int k) {
       const double y = static_cast<double>(s[i].get(k)) * r64 * static_cast<double>(w[i].get(k));
