@@ -442,8 +442,12 @@ mrr_status mrr_few_tokens(const mrr_few_tokens_args* args, void* workspace, size
  * The conventions at the top of this file hold for them too: device pointers,
  * dense rows (of any alignment of their elements), host-detectable errors
  * before anything is launched, asynchronous on `stream`, no allocation. No
- * call adds in an order that depends on timing: results are the same bits
- * each time.
+ * call adds in an order that depends on timing: the same call gives the same
+ * bits each time. (The order depends on sizes: a row of the norm adds its
+ * squares otherwise among up to 256 rows than among more.) What is not rounded
+ * from the exact number is computed in 32 bits, its sums included, and rounded
+ * once to a result's type; numbers on the way that lie below 2^-126 have 32
+ * bits' smallest steps there.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -454,7 +458,8 @@ mrr_status mrr_few_tokens(const mrr_few_tokens_args* args, void* workspace, size
  *   - dtype (x's own): no scales.
  *   - I8 or F8_E4M3FN with scales F32 [rows]: scale = max |y| / 127 or / 448 of
  *     the row, values y / scale = 127 (448) p / max |p| with p = weight * s,
- *     rounded to nearest, ties to even. A row of zeros has scale 0. A row of
+ *     each rounded once from the exact number to nearest, ties to even. A row of
+ *     zeros has scale 0. A row of
  *     which some p is not finite has the scale NaN and zeros as values.
  *   - F8_E4M3FN or F4_E2M1 with scales F8_E8M0 [rows, ceil(H/64), 2]:
  *     microscaled, as mrr_mx_quantize() does for 4 bits: 32 values share
@@ -489,7 +494,7 @@ mrr_status mrr_rms_norm(const mrr_rms_norm_args* args, struct ihipStream_t* stre
  *     grad_weight = sum over the rows of grad * n
  * x is what the norm was taken of: the sum, where a residual was added; grad_x
  * is then the gradient of both x and residual. Sums are kept in 32 bits, each
- * result is rounded once.
+ * result is rounded once. grad * weight has to lie in the range of 32 bits.
  */
 typedef struct mrr_rms_norm_backward_args {
   const void* grad;                /* [rows, H], dtype */
@@ -519,7 +524,8 @@ mrr_status mrr_rms_norm_backward(const mrr_rms_norm_backward_args* args, void* w
  * the row's softmax, over all E logits or with renormalize over the chosen
  * ones. An expert whose logit is -inf is never chosen: where fewer than top_k
  * are left the id is -1 and the weight 0. NaN counts as the largest; a NaN or
- * +inf in a row makes the weights of its chosen experts NaN.
+ * +inf in a row makes the weights of its chosen experts NaN (an id of -1 has
+ * the weight 0 still).
  */
 typedef struct mrr_router_args {
   const void* logits;              /* [T, E] F16, BF16 or F32 */
@@ -541,7 +547,8 @@ mrr_status mrr_router(const mrr_router_args* args, struct ihipStream_t* stream);
  * (over all experts, or the chosen ones) and g the gradient of each p (0 where
  * it is not returned): grad_logits = p (g - sum of g p). Ids outside [0, E) add
  * nothing. expert_weight and expert_ids are what mrr_router() returned: no expert
- * twice in a row.
+ * twice in a row. Over all experts a NaN or +inf among the logits makes the row's
+ * gradient NaN, and a p below e^-87 of the largest counts as 0.
  */
 typedef struct mrr_router_backward_args {
   const float* grad_weight;        /* [T, top_k] */

@@ -11,7 +11,7 @@
 // Rows move in units of 16 bytes at any alignment; the last unit of a row that is no
 // whole number of them begins earlier, so that two lanes write the same bytes twice. A
 // wave holds 1 KiB of a token and writes it top_k times: 16384 tokens of 7168 bytes and
-// their scales, 8 choices each, move in 205 to 211 us, 5.3 TB/s (a plain copy of 1 GiB: 5.0);
+// their scales, 8 choices each, move in 205 to 211 us, 5.3 TB/s (a plain copy of 1 GiB: 6.7);
 // waves that write an output row's 1 KiB each and read it anew take 258 to 390, workgroups
 // of whole rows, two KiB a wave and waves that stay as long as this. With the sort 225 us;
 // one token 3.5 us of kernel.

@@ -99,7 +99,9 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optional[torch.
       "mxfp8", "mxfp4"  microscaled float8_e4m3fn or float4_e2m1fn_x2 [..., H/2] rows,
                scales [..., ceil(H/64), 2] float8_e8m0fnu, as mx_quantize makes them.
     These are tokens and per_token_scales as moe_token_permute and moe_re_routing
-    take them; "mxfp4" rows are mx_grouped_mm's. `out` is a tuple like the result."""
+    take them; "mxfp4" rows are mx_grouped_mm's. `out` is a tuple like the result.
+    Up to 256 rows add their squares in another order than more do: the last place of a
+    wide value, or of a scale, may differ between the same row in a small and a large batch."""
     if out is None:
         done = _lib.plain_calls().rms_norm(x, weight, residual, eps, quantize)
         if done is not None:
@@ -146,7 +148,8 @@ def rms_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     that reaches s by itself (from what reads the residual later), added to the result.
 
     Returns (grad_x, grad_weight) of x's and weight's dtypes: grad_x is the gradient of
-    x and of the residual alike, grad_weight [H] is summed over all rows in float32."""
+    x and of the residual alike, grad_weight [H] is summed over all rows in float32. grad *
+    weight has to lie in float32's range."""
     if out is None and workspace is None:
         done = _lib.plain_calls().rms_norm_backward(grad, x, weight, grad_residual, eps)
         if done is not None:
