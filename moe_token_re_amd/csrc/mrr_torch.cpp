@@ -35,7 +35,6 @@ bool is_packed(const at::Tensor& t) {
 struct Call {
   c10::Device device{c10::DeviceType::CPU};
   bool ok = true;
-  bool leads_back = false;  // one of them requires a gradient
 
   const at::Tensor* take(PyObject* o) {
     if (!ok || !THPVariable_CheckExact(o)) {
@@ -51,11 +50,8 @@ struct Call {
     } else {
       ok = t.device() == device;
     }
-    leads_back = leads_back || t.requires_grad();
     return &t;
   }
-  // Whether autograd would have to record the call, which no operator does.
-  bool recorded() const { return leads_back && c10::GradMode::is_enabled(); }
   const at::Tensor* take_optional(PyObject* o) { return o == Py_None ? nullptr : take(o); }
 
   // A pair of packed rows and scales; the values of a row.
@@ -79,6 +75,14 @@ struct Call {
 };
 
 PyObject* none() { Py_RETURN_NONE; }
+
+// Whether autograd would have to record a call with these inputs, which no operator does.
+bool recorded(std::initializer_list<const at::Tensor*> inputs) {
+  if (!c10::GradMode::is_enabled()) return false;
+  for (const at::Tensor* t : inputs)
+    if (t != nullptr && t->requires_grad()) return true;
+  return false;
+}
 
 template <typename F>
 mrr_status unlocked(F&& f) {
@@ -281,7 +285,7 @@ PyObject* rms_norm(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const at::Tensor* x = c.take(args[0]);
   const at::Tensor* weight = c.take(args[1]);
   const at::Tensor* residual = c.take_optional(args[2]);
-  if (!c.ok || c.recorded() || wide_code(x->scalar_type()) < 0 || x->dim() < 1) return none();
+  if (!c.ok || recorded({x, weight, residual}) || wide_code(x->scalar_type()) < 0 || x->dim() < 1) return none();
   const int64_t H = x->size(-1);
   if (H == 0 || !norm_weight(weight, x) || !same_shape(residual, x)) return none();
   const at::ScalarType dtype = x->scalar_type();
@@ -350,7 +354,7 @@ PyObject* router(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != 3 || !whole(args[1], &k) || !PyBool_Check(args[2])) return none();
   Call c;
   const at::Tensor* logits = c.take(args[0]);
-  if (!c.ok || c.recorded() || wide_code(logits->scalar_type()) < 0 || logits->dim() != 2) return none();
+  if (!c.ok || recorded({logits}) || wide_code(logits->scalar_type()) < 0 || logits->dim() != 2) return none();
   const int64_t T = logits->size(0), E = logits->size(1);
   if (k < 1 || k > E || k > 16) return none();
   at::Tensor weight = c.empty({T, k}, at::kFloat), ids = c.empty({T, k}, at::kInt);
@@ -408,7 +412,7 @@ PyObject* permute(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const at::Tensor* ids = c.take(args[1]);
   const at::Tensor* scales = c.take_optional(args[3]);
   const at::Tensor* weight = c.take_optional(args[4]);
-  if (!c.ok || c.recorded() || tokens->dim() != 2 || ids->dim() != 2) return none();
+  if (!c.ok || recorded({tokens, scales, weight}) || tokens->dim() != 2 || ids->dim() != 2) return none();
   const int code = moved_code(tokens->scalar_type());
   const int64_t T = tokens->size(0), k = ids->size(1), H = tokens->size(1) * (code == MRR_F4_E2M1 ? 2 : 1);
   if (code < 0 || H == 0 || E < 1 || !choices(ids, at::kInt, T, k) || !choices(weight, at::kFloat, T, k)) return none();
@@ -470,7 +474,7 @@ PyObject* unpermute(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const at::Tensor* rows = c.take(args[0]);
   const at::Tensor* idx = c.take(args[1]);
   const at::Tensor* weight = c.take_optional(args[2]);
-  if (!c.ok || c.recorded() || !sum_sizes(rows, idx, weight)) return none();
+  if (!c.ok || recorded({rows, weight}) || !sum_sizes(rows, idx, weight)) return none();
   at::Tensor y = c.empty({idx->size(0), rows->size(1)}, rows->scalar_type());
   const mrr_token_unpermute_args a{rows->data_ptr(), wide_code(rows->scalar_type()), rows->size(0), rows->size(1),
                                    static_cast<const int32_t*>(idx->data_ptr()), idx->size(0), idx->size(1),
