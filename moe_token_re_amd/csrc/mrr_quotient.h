@@ -12,18 +12,28 @@
 
 namespace mrr {
 
-// The nearer of 32 bits' neighbours towards 0, its last bit set, where the number is none of
-// them: a rounding of it to fewer bits is then that of the number, which is d, or off from it
-// towards the sign of `rest` by less than d's neighbours in 64 bits are.
-MRR_ANYWHERE float to_odd(double d, double rest = 0.0) {
+// The nearer of 32 bits' neighbours towards 0, its last bit set, where d is none of them: a
+// rounding of it to fewer bits is then that of d.
+MRR_ANYWHERE float to_odd(double d) {
   const float f = static_cast<float>(d);
   const double back = static_cast<double>(f);
-  const bool nearer = d < 0.0 ? rest > 0.0 : rest < 0.0;  // to 0 than d
-  if (!(__builtin_fabsf(f) < __builtin_inff()) || (back == d && rest == 0.0)) return f;
-  const bool over = back == d ? nearer : __builtin_fabs(back) > __builtin_fabs(d);
+  if (back == d || !(__builtin_fabsf(f) < __builtin_inff())) return f;
   uint32_t b;
   __builtin_memcpy(&b, &f, 4);
-  b = (b - (over ? 1u : 0u)) | 1u;
+  b = (b - (__builtin_fabs(back) > __builtin_fabs(d) ? 1u : 0u)) | 1u;
+  float odd;
+  __builtin_memcpy(&odd, &b, 4);
+  return odd;
+}
+
+// The same of a number that lies off a finite d towards the sign of `rest`, by less than d's
+// neighbours in 64 bits do.
+MRR_ANYWHERE float to_odd(double d, double rest) {
+  const float f = static_cast<float>(d);
+  if (rest == 0.0 || static_cast<double>(f) != d) return to_odd(d);
+  uint32_t b;
+  __builtin_memcpy(&b, &f, 4);
+  b = (b - ((d < 0.0) == (rest > 0.0) ? 1u : 0u)) | 1u;
   float odd;
   __builtin_memcpy(&odd, &b, 4);
   return odd;

@@ -12,6 +12,7 @@ called, and captured into a graph, like any other operator here, or stand in
 the backward of a torch.autograd.Function. While autograd records, an operator
 refuses inputs that require a gradient, which would be lost: it is called under
 torch.no_grad(), or in the forward of such a Function, where nothing is recorded.
+The gradients take any tensors, and what they return leads no further.
 """
 from __future__ import annotations
 
