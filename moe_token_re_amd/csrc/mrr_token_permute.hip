@@ -197,14 +197,14 @@ __global__ __launch_bounds__(kFewThreads) void permute_few_kernel(SortArgs a, Ro
     if (moves_scales) s.store(scales, to, zero);
   }
   if (blockIdx.x != 0) return;
-  // every lane takes every turn: lane j holds the row of choice j
-  for (uint32_t base = kFewThreads; base < scales.units; base += kFewThreads) {
-    const bool moves_more = base + tid < scales.units;
-    if (moves_more) s.load(scales, token, base + tid);
+  for (uint32_t more = tid + kFewThreads; more < scales.units; more += kFewThreads) {
+    s.load(scales, token, more);
 #pragma unroll 1
     for (uint32_t j = 0; j < a.k; ++j) {
-      const uint32_t to = __builtin_amdgcn_readlane(mine, j);
-      if (moves_more) s.store(scales, to, gone >> j & 1);
+      uint32_t to = 0;  // not read from lane j: it may have no more of them, and be out of the loop
+#pragma unroll 1
+      for (int w = 0; w < kFewWaves; ++w) to += sh_before[w][j];
+      s.store(scales, to, gone >> j & 1);
     }
   }
 }
