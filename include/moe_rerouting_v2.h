@@ -494,7 +494,8 @@ mrr_status mrr_rms_norm(const mrr_rms_norm_args* args, struct ihipStream_t* stre
  *     grad_weight = sum over the rows of grad * n
  * x is what the norm was taken of: the sum, where a residual was added; grad_x
  * is then the gradient of both x and residual. Sums are kept in 32 bits, each
- * result is rounded once. grad * weight has to lie in the range of 32 bits.
+ * result is rounded once. grad * weight is to lie between 2^-70 and 2^100 (or
+ * be 0), so that its sums with x stay in the range of 32 bits.
  */
 typedef struct mrr_rms_norm_backward_args {
   const void* grad;                /* [rows, H], dtype */

@@ -150,7 +150,7 @@ def rms_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
 
     Returns (grad_x, grad_weight) of x's and weight's dtypes: grad_x is the gradient of
     x and of the residual alike, grad_weight [H] is summed over all rows in float32. grad *
-    weight has to lie in float32's range."""
+    weight is to lie between 2^-70 and 2^100, or be 0."""
     if out is None and workspace is None:
         done = _lib.plain_calls().rms_norm_backward(grad, x, weight, grad_residual, eps)
         if done is not None:
